@@ -15,8 +15,8 @@
  * or copying between host and device (they may be captured into a graph),
  * argument checks run before any launch and have no side effects, no exception
  * crosses the ABI, and work runs on the HIP device that is current.  q, k,
- * v, o, states, logits, regions and workspaces are 16-byte aligned, arrays of
- * 32-bit values (lengths, ids, beta, gate, scores) 4-byte aligned.  Two calls that use one workspace must be
+ * v, o, states, regions and workspaces are 16-byte aligned, logits and arrays of
+ * 32-bit values (lengths, ids, beta, gate, scores) as their elements.  Two calls that use one workspace must be
  * ordered; its contents need no initialisation and mean nothing afterwards.
  */
 #ifndef STEPQ_SEQ_H
@@ -100,8 +100,7 @@ stepq_status stepq_linear_step(const stepq_linear_desc *desc, int32_t batch, con
 size_t stepq_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t num_out);
 
 /* Selection.  Beam i of request b is row r = b * beams + i of logits (dtype,
- * logits_stride elements from row to row, at least vocab and a multiple of 16
- * bytes), of scores (float, the beam's sum of log probabilities) and of
+ * logits_stride >= vocab elements from row to row), of scores (float, the beam's sum of log probabilities) and of
  * finished.  Token t continues it at score scores[r] + (x_t - max x) - log sum
  * exp(x - max x); a beam with finished[r] != 0 has one continuation, eos_token,
  * at scores[r].  The num_out best of a request, 1 .. 64, are written in order:

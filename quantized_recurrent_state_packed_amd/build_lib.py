@@ -20,7 +20,8 @@ ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wno-unused-command-line-argument", f"-I{INCLUDE}"]
-SOURCES = ["stepq_kernels.hip", "stepq_api.cpp", "linear_kernels.hip", "linear_api.cpp"]
+SOURCES = ["stepq_kernels.hip", "stepq_api.cpp", "linear_kernels.hip", "linear_api.cpp", "beam_kernels.hip",
+           "beam_api.cpp"]
 
 
 def build(verbose: bool = False) -> Path:

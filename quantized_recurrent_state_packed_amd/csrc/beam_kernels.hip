@@ -1,0 +1,276 @@
+// gfx950 kernels of beam search: selection over beams and vocabulary, and the
+// reordering of state slots.
+//
+// Selection.  A beam's candidates are ordered by logit, which orders them by
+// score too, so the best num_out of a beam need no softmax: one pass over the
+// logits keeps a running maximum and sum of exponentials, and a list of the
+// num_out largest.  A wave owns a stretch of a row (k_select_scan); its list is
+// sorted across its lanes, one entry a lane.  k_select_merge joins a request's
+// lists, turns logits into scores and orders the beams' candidates.
+#include "beam_internal.hpp"
+
+namespace stepq {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kScanWaves = 4096;      // 256 CUs x 16 waves
+constexpr int kPer = kTile / 64;      // logits a lane holds
+constexpr float kInf = __builtin_inff();
+constexpr float kLog2e = 1.4426950408889634f;
+
+// List of a wave: entry i in lane i, best first; (-inf, -1) where there is
+// none, which nothing ties with.
+struct List {
+  float x = -kInf;
+  int32_t i = -1;
+};
+
+__device__ __forceinline__ bool better(float x, int32_t i, float y, int32_t j) { return x > y || (x == y && i < j); }
+
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+// The value of the lane below (lane 0 keeps its own).
+__device__ __forceinline__ int from_below(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, 0x138, 0xf, 0xf, false);   // wave_shr:1
+}
+
+// Inserts (x, i), the same in every lane, which beats the list's last entry.
+__device__ __forceinline__ void insert(List& l, float x, int32_t i, int lane) {
+  const bool after = better(x, i, l.x, l.i);
+  const uint64_t m = __ballot(after);
+  const float bx = __builtin_bit_cast(float, from_below(__builtin_bit_cast(int, l.x)));
+  const int32_t bi = from_below(l.i);
+  const bool here = lane == __builtin_ctzll(m | (1ull << 63));
+  if (after) {
+    l.x = here ? x : bx;
+    l.i = here ? i : bi;
+  }
+}
+
+// Offers every lane's (x, i) to the list, which keeps `n` entries that matter.
+__device__ __forceinline__ void offer(List& l, float x, int32_t i, int n, int lane) {
+  uint64_t m = __ballot(better(x, i, lane_value(l.x, n - 1), __builtin_amdgcn_readlane(l.i, n - 1)));
+  while (m) {
+    const int from = __builtin_ctzll(m);
+    insert(l, lane_value(x, from), __builtin_amdgcn_readlane(i, from), lane);
+    m &= m - 1;
+    m &= __ballot(better(x, i, lane_value(l.x, n - 1), __builtin_amdgcn_readlane(l.i, n - 1)));
+  }
+}
+
+// exp(x - m) for x <= m; 1 where both are the same infinity.
+__device__ __forceinline__ float exp_below(float x, float m) {
+  return x == m ? 1.0f : __builtin_amdgcn_exp2f((x - m) * kLog2e);
+}
+
+// kVec consecutive logits from a 16-byte boundary, and a single one.
+template <typename T>
+struct Loader;
+template <>
+struct Loader<float> {
+  static constexpr int kVec = 4;
+  static __device__ __forceinline__ void load(const void* p, float (&x)[kVec]) {
+    const f32x4 a = *static_cast<const f32x4*>(p);
+    for (int i = 0; i < 4; ++i) x[i] = a[i];
+  }
+  static __device__ __forceinline__ float one(const void* p) { return *static_cast<const float*>(p); }
+};
+template <>
+struct Loader<__bf16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ void load(const void* p, float (&x)[kVec]) {
+    const u16x8 a = *static_cast<const u16x8*>(p);
+    for (int i = 0; i < 8; ++i) x[i] = __builtin_bit_cast(float, static_cast<uint32_t>(a[i]) << 16);
+  }
+  static __device__ __forceinline__ float one(const void* p) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(*static_cast<const uint16_t*>(p)) << 16);
+  }
+};
+template <>
+struct Loader<_Float16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ void load(const void* p, float (&x)[kVec]) {
+    const u16x8 a = *static_cast<const u16x8*>(p);
+    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(a[i])));
+  }
+  static __device__ __forceinline__ float one(const void* p) { return static_cast<float>(*static_cast<const _Float16*>(p)); }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
+  using L = Loader<T>;
+  constexpr int V = L::kVec;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  if (unit >= static_cast<int64_t>(p.batch) * p.beams * p.parts) return;
+  const int64_t row = unit / p.parts;
+  const int part = static_cast<int>(unit % p.parts);
+  const T* x = static_cast<const T*>(p.logits) + row * p.stride;
+  // tiles begin at the 16-byte boundary at or below the row's start
+  const int before = static_cast<int>((reinterpret_cast<uintptr_t>(x) % 16) / sizeof(T));
+  List list;
+  float m = -kInf, sum = 0.0f;
+  if (p.finished == nullptr || p.finished[row] == 0) {
+    for (int tile = part * p.tiles; tile < (part + 1) * p.tiles && static_cast<int64_t>(tile) * kTile < p.vocab + before; ++tile) {
+      const int base = tile * kTile - before;
+      float y[kPer];
+      for (int e = 0; e < kPer; e += V) {
+        const int at = base + e * 64 + lane * V;
+        float z[V];
+        if (at >= 0 && at + V <= p.vocab) {
+          L::load(x + at, z);
+        } else {
+          for (int i = 0; i < V; ++i) z[i] = at + i >= 0 && at + i < p.vocab ? L::one(x + at + i) : -kInf;
+        }
+        for (int i = 0; i < V; ++i) y[e + i] = fmaxf(z[i], -kInf);   // NaN: banned
+      }
+      float top = y[0];
+      for (int e = 1; e < kPer; ++e) top = fmaxf(top, y[e]);
+      if (top > -kInf) {
+        const float now = fmaxf(m, top);
+        sum *= exp_below(m, now);
+        for (int e = 0; e < kPer; ++e) sum += exp_below(y[e], now);
+        m = now;
+      }
+      // tiles come in ascending order, so a tie with an entry of an earlier tile is lost
+      if (__ballot(top > lane_value(list.x, p.num_out - 1)))
+        for (int e = 0; e < kPer; ++e) offer(list, y[e], base + (e / V) * V * 64 + lane * V + e % V, p.num_out, lane);
+    }
+    for (int s = 1; s < 64; s <<= 1) {
+      const float om = __shfl_xor(m, s), os = __shfl_xor(sum, s);
+      const float now = fmaxf(m, om);
+      if (now > -kInf) sum = sum * exp_below(m, now) + os * exp_below(om, now);
+      m = now;
+    }
+  }
+  float* out = reinterpret_cast<float*>(p.workspace + unit * select_part_bytes(p.num_out));
+  if (lane == 0) out[0] = m, out[1] = sum;
+  if (lane < p.num_out) {
+    out[2 + lane] = list.x;
+    reinterpret_cast<int32_t*>(out)[2 + p.num_out + lane] = list.i;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) k_select_merge(SelectArgs p) {
+  __shared__ float sx[kMaxBeams][64];
+  __shared__ int32_t si[kMaxBeams][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = p.num_out;
+  const int64_t b = blockIdx.x;
+  for (int beam = wave; beam < p.beams; beam += kWaves) {
+    const int64_t row = b * p.beams + beam;
+    const float start = p.scores[row];
+    float score = -kInf;
+    int32_t token = -1;
+    if (p.finished != nullptr && p.finished[row] != 0) {
+      if (lane == 0) score = start, token = p.eos;
+    } else {
+      List list;
+      float m = -kInf, sum = 0.0f;
+      for (int part = 0; part < p.parts; ++part) {
+        const float* in = reinterpret_cast<const float*>(p.workspace + (row * p.parts + part) * select_part_bytes(n));
+        const float om = in[0], os = in[1], now = fmaxf(m, om);
+        if (now > -kInf) sum = sum * exp_below(m, now) + os * exp_below(om, now);
+        m = now;
+        const float x = lane < n ? in[2 + lane] : -kInf;
+        const int32_t i = lane < n ? reinterpret_cast<const int32_t*>(in)[2 + n + lane] : -1;
+        offer(list, x, i, n, lane);
+      }
+      if (list.x > -kInf) {
+        score = start + ((list.x == m ? 0.0f : list.x - m) - logf(sum));
+        token = list.i;
+      }
+    }
+    sx[beam][lane] = lane < n && score > -kInf ? score : -kInf;   // a NaN score is none
+    si[beam][lane] = token;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  List best;      // by score, then by place beam * 64 + rank
+  for (int beam = 0; beam < p.beams; ++beam) offer(best, sx[beam][lane], beam * 64 + lane, n, lane);
+  if (lane < n) {
+    const bool some = best.x > -kInf;
+    p.tokens[b * n + lane] = some ? si[best.i >> 6][best.i & 63] : -1;
+    p.parents[b * n + lane] = some ? best.i >> 6 : -1;
+    p.out_scores[b * n + lane] = best.x;
+  }
+}
+
+// One workgroup per (new beam, segment of a slot).  Every wave works out the
+// request's assignment from its parents: bit j of `first` says that new beam j
+// is its parent's first child, bit i of `dead` that old beam i has none.
+__global__ void __launch_bounds__(kThreads) k_beam_reorder(ReorderArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int j = blockIdx.x % p.beams;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) - j;
+  const int32_t parent = lane < p.beams ? p.parents[base + lane] : -1;
+  const uint64_t all = p.beams == 64 ? ~0ull : (1ull << p.beams) - 1;
+  uint64_t first = 0, dead = 0;
+  for (int i = 0; i < p.beams; ++i) {
+    const uint64_t m = __ballot(parent == i);
+    if (m) first |= m & (~m + 1);
+    else dead |= 1ull << i;
+  }
+  const int32_t mine = __builtin_amdgcn_readlane(parent, j);
+  const int32_t from = mine >= 0 && mine < p.beams ? p.slot_ids[base + mine] : -1;
+  if (first >> j & 1) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) p.new_slot_ids[base + j] = from;
+    return;
+  }
+  const int rank = __popcll(all & ~first & ((1ull << j) - 1));
+  const bool pick = (dead >> lane & 1) && __popcll(dead & ((1ull << lane) - 1)) == rank;
+  const int32_t to = p.slot_ids[base + __builtin_ctzll(__ballot(pick))];
+  if (blockIdx.y == 0 && threadIdx.x == 0) p.new_slot_ids[base + j] = to;
+  if (mine < 0 || mine >= p.beams || from < 0 || from >= p.num_slots || to < 0 || to >= p.num_slots) return;
+  if (p.num_regions == 0) return;
+  int r = 0;
+  for (int lo = 1, hi = p.num_regions - 1; lo <= hi;) {
+    const int mid = (lo + hi) / 2;
+    if (p.regions[mid].first_segment <= blockIdx.y) r = mid, lo = mid + 1;
+    else hi = mid - 1;
+  }
+  const uint64_t bytes = p.regions[r].slot_bytes;
+  const uint64_t begin = static_cast<uint64_t>(blockIdx.y - p.regions[r].first_segment) * kSegment;
+  const uint64_t end = begin + kSegment < bytes ? begin + kSegment : bytes;
+  const uint8_t* src = p.regions[r].base + from * bytes;
+  uint8_t* dst = p.regions[r].base + to * bytes;
+  for (uint64_t at = begin + threadIdx.x * 16; at < end; at += kThreads * 16)
+    *reinterpret_cast<u32x4*>(dst + at) = *reinterpret_cast<const u32x4*>(src + at);
+}
+
+}  // namespace
+
+int select_parts(int64_t rows, int32_t vocab) {
+  const int64_t tiles = (static_cast<int64_t>(vocab) + kTile - 1) / kTile;
+  int64_t parts = rows > 0 ? (kScanWaves + rows - 1) / rows : 1;
+  if (parts > 64) parts = 64;
+  if (parts > tiles) parts = tiles;
+  return static_cast<int>(parts);
+}
+
+hipError_t launch_beam_select(const SelectArgs& a, int dtype, hipStream_t s) {
+  const int64_t units = static_cast<int64_t>(a.batch) * a.beams * a.parts;
+  const dim3 grid(static_cast<uint32_t>((units + kWaves - 1) / kWaves));
+  switch (dtype) {
+    case STEPQ_BF16: k_select_scan<__bf16><<<grid, kThreads, 0, s>>>(a); break;
+    case STEPQ_F16: k_select_scan<_Float16><<<grid, kThreads, 0, s>>>(a); break;
+    default: k_select_scan<float><<<grid, kThreads, 0, s>>>(a); break;
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_select_merge<<<dim3(static_cast<uint32_t>(a.batch)), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_beam_reorder(const ReorderArgs& a, int32_t batch, uint32_t segments, hipStream_t s) {
+  k_beam_reorder<<<dim3(static_cast<uint32_t>(batch * a.beams), segments), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace stepq
