@@ -63,8 +63,8 @@ size_t stepq_linear_workspace_bytes(const stepq_linear_desc *desc, int32_t batch
  * [0, total_tokens]; entries outside are clamped).  Any length is allowed,
  * 0 and 1 among them: an empty request leaves the state it starts from.
  *   q, k: [total_tokens][Hk][D], v, o: [total_tokens][H][D] of desc->dtype;
- *         *_stride is the distance of two tokens in elements (>= heads * D and a
- *         multiple of 16 bytes), so slices of one fused projection need no copy.
+ *         *_stride is the distance of two tokens in elements (>= heads * D, at most
+ *         2^24, a multiple of 16 bytes), so slices of one fused projection need no copy.
  *         q and k are used as given.  o must not overlap an input.
  *   beta: float [total_tokens][H], NULL for the additive rule.
  *   gate: float [total_tokens][H], linear retention a in [0, 1]; 0 clears the

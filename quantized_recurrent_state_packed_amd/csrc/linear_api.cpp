@@ -34,7 +34,8 @@ stepq_status check_tensors(const stepq_linear_desc& d, const void* q, int64_t qs
   const int64_t qk = static_cast<int64_t>(d.num_qk_heads) * d.d, vo = static_cast<int64_t>(d.num_heads) * d.d;
   if (!stride_ok(qs, qk, e) || !stride_ok(ks, qk, e) || !stride_ok(vs, vo, e) || !stride_ok(os, vo, e))
     return STEPQ_ERR_INVALID_ARG;
-  return STEPQ_OK;
+  const int64_t most = 1 << 24;     // a chunk's 64 rows are addressed in 32 bits
+  return qs <= most && ks <= most && vs <= most && os <= most ? STEPQ_OK : STEPQ_ERR_UNSUPPORTED;
 }
 
 stepq_status from_hip(hipError_t e) { return e == hipSuccess ? STEPQ_OK : STEPQ_ERR_HIP; }

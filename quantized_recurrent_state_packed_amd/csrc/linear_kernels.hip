@@ -331,6 +331,644 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
     for (int e = 0; e < 4; ++e) state[(16 * i + 4 * g + e) * D] = m[i][e];
 }
 
+// ------------------------------------------------ 16-bit inputs: bfloat16 parts
+//
+// Matrix products of 16-bit inputs run on bfloat16 matrix instructions, which
+// multiply exactly and add in binary32, sixteen times as fast as the binary32
+// ones.  A bfloat16 q, k or v is its own operand; a binary16 q or k is the sum of
+// two bfloat16 parts exactly (11 bits in 8 + 8).  Computed operands (state, T, R,
+// U) are split into a part of 8 bits and a rest of 8, 2^-17 of the value at
+// worst, wherever they lead into the state, which lives long; products take the
+// terms above 2^-16.  What only leads into a bfloat16 o (the state under q, A, U
+// under A) is one part: a single rounding of each, not larger than o's own.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Keeps the compiler from moving loads across: registers are what bounds it.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// x, in a register whose value the compiler does not know: addresses derived from
+// it are computed where they are used instead of being kept through the loop over
+// chunks (some 80 registers of them).
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// LDS accesses of one wave's lanes to each other's words: ordered in hardware, this
+// keeps the compiler to it.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int NP>
+struct Parts {
+  bf16x8 p[NP];
+};
+
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ bf16x4 rounded(const f32x4& x) { return __builtin_convertvector(x, bf16x4); }
+__device__ __forceinline__ f32x4 widened(const bf16x4& x) { return __builtin_convertvector(x, f32x4); }
+
+template <int NP>
+__device__ __forceinline__ Parts<NP> parts_of(const f32x4& a, const f32x4& b) {
+  Parts<NP> r;
+  const bf16x4 ah = rounded(a), bh = rounded(b);
+  r.p[0] = join(ah, bh);
+  if constexpr (NP == 2) r.p[1] = join(rounded(a - widened(ah)), rounded(b - widened(bh)));
+  return r;
+}
+
+// Product of operands in NA and NB parts.  FULL: with the product of two rests
+// (q . k and k . k, whose parts are exact and whose sums may all but cancel).
+template <bool FULL = false, int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Parts<NA>& a, const Parts<NB>& b, f32x4 c) {
+  for (int i = NA - 1; i >= 0; --i)
+    for (int j = NB - 1; j >= 0; --j)
+      if (FULL || i + j < 2) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
+  return c;
+}
+
+template <int D, typename T>
+struct Dims16 {
+  static constexpr int NP = sizeof(T) == 2 && __is_same(T, bf16) ? 1 : 2;   // parts of q and k
+  static constexpr int DP = D < 32 ? 32 : D;
+  static constexpr int RB = 2 * DP;              // bytes of a row in LDS
+  static constexpr int CPR = RB / 16;            // 16-byte units of a row
+  static constexpr int KB = DP / 32;
+  static constexpr int RT = D / 16;
+  static constexpr int MAT = C * RB;             // bytes of one part of q, k or v
+};
+
+// A row's 16-byte units are permuted within it (exclusive or with a number that
+// depends on the row), so that the 16 rows an operand takes from a column of
+// units, and the four 8-byte pieces a transposing read takes from each of 16
+// rows, fall on different banks.
+template <int RB>
+__device__ __forceinline__ int unit_at(int row, int unit) {
+  return row * RB + ((unit ^ ((row / (256 / RB)) & (RB / 16 - 1))) << 4);
+}
+
+// An operand (i, tb) of a lower triangle, i = 0 .. 3, tb <= i / 2, is 16 x 32: 16
+// bytes a lane, 1024 in all, in the order lanes hold it.
+constexpr int kTri = 6 * 1024;
+
+// Where a lane reads the operands of a matrix in LDS: `row` for row_operand and
+// `col` for column_piece with i = kb = t = 0.  Others differ by whole 16 rows and
+// in the bits of the unit, which commute with the permutation.
+struct At {
+  int row, col;
+};
+template <int RB>
+__device__ __forceinline__ At lane_at(int lane) {
+  const int g = lane >> 4, c = lane & 15;
+  return {unit_at<RB>(c, g >> 1) + (g & 1) * 8, unit_at<RB>(4 * g + (c >> 2), (c & 3) >> 1) + (c & 1) * 8};
+}
+// Operand whose row lane % 16 is row 16 i + lane % 16 of x, depth 32 kb ..
+template <int RB>
+__device__ __forceinline__ bf16x8 row_operand(const uint8_t* x, int i, int kb, At at) {
+  x += 16 * i * RB;
+  return join(*reinterpret_cast<const bf16x4*>(x + (at.row ^ (4 * kb) << 4)),
+              *reinterpret_cast<const bf16x4*>(x + (at.row ^ (4 * kb + 2) << 4)));
+}
+// Rows 16 i + 4 g .. + 3 (g = lane / 16) of column 16 t + lane % 16 of x.
+template <int RB>
+__device__ __forceinline__ s16x4 column_piece(const uint8_t* x, int i, int t, At at) {
+  x += 16 * i * RB;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(const_cast<uint8_t*>(x + (at.col ^ (2 * t) << 4))));
+}
+// Operand whose row lane % 16 is column 16 t + lane % 16 of x, depth rows 32 tb ..
+template <int RB>
+__device__ __forceinline__ bf16x8 column_operand(const uint8_t* x, int tb, int t, At at) {
+  return join(__builtin_bit_cast(bf16x4, column_piece<RB>(x, 2 * tb, t, at)),
+              __builtin_bit_cast(bf16x4, column_piece<RB>(x, 2 * tb + 1, t, at)));
+}
+__device__ __forceinline__ bf16x8 stored_operand(const uint8_t* x, int n, int lane) {
+  return *reinterpret_cast<const bf16x8*>(x + n * 1024 + lane * 16);
+}
+// Index of operand (i, tb) of a lower triangle.
+__device__ constexpr int tri(int i, int tb) { return i < 2 ? i : 2 * (i - 1) + tb; }
+
+// Half `half` of operand n of a triangle, in two parts.
+__device__ __forceinline__ void store_parts(uint8_t* hi, uint8_t* lo, int n, int half, const f32x4& x, int lane) {
+  const int at = n * 1024 + lane * 16 + half * 8;
+  const bf16x4 h = rounded(x);
+  *reinterpret_cast<bf16x4*>(hi + at) = h;
+  *reinterpret_cast<bf16x4*>(lo + at) = rounded(x - widened(h));
+}
+// Operand n of a triangle.
+__device__ __forceinline__ Parts<2> stored_parts(const uint8_t* hi, const uint8_t* lo, int n, int lane) {
+  return {{stored_operand(hi, n, lane), stored_operand(lo, n, lane)}};
+}
+
+__device__ __forceinline__ f32x4 floats_of(const s16x4& x, bf16) {
+  return widened(__builtin_bit_cast(bf16x4, x));
+}
+__device__ __forceinline__ f32x4 floats_of(const s16x4& x, f16) {
+  typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_convertvector(__builtin_bit_cast(f16x4, x), f32x4);
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Units u0 .. u0 + N - 1 of the rows of a chunk of x (q, k or v of a head), on the
+// way from memory to LDS in the registers of THREADS threads: all loads are under
+// way before the first is waited for.  A thread has a unit of every THREADS / N'th
+// row, so one 32-bit offset serves all of them (strides are below 2^24 elements).
+// Past `count` tokens and past D channels the last valid ones are read, and zeros
+// are stored.
+template <int D, typename T, int N, int THREADS>
+struct Rows {
+  using S = Dims16<D, T>;
+  static constexpr int L = C * N / THREADS;
+  static constexpr int STEP = THREADS / N;       // a power of two, as N is
+  u32x4 raw[L];
+  __device__ __forceinline__ void load(const T* x, int64_t stride, int count, int u0, int tid) {
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(x);
+    const int unit = min(u0 + tid % N, D / 8 - 1);
+    const uint32_t s = static_cast<uint32_t>(stride) * 2;
+    if (count == C) {
+      const uint32_t off = tid / N * s + unit * 16;
+      for (int j = 0; j < L; ++j) raw[j] = *reinterpret_cast<const u32x4*>(base + static_cast<uint64_t>(s) * (j * STEP) + off);
+    } else {
+      for (int j = 0; j < L; ++j)
+        raw[j] = *reinterpret_cast<const u32x4*>(base + (min(tid / N + j * STEP, count - 1) * s + unit * 16));
+    }
+  }
+  // SPLIT: in two bfloat16 parts, the second S::MAT bytes after the first.
+  template <bool SPLIT>
+  __device__ __forceinline__ void store(uint8_t* lds, int count, int u0, int tid) {
+    if (count < C || S::CPR * 8 > D)
+      for (int j = 0; j < L; ++j)
+        if (tid / N + j * STEP >= count || u0 + tid % N >= D / 8) raw[j] = u32x4{};
+    const int to0 = unit_at<S::RB>(tid / N, u0 + tid % N);
+    for (int j = 0; j < L; ++j) {
+      // tid / N < STEP, so the row's number in the permutation is that of its two parts, joined
+      uint8_t* to = lds + j * STEP * S::RB + (to0 ^ ((j * STEP / (256 / S::RB)) & (S::CPR - 1)) << 4);
+      if constexpr (SPLIT) {
+        typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+        typedef float f32x8 __attribute__((ext_vector_type(8)));
+        const f32x8 y = __builtin_convertvector(__builtin_bit_cast(f16x8, raw[j]), f32x8);
+        const bf16x8 hi = __builtin_convertvector(y, bf16x8);
+        *reinterpret_cast<bf16x8*>(to) = hi;
+        *reinterpret_cast<bf16x8*>(to + S::MAT) = __builtin_convertvector(y - __builtin_convertvector(hi, f32x8), bf16x8);
+      } else {
+        *reinterpret_cast<u32x4*>(to) = raw[j];
+      }
+    }
+  }
+};
+
+// What a chunk's retentions and betas come to, in LDS.
+struct Rates {
+  double lg[C];      // log2 G
+  float grow[C];     // G_t
+  float left[C];     // G_C / G_t
+  float beta[C];
+};
+
+// One wave: the chunk's log2 G as a running sum in binary64, so that ratios of
+// retentions far into a fast-forgetting chunk keep binary32 accuracy.  A
+// retention of 0 (or below 2^-200) counts as 2^-200, which leaves nothing in
+// binary32.  Past `count` tokens: retention 1, beta 0.
+__device__ __forceinline__ void set_rates(Rates& r, float gate, float beta, int count, int lane) {
+  double x = 0.0;
+  if (lane < count) {
+    const float y = __builtin_amdgcn_logf(gate);
+    x = y < -200.0f ? -200.0 : static_cast<double>(y);
+  }
+  for (int s = 1; s < 64; s <<= 1) {
+    const double y = __shfl_up(x, s);
+    if (lane >= s) x += y;
+  }
+  const double all = __shfl(x, 63);
+  r.lg[lane] = x;
+  r.grow[lane] = __builtin_amdgcn_exp2f(static_cast<float>(x));
+  r.left[lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - x));
+  r.beta[lane] = lane < count ? beta : 0.0f;
+}
+
+// Scratch of the chunk matrices: the blocks of B below the diagonal as operands
+// (lane: row lane % 16 of the transposed block, depth 4 g + e), and the diagonal
+// blocks, later their inverses, in rows of 20.
+struct Scratch {
+  f32x4 off[6][64];
+  float diag[4][16 * 20];
+};
+__device__ constexpr int pair(int k, int j) { return k * (k - 1) / 2 + j; }
+
+// The ten blocks (i, j), j <= i < 4, of a chunk's lower triangles, dealt out to four
+// waves; a wave's first is the diagonal one of its number.
+constexpr int kTiles = 3;
+__device__ __forceinline__ int tile_of(int wave, int n) {      // 4 i + j, or -1
+  switch (n) {
+    case 0: return 5 * wave;                                              // (w, w)
+    case 1: return wave == 0 ? 12 : wave == 1 ? 4 : wave == 2 ? 9 : 14;   // (3,0) (1,0) (2,1) (3,2)
+    default: return wave == 0 ? 8 : wave == 1 ? 13 : -1;                  // (2,0) (3,1)
+  }
+}
+
+// A block's A values on their way to LDS.
+struct ATile {
+  bf16x4 hi, lo;
+};
+
+// First part, wave `wave` of four: its blocks of B into the scratch, its blocks of
+// A into registers, and the inverse of its diagonal block of I + B by forward
+// substitution (a column for every lane of 16, the other lanes doing the same).
+template <int D, typename T, bool DELTA>
+__device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq, const Rates& r, Scratch* sc,
+                                            ATile (&tiles)[kTiles], int wave, int lane) {
+  using S = Dims16<D, T>;
+  const At at = lane_at<S::RB>(lane);
+  const int g = lane >> 4, c = lane & 15;
+  for (int n = 0; n < kTiles; ++n) {
+    const int tile = tile_of(wave, n);
+    if (tile < 0) break;
+    const int i = tile >> 2, j = tile & 3;
+    f32x4 kk = {}, qk = {};
+    for (int kb = 0; kb < S::KB; ++kb) {
+      Parts<S::NP> ki, qi, kj;
+      for (int x = 0; x < S::NP; ++x) {
+        kj.p[x] = row_operand<S::RB>(lk + x * S::MAT, j, kb, at);
+        qi.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
+        if constexpr (DELTA) ki.p[x] = n == 0 ? kj.p[x] : row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
+      }
+      qk = mma<true>(kj, qi, qk);                            // rows: key token 16 j + 4 g + e, column: query token 16 i + c
+      if constexpr (DELTA) kk = mma<true>(ki, kj, kk);       // rows: token 16 i + 4 g + e, column: token 16 j + c
+    }
+    const double lq_i = r.lg[16 * i + c];
+    for (int e = 0; e < 4; ++e) {
+      const int t = 16 * j + 4 * g + e;
+      const float ratio = __builtin_amdgcn_exp2f(static_cast<float>(lq_i - r.lg[t]));
+      qk[e] = n > 0 || 4 * g + e <= c ? qk[e] * ratio : 0.0f;
+    }
+    tiles[n].hi = rounded(qk);
+    tiles[n].lo = rounded(qk - widened(tiles[n].hi));
+    if constexpr (DELTA) {
+      const double lk_j = r.lg[16 * j + c];
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * i + 4 * g + e;
+        kk[e] *= r.beta[t] * __builtin_amdgcn_exp2f(static_cast<float>(r.lg[t] - lk_j));
+      }
+      if (n > 0) {
+        sc->off[pair(i, j)][lane] = kk;
+      } else {
+        // only what lies below the diagonal is read; a wave's own LDS accesses are in order
+        float* d = sc->diag[wave];
+        for (int e = 0; e < 4; ++e) d[(4 * g + e) * 20 + c] = kk[e];
+        wave_order();
+        float x[16];
+        for (int q = 0; q < 4; ++q) {
+          f32x4 row[4][4];
+          for (int ii = 0; ii < 4; ++ii)
+            for (int b = 0; b <= q; ++b) row[ii][b] = *reinterpret_cast<const f32x4*>(d + (4 * q + ii) * 20 + 4 * b);
+          for (int ii = 0; ii < 4; ++ii) {
+            float s = 4 * q + ii == c ? 1.0f : 0.0f;
+            for (int jj = 0; jj < 4 * q + ii; ++jj) s = fmaf(-row[ii][jj >> 2][jj & 3], x[jj], s);
+            x[4 * q + ii] = s;
+          }
+          in_order();
+        }
+        wave_order();
+        if (g == 0)
+          for (int ii = 0; ii < 16; ++ii) d[ii * 20 + c] = x[ii];
+      }
+    }
+    in_order();
+  }
+}
+
+// Writes one part of a wave's blocks of A, and the zeros beside its diagonal block.
+__device__ __forceinline__ void store_tiles(uint8_t* to, const ATile (&tiles)[kTiles], bool rest, int wave, int lane) {
+  for (int n = 0; n < kTiles; ++n) {
+    const int tile = tile_of(wave, n);
+    if (tile < 0) break;
+    const int i = tile >> 2, j = tile & 3;
+    *reinterpret_cast<bf16x4*>(to + tri(i, j >> 1) * 1024 + lane * 16 + (j & 1) * 8) = rest ? tiles[n].lo : tiles[n].hi;
+  }
+  if ((wave & 1) == 0) *reinterpret_cast<bf16x4*>(to + tri(wave, wave >> 1) * 1024 + lane * 16 + 8) = bf16x4{};
+}
+
+// Second part, wave i: block row i of T = (I + B)^-1 diag(beta), transposed, from
+// the diagonal leftwards: X_ij = -(sum_{k > j} X_ik B_kj) (I + B_jj)^-1.  Like the
+// substitution it is as stable as solving for U token by token.
+__device__ __forceinline__ void invert_row(const Scratch* sc, const Rates& r, uint8_t* lt, int i, int lane) {
+  const int g = lane >> 4, c = lane & 15;
+  f32x4 x[4] = {};
+  for (int j = 3; j >= 0; --j) {
+    if (j > i) continue;
+    if (j == i) {
+      x[j] = *reinterpret_cast<const f32x4*>(&sc->diag[j][c * 20 + 4 * g]);
+      continue;
+    }
+    f32x4 d, s = {};
+    for (int e = 0; e < 4; ++e) d[e] = -sc->diag[j][(4 * g + e) * 20 + c];
+    for (int k = j + 1; k < 4; ++k)
+      if (k <= i) s = mma16(sc->off[pair(k, j)][lane], x[k], s);
+    x[j] = mma16(d, s, f32x4{});
+  }
+  for (int j = 0; j < 4; ++j) {
+    if (j > (i | 1)) break;
+    const f32x4 s = x[j] * *reinterpret_cast<const f32x4*>(&r.beta[16 * j + 4 * g]);
+    store_parts(lt, lt + kTri, tri(i, j >> 1), j & 1, s, lane);
+  }
+}
+
+// A (chunk, head) of the workspace of 16-bit inputs: G, G_C / G, A, T.
+__device__ __forceinline__ uint8_t* chunk_ws16(uint8_t* ws, int64_t index, bool delta) {
+  return ws + index * (2 * C * 4 + 2 * kTri + (delta ? 2 * kTri : 0));
+}
+
+template <int D, typename T>
+struct Lds16 {
+  using S = Dims16<D, T>;
+  static constexpr int K = 0;
+  static constexpr int Q = K + S::NP * S::MAT;
+  static constexpr int V = Q + S::NP * S::MAT;
+  static constexpr int A = V + S::MAT;                                 // the larger part of A
+  static constexpr int RATES = A + kTri;
+  static constexpr int TT = RATES + 2 * static_cast<int>(sizeof(Rates));   // this chunk's and the next one's; T (delta)
+  // the smaller part of A takes the place of the blocks of B, which are done with by then
+  static constexpr int rest(bool delta) { return delta ? TT + 2 * kTri : TT; }
+  static constexpr int fused(bool delta) { return rest(delta) + (delta ? static_cast<int>(sizeof(Scratch)) : kTri); }
+  static constexpr int split(bool delta) { return rest(delta) + kTri; }
+};
+
+// The chunk matrices of every (chunk, head), for k_linear16_walk<.., false>.
+template <int D, typename T, bool DELTA>
+__global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
+  using S = Dims16<D, T>;
+  using L = Lds16<D, T>;
+  extern __shared__ __align__(16) uint8_t lds16[];
+  Rates& rates = *reinterpret_cast<Rates*>(lds16 + L::RATES);
+  uint8_t* lr = lds16 + L::rest(DELTA);
+  Scratch* sc = reinterpret_cast<Scratch*>(lr);
+  const int h = blockIdx.x % p.H;
+  const int64_t w = blockIdx.x / p.H;
+  int b = 0;     // the last request with cu[b] / C + b <= w
+  for (int lo = 0, hi = p.batch - 1; lo <= hi;) {
+    const int mid = (lo + hi) / 2;
+    if (request_span(p, mid).first / C + mid <= w) b = mid, lo = mid + 1;
+    else hi = mid - 1;
+  }
+  const Span r = request_span(p, b);
+  const int64_t c = w - (r.first / C + b);
+  if (c < 0 || c * C >= r.count) return;
+  const int64_t first = r.first + c * C;
+  const int count = min(C, static_cast<int>(r.count - c * C));
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const T* k = static_cast<const T*>(p.k) + first * p.k_stride + (h / p.rep) * D;
+  const T* q = static_cast<const T*>(p.q) + first * p.q_stride + (h / p.rep) * D;
+  Rows<D, T, S::CPR, kThreads> kr, qr;
+  kr.load(k, p.k_stride, count, 0, tid);
+  qr.load(q, p.q_stride, count, 0, tid);
+  if (wave == 0) {
+    const int64_t at = (first + min(lane, count - 1)) * p.H + h;
+    set_rates(rates, p.gate[at], DELTA ? p.beta[at] : 0.0f, count, lane);
+  }
+  kr.template store<S::NP == 2>(lds16 + L::K, count, 0, tid);
+  qr.template store<S::NP == 2>(lds16 + L::Q, count, 0, tid);
+  __syncthreads();
+  ATile tiles[kTiles];
+  chunk_tiles<D, T, DELTA>(lds16 + L::K, lds16 + L::Q, rates, sc, tiles, wave, lane);
+  store_tiles(lds16 + L::A, tiles, false, wave, lane);
+  if constexpr (DELTA) {
+    __syncthreads();
+    invert_row(sc, rates, lds16 + L::TT, wave, lane);
+    __syncthreads();
+  }
+  store_tiles(lr, tiles, true, wave, lane);
+  __syncthreads();
+  uint8_t* ws = chunk_ws16(p.workspace, w * p.H + h, DELTA);
+  if (tid < 2 * C) reinterpret_cast<float*>(ws)[tid] = (tid < C ? rates.grow : rates.left)[tid % C];
+  ws += 2 * C * 4;
+  for (int i = tid * 16; i < kTri; i += kThreads * 16) {
+    *reinterpret_cast<u32x4*>(ws + i) = *reinterpret_cast<const u32x4*>(lds16 + L::A + i);
+    *reinterpret_cast<u32x4*>(ws + kTri + i) = *reinterpret_cast<const u32x4*>(lr + i);
+  }
+  if constexpr (DELTA)
+    for (int i = tid * 16; i < 2 * kTri; i += kThreads * 16)
+      *reinterpret_cast<u32x4*>(ws + 2 * kTri + i) = *reinterpret_cast<const u32x4*>(lds16 + L::TT + i);
+}
+
+// Walks a request's chunks in order for 16 NCT NW value columns of one head.
+// FUSED: all columns of the head in one workgroup, which computes the chunk
+// matrices itself; otherwise they come from k_linear16_chunks.
+template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED>
+__global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) k_linear16_walk(LinearArgs p) {
+  using S = Dims16<D, T>;
+  using L = Lds16<D, T>;
+  constexpr int NP = S::NP;
+  constexpr int COLS = 16 * NCT * NW;
+  constexpr int SPLIT = D / COLS;
+  extern __shared__ __align__(16) uint8_t lds16[];
+  uint8_t* lk = lds16 + L::K;
+  uint8_t* lq = lds16 + L::Q;
+  uint8_t* lv = lds16 + L::V;
+  uint8_t* la = lds16 + L::A;
+  uint8_t* lt = lds16 + L::TT;
+  Rates* all_rates = reinterpret_cast<Rates*>(lds16 + L::RATES);
+  uint8_t* lr = lds16 + L::rest(DELTA);
+  Scratch* sc = reinterpret_cast<Scratch*>(lr);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int part = blockIdx.x % SPLIT;
+  const int h = (blockIdx.x / SPLIT) % p.H;
+  const int b = blockIdx.x / (SPLIT * p.H);
+  const int ct0 = part * (COLS / 16) + wave * NCT;      // first column tile of the wave
+  const Span r = request_span(p, b);
+  const int slot = p.slot_ids[b];
+  T* o = static_cast<T*>(p.o) + r.first * p.o_stride + h * D;
+  if (slot < 0 || slot >= p.num_slots) {
+    for (int t = tid / COLS; t < r.count; t += 64 * NW / COLS > 0 ? 64 * NW / COLS : 1)
+      for (int j = tid % COLS; j < COLS; j += 64 * NW) o[t * p.o_stride + part * COLS + j] = static_cast<T>(__builtin_nanf(""));
+    return;
+  }
+  const T* v = static_cast<const T*>(p.v) + r.first * p.v_stride + h * D;
+  const T* k = static_cast<const T*>(p.k) + r.first * p.k_stride + (h / p.rep) * D;
+  const T* q = static_cast<const T*>(p.q) + r.first * p.q_stride + (h / p.rep) * D;
+  float* state = p.state + (static_cast<int64_t>(slot) * p.H + h) * D * D + 16 * ct0;
+
+  f32x4 m[NCT][S::RT] = {};    // column 16 (ct0 + n) + lane % 16; tile i holds key channels 16 i + 4 (lane / 16) + e
+  if (p.resume != nullptr && p.resume[b] != 0) {
+    const int l = fresh(lane), at = (l >> 4) * 4 * D + (l & 15);
+    for (int n = 0; n < NCT; ++n)
+      for (int i = 0; i < S::RT; ++i)
+        for (int e = 0; e < 4; ++e) m[n][i][e] = state[at + (16 * i + e) * D + 16 * n];
+  }
+
+  const int64_t base = r.first / C + b;
+  constexpr int VU = COLS / 8;      // units of the workgroup's columns
+  Rows<D, T, S::CPR, 64 * NW> kr, qr;
+  Rows<D, T, VU, 64 * NW> vr;
+  float gate = 0.0f, beta = 0.0f;
+  // the next chunk's rows are on their way while this one is computed
+  auto fetch = [&](int c) {
+    const int count = min(C, r.count - c * C);
+    const int64_t t0 = static_cast<int64_t>(c) * C;
+    const int t = fresh(tid);
+    kr.load(k + t0 * p.k_stride, p.k_stride, count, 0, t);
+    qr.load(q + t0 * p.q_stride, p.q_stride, count, 0, t);
+    vr.load(v + t0 * p.v_stride, p.v_stride, count, part * VU, t);
+  };
+  // the last wave, which has the fewest blocks, sets the next chunk's rates
+  auto fetch_rates = [&](int c) {
+    const int count = min(C, r.count - c * C);
+    const int64_t token = (r.first + static_cast<int64_t>(c) * C + min(lane, count - 1)) * p.H + h;
+    gate = p.gate[token];
+    if constexpr (DELTA) beta = p.beta[token];
+  };
+  if (r.count > 0) {
+    fetch(0);
+    if (FUSED && wave == NW - 1) {
+      fetch_rates(0);
+      set_rates(all_rates[0], gate, beta, min(C, r.count), lane);
+    }
+  }
+  for (int c = 0; c * C < r.count; ++c) {
+    const int count = min(C, r.count - c * C);
+    const int64_t t0 = static_cast<int64_t>(c) * C;
+    const bool more = t0 + C < r.count;
+    Rates& rates = all_rates[FUSED ? c & 1 : 0];
+    __syncthreads();
+    {
+      const int t = fresh(tid);
+      kr.template store<NP == 2>(lk, count, 0, t);
+      qr.template store<NP == 2>(lq, count, 0, t);
+      vr.template store<false>(lv, count, part * VU, t);
+    }
+    ATile tiles[kTiles];
+    if constexpr (FUSED) {
+      const bool next = more && wave == NW - 1;
+      if (next) fetch_rates(c + 1);
+      __syncthreads();
+      chunk_tiles<D, T, DELTA>(lk, lq, rates, sc, tiles, wave, fresh(lane));
+      store_tiles(la, tiles, false, wave, fresh(lane));
+      if constexpr (!DELTA) store_tiles(lr, tiles, true, wave, fresh(lane));
+      if (next) set_rates(all_rates[(c + 1) & 1], gate, beta, min(C, r.count - (c + 1) * C), lane);
+    } else {
+      const uint8_t* ws = chunk_ws16(p.workspace, (base + c) * p.H + h, DELTA);
+      for (int i = tid; i < C; i += 64 * NW) {
+        rates.grow[i] = reinterpret_cast<const float*>(ws)[i];
+        rates.left[i] = reinterpret_cast<const float*>(ws)[C + i];
+      }
+      ws += 2 * C * 4;
+      for (int i = tid * 16; i < kTri; i += 64 * NW * 16) {
+        *reinterpret_cast<u32x4*>(la + i) = *reinterpret_cast<const u32x4*>(ws + i);
+        *reinterpret_cast<u32x4*>(lr + i) = *reinterpret_cast<const u32x4*>(ws + kTri + i);
+      }
+      if constexpr (DELTA)
+        for (int i = tid * 16; i < 2 * kTri; i += 64 * NW * 16)
+          *reinterpret_cast<u32x4*>(lt + i) = *reinterpret_cast<const u32x4*>(ws + 2 * kTri + i);
+      __syncthreads();
+    }
+
+    // K M and (transposed: rows value columns, columns tokens, so that a lane stores
+    // 4 neighbours) Q M, the state split into its parts once for both
+    f32x4 u[NCT][4] = {}, y[NCT][4] = {};
+    {
+    const At at = lane_at<S::RB>(fresh(lane));
+    for (int kb = 0; kb < S::KB; ++kb) {
+      Parts<2> mf[NCT];
+      for (int n = 0; n < NCT; ++n) {
+        const f32x4 zero = {};
+        mf[n] = parts_of<2>(m[n][2 * kb], D < 32 ? zero : m[n][D < 32 ? 0 : 2 * kb + 1]);
+      }
+      for (int i = 0; i < 4; ++i) {
+        Parts<NP> a;
+        if constexpr (DELTA) {
+          for (int x = 0; x < NP; ++x) a.p[x] = row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
+          for (int n = 0; n < NCT; ++n) u[n][i] = mma(a, mf[n], u[n][i]);
+        }
+        for (int x = 0; x < NP; ++x) a.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
+        for (int n = 0; n < NCT; ++n) y[n][i] = mma(mf[n], a, y[n][i]);
+      }
+      in_order();
+    }
+    }
+    if constexpr (FUSED && DELTA) {
+      __syncthreads();
+      invert_row(sc, rates, lt, wave, fresh(lane));
+      __syncthreads();
+      store_tiles(lr, tiles, true, wave, fresh(lane));
+    }
+    {
+    const int l = fresh(lane), g = l >> 4;
+    const At at = lane_at<S::RB>(l);
+    for (int n = 0; n < NCT; ++n)
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 x = floats_of(column_piece<S::RB>(lv, i, ct0 + n, at), T{});
+        u[n][i] = DELTA ? x - *reinterpret_cast<const f32x4*>(&rates.grow[16 * i + 4 * g]) * u[n][i] : x;
+      }
+    if constexpr (DELTA) {
+      Parts<2> rf[NCT][2];
+      for (int n = 0; n < NCT; ++n)
+        for (int tb = 0; tb < 2; ++tb) rf[n][tb] = parts_of<2>(u[n][2 * tb], u[n][2 * tb + 1]);
+      for (int i = 0; i < 4; ++i) {
+        f32x4 s[NCT] = {};
+        for (int tb = 0; tb <= i / 2; ++tb) {
+          const Parts<2> a = stored_parts(lt, lt + kTri, tri(i, tb), l);
+          for (int n = 0; n < NCT; ++n) s[n] = mma(a, rf[n][tb], s[n]);
+        }
+        for (int n = 0; n < NCT; ++n) u[n][i] = s[n];
+      }
+      in_order();
+    }
+    }
+    if constexpr (FUSED) __syncthreads();     // A
+    {
+      const int l = fresh(lane), g = l >> 4, cl = l & 15;
+      Parts<2> uf[NCT][2];
+      for (int n = 0; n < NCT; ++n)
+        for (int tb = 0; tb < 2; ++tb) uf[n][tb] = parts_of<2>(u[n][2 * tb], u[n][2 * tb + 1]);
+      for (int i = 0; i < 4; ++i) {
+        const float grow = rates.grow[16 * i + cl];
+        for (int n = 0; n < NCT; ++n) y[n][i] *= grow;
+        for (int tb = 0; tb <= i / 2; ++tb) {
+          const Parts<2> a = stored_parts(la, lr, tri(i, tb), l);
+          for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
+        }
+        const int t = 16 * i + cl;
+        if (t < count)
+          for (int n = 0; n < NCT; ++n) {
+            typedef T t16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<t16x4*>(o + (t0 + t) * p.o_stride + 16 * (ct0 + n) + 4 * g) =
+                __builtin_convertvector(y[n][i], t16x4);
+          }
+      }
+    }
+    in_order();
+    if (more) fetch(c + 1);
+    const int l = fresh(lane), g = l >> 4;
+    const At at = lane_at<S::RB>(l);
+    Parts<2> wf[NCT][2];
+    const float all = rates.grow[C - 1];
+    for (int n = 0; n < NCT; ++n)
+      for (int tb = 0; tb < 2; ++tb)
+        wf[n][tb] = parts_of<2>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&rates.left[32 * tb + 4 * g]),
+                                u[n][2 * tb + 1] * *reinterpret_cast<const f32x4*>(&rates.left[32 * tb + 16 + 4 * g]));
+    for (int i = 0; i < S::RT; ++i) {
+      for (int n = 0; n < NCT; ++n) m[n][i] *= all;
+      for (int tb = 0; tb < 2; ++tb) {
+        Parts<NP> a;
+        for (int x = 0; x < NP; ++x) a.p[x] = column_operand<S::RB>(lk + x * S::MAT, tb, i, at);
+        for (int n = 0; n < NCT; ++n) m[n][i] = mma(a, wf[n][tb], m[n][i]);
+      }
+      if (i % 2) in_order();
+    }
+  }
+  const int l = fresh(lane), at = (l >> 4) * 4 * D + (l & 15);
+  for (int n = 0; n < NCT; ++n)
+    for (int i = 0; i < S::RT; ++i)
+      for (int e = 0; e < 4; ++e) state[at + (16 * i + e) * D + 16 * n] = m[n][i][e];
+}
+
 // One token: a workgroup owns CW columns of one (request, head) state; a lane
 // holds 4 columns of D / RG rows in registers.  With the decayed state M~,
 // u = M~^T k and w = M~^T q (one reduction for both) the new state's readout is
@@ -419,6 +1057,30 @@ hipError_t prefill_dt(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename K>
+hipError_t launch_lds(K* kern, int64_t grid, int threads, int lds, const LinearArgs& a, hipStream_t s) {
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  kern<<<dim3(static_cast<uint32_t>(grid)), threads, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int D, typename T, bool DELTA>
+hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
+  using L = Lds16<D, T>;
+  const int64_t tiles = static_cast<int64_t>(a.batch) * a.H;
+  if constexpr (D >= 64) {
+    if (tiles >= 256)
+      return launch_lds(k_linear16_walk<D, T, DELTA, D / 64, 4, true>, tiles, 256, L::fused(DELTA), a, s);
+  }
+  const int64_t chunks = max_chunks(a.total_tokens, a.batch);
+  const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, chunks * a.H, kThreads, L::fused(DELTA), a, s);
+  if (e != hipSuccess) return e;
+  constexpr int NW = D >= 64 ? 2 : 1;
+  return launch_lds(k_linear16_walk<D, T, DELTA, 1, NW, false>, tiles * (D / (16 * NW)), 64 * NW, L::split(DELTA), a, s);
+}
+
 template <int D, typename T>
 hipError_t step_dt(const LinearArgs& a, hipStream_t s) {
   constexpr int CW = D;
@@ -428,13 +1090,18 @@ hipError_t step_dt(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int D, typename T>
+hipError_t prefill_any(const LinearArgs& a, hipStream_t s) {
+  if constexpr (sizeof(T) == 4) return prefill_dt<D, T>(a, s);
+  else return a.beta ? prefill16<D, T, true>(a, s) : prefill16<D, T, false>(a, s);
+}
 template <typename T>
 hipError_t prefill_t(int d, const LinearArgs& a, hipStream_t s) {
   switch (d) {
-    case 16: return prefill_dt<16, T>(a, s);
-    case 32: return prefill_dt<32, T>(a, s);
-    case 64: return prefill_dt<64, T>(a, s);
-    default: return prefill_dt<128, T>(a, s);
+    case 16: return prefill_any<16, T>(a, s);
+    case 32: return prefill_any<32, T>(a, s);
+    case 64: return prefill_any<64, T>(a, s);
+    default: return prefill_any<128, T>(a, s);
   }
 }
 template <typename T>
@@ -450,8 +1117,9 @@ hipError_t step_t(int d, const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t chunk_bytes(int rule, int dtype) {
-  (void)dtype;
-  return sizeof(float) * ((rule == STEPQ_RULE_DELTA ? 2 : 1) * C * C + 2 * C);
+  const bool delta = rule == STEPQ_RULE_DELTA;
+  if (dtype == STEPQ_F32) return sizeof(float) * ((delta ? 2 : 1) * C * C + 2 * C);
+  return 2 * C * sizeof(float) + (delta ? 4 : 2) * kTri;
 }
 
 hipError_t launch_linear_prefill(const stepq_linear_desc& d, const LinearArgs& a, hipStream_t s) {

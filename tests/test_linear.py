@@ -302,6 +302,20 @@ def test_slices_of_a_fused_projection(dtype, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("rule", ["additive", "delta"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_many_requests(dtype, rule, D):
+    """More (request, head) pairs than compute units: a head is not split over workgroups."""
+    g = np.random.default_rng(D)
+    lengths = [int(x) for x in g.choice([0, 1, 3, 40, 64, 70, 130], size=90)]
+    r = Run(dtype, 3, 3, D, rule, lengths, seed=D, fused=D == 64)
+    resume = (g.random(90) < 0.5).astype(np.uint8)
+    r.prefill(resume)
+    r.check(resume)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rule", ["additive", "delta"])
 def test_long_prompt_many_chunks(rule):
     r = Run("bf16", 2, 1, 128, rule, [3001, 5], seed=8)
