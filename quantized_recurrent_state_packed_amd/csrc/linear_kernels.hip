@@ -78,6 +78,19 @@ __device__ __forceinline__ Frag cols_of(const float* x, int ld, int lane) {
   return f;
 }
 
+// Keeps the compiler from moving loads across: registers are what bounds it.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// Stands between matrix instructions and a branch.  A matrix instruction's result
+// may be read only some cycles later (up to 11 wait states here), which the compiler
+// sees to within a straight run of code; over a branch it has been seen to read
+// too early, so no such result is left open at one.
+__device__ __forceinline__ void settle() {
+  in_order();
+  asm volatile("s_nop 15");
+  in_order();
+}
+
 template <int D>
 struct Dims {
   static constexpr int DP = D < 32 ? 32 : D;   // depth of products over key channels, zero-padded to 32
@@ -132,7 +145,25 @@ __device__ __forceinline__ void stage(float* lds, const T* x, int64_t stride, in
   }
 }
 
-template <int D, typename T>
+// Block column J of (I + B)^-1 diag(beta), one wave.
+template <int J>
+__device__ __forceinline__ void invert_column(const float* low, int ls, const float (*inv)[16 * 20], const float* bt,
+                                              float* t, int lane) {
+  const int g = lane >> 4, c = lane & 15;
+  f32x4 col[4] = {};
+  for (int e = 0; e < 4; ++e) col[J][e] = inv[J][(4 * g + e) * 20 + c];
+  for (int i = J + 1; i < 4; ++i) {
+    f32x4 s = {};
+    for (int k = J; k < i; ++k) s = mma16(*reinterpret_cast<const f32x4*>(low + (16 * i + c) * ls + 16 * k + 4 * g), col[k], s);
+    const f32x4 ti = *reinterpret_cast<const f32x4*>(&inv[i][c * 20 + 4 * g]);
+    col[i] = mma16(-ti, s, f32x4{});
+  }
+  settle();
+  for (int i = 0; i < 4; ++i)
+    for (int e = 0; e < 4; ++e) t[(16 * i + 4 * g + e) * C + 16 * J + c] = col[i][e] * bt[16 * J + c];
+}
+
+template <int D, typename T, bool DELTA>
 __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
   using S = Dims<D>;
   constexpr int LS = C + 4;
@@ -141,7 +172,6 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
   __shared__ __align__(16) float inv[4][16 * 20];
   __shared__ double lg[C];
   __shared__ float bt[C];
-  const bool delta = p.beta != nullptr;
   const int h = blockIdx.x % p.H;
   const int64_t w = blockIdx.x / p.H;
   // the request whose range of chunk indices holds w: the last b with cu[b] / C + b <= w
@@ -156,11 +186,11 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
   if (c < 0 || c * C >= r.count) return;
   const int64_t first = r.first + c * C;
   const int count = min(C, static_cast<int>(r.count - c * C));
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
 
   stage<D>(kq[0], static_cast<const T*>(p.k) + first * p.k_stride + (h / p.rep) * D, p.k_stride, count);
   stage<D>(kq[1], static_cast<const T*>(p.q) + first * p.q_stride + (h / p.rep) * D, p.q_stride, count);
-  const ChunkWs ws = chunk_ws(p.workspace, w * p.H + h, delta);
+  const ChunkWs ws = chunk_ws(p.workspace, w * p.H + h, DELTA);
   if (wave == 0) {
     // log2 G as a running sum in binary64, so that ratios of retentions far
     // into a fast-forgetting chunk keep binary32 accuracy; a retention of 0 (or
@@ -176,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
     }
     const double all = __shfl(x, 63);
     lg[lane] = x;
-    bt[lane] = delta && lane < count ? p.beta[(first + lane) * p.H + h] : 0.0f;
+    bt[lane] = DELTA && lane < count ? p.beta[(first + lane) * p.H + h] : 0.0f;
     ws.grow[lane] = exp2f(static_cast<float>(x));
     ws.left[lane] = exp2f(static_cast<float>(all - x));
   }
@@ -185,21 +215,21 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
   // rows 16 wave .. 16 wave + 15 of K K^T and Q K^T
   for (int ct = 0; ct < 4; ++ct) {
     f32x4 kk = {}, qk = {};
-    if (ct <= wave)
-      for (int kb = 0; kb < S::KB; ++kb) {
-        const Frag kr = rows_of(kq[0] + 16 * ct * S::LD + 32 * kb, S::LD, lane);
-        if (delta) kk = mma(rows_of(kq[0] + 16 * wave * S::LD + 32 * kb, S::LD, lane), kr, kk);
-        qk = mma(rows_of(kq[1] + 16 * wave * S::LD + 32 * kb, S::LD, lane), kr, qk);
-      }
+    for (int kb = 0; kb < S::KB; ++kb) {
+      const Frag kr = rows_of(kq[0] + 16 * ct * S::LD + 32 * kb, S::LD, lane);
+      if constexpr (DELTA) kk = mma(rows_of(kq[0] + 16 * wave * S::LD + 32 * kb, S::LD, lane), kr, kk);
+      qk = mma(rows_of(kq[1] + 16 * wave * S::LD + 32 * kb, S::LD, lane), kr, qk);
+    }
+    settle();
     const int j = 16 * ct + (lane & 15);
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * wave + 4 * g + e;
-      const float ratio = exp2f(static_cast<float>(lg[i] - lg[j]));
-      ws.a[i * C + j] = j <= i ? qk[e] * ratio : 0.0f;
-      if (delta) low[i * LS + j] = j < i ? kk[e] * ratio * bt[i] : 0.0f;
+      const float ratio = j <= i ? exp2f(static_cast<float>(lg[i] - lg[j])) : 0.0f;
+      ws.a[i * C + j] = qk[e] * ratio;
+      if constexpr (DELTA) low[i * LS + j] = j < i ? kk[e] * ratio * bt[i] : 0.0f;
     }
   }
-  if (!delta) return;
+  if constexpr (!DELTA) return;
   __syncthreads();
 
   // (I + B)^-1.  Diagonal blocks of 16 by forward substitution, one column per
@@ -216,26 +246,15 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
     for (int i = 0; i < 16; ++i) inv[g][i * 20 + (lane & 15)] = x[i];
   }
   __syncthreads();
-  f32x4 col[4];
-  const int j = 16 * wave + (lane & 15);
-  for (int i = 0; i < 4; ++i) {
-    if (i < wave) {
-      col[i] = f32x4{};
-    } else if (i == wave) {
-      for (int e = 0; e < 4; ++e) col[i][e] = inv[i][(4 * g + e) * 20 + (lane & 15)];
-    } else {
-      f32x4 s = {};
-      for (int k = 0; k < i; ++k)
-        if (k >= wave)
-          s = mma16(*reinterpret_cast<const f32x4*>(low + (16 * i + (lane & 15)) * LS + 16 * k + 4 * g), col[k], s);
-      f32x4 ti = *reinterpret_cast<const f32x4*>(&inv[i][(lane & 15) * 20 + 4 * g]);
-      col[i] = mma16(-ti, s, f32x4{});
-    }
-    for (int e = 0; e < 4; ++e) ws.t[(16 * i + 4 * g + e) * C + j] = col[i][e] * bt[j];
+  switch (wave) {
+    case 0: return invert_column<0>(low, LS, inv, bt, ws.t, lane);
+    case 1: return invert_column<1>(low, LS, inv, bt, ws.t, lane);
+    case 2: return invert_column<2>(low, LS, inv, bt, ws.t, lane);
+    default: return invert_column<3>(low, LS, inv, bt, ws.t, lane);
   }
 }
 
-template <int D, typename T, int NW>
+template <int D, typename T, bool DELTA, int NW>
 __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
   using S = Dims<D>;
   constexpr int LA = C + 4;
@@ -246,8 +265,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
   float* la = lq + C * S::LD;
   float* lt = la + C * LA;
   __shared__ float grow[C], left[C];
-  const bool delta = p.beta != nullptr;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
   const int h = (blockIdx.x / SPLIT) % p.H;
   const int b = blockIdx.x / (SPLIT * p.H);
   const int vcol = (blockIdx.x % SPLIT) * 16 * NW + 16 * wave + (lane & 15);
@@ -272,14 +290,14 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
   for (int c = 0; c * C < r.count; ++c) {
     const int count = min(C, r.count - c * C);
     const int64_t t0 = static_cast<int64_t>(c) * C;
-    const ChunkWs ws = chunk_ws(p.workspace, (base + c) * p.H + h, delta);
+    const ChunkWs ws = chunk_ws(p.workspace, (base + c) * p.H + h, DELTA);
     __syncthreads();
     stage<D>(lk, k + t0 * p.k_stride, p.k_stride, count);
     stage<D>(lq, q + t0 * p.q_stride, p.q_stride, count);
     for (int i = tid; i < C * C / 4; i += 64 * NW) {
       const int row = i / (C / 4), col = i % (C / 4) * 4;
       *reinterpret_cast<f32x4*>(la + row * LA + col) = reinterpret_cast<const f32x4*>(ws.a)[i];
-      if (delta) *reinterpret_cast<f32x4*>(lt + row * LA + col) = reinterpret_cast<const f32x4*>(ws.t)[i];
+      if constexpr (DELTA) *reinterpret_cast<f32x4*>(lt + row * LA + col) = reinterpret_cast<const f32x4*>(ws.t)[i];
     }
     for (int i = tid; i < C; i += 64 * NW) grow[i] = ws.grow[i], left[i] = ws.left[i];
     f32x4 u[4];
@@ -292,7 +310,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
 
     Frag mf[S::KB];
     for (int kb = 0; kb < S::KB; ++kb) mf[kb] = from_tiles(m[2 * kb], D < 32 ? f32x4{} : m[D < 32 ? 0 : 2 * kb + 1]);
-    if (delta) {
+    if constexpr (DELTA) {
       for (int i = 0; i < 4; ++i) {
         f32x4 s = {};
         for (int kb = 0; kb < S::KB; ++kb) s = mma(rows_of(lk + 16 * i * S::LD + 32 * kb, S::LD, lane), mf[kb], s);
@@ -312,6 +330,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
       for (int e = 0; e < 4; ++e) s[e] *= grow[16 * i + 4 * g + e];
       s = mma(rows_of(la + 16 * i * LA, LA, lane), uf[0], s);
       if (i >= 2) s = mma(rows_of(la + 16 * i * LA + 32, LA, lane), uf[1], s);
+      settle();
       for (int e = 0; e < 4; ++e) {
         const int t = 16 * i + 4 * g + e;
         if (t < count) o[(t0 + t) * p.o_stride] = static_cast<T>(s[e]);
@@ -326,6 +345,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
       for (int tb = 0; tb < 2; ++tb) s = mma(cols_of(lk + 32 * tb * S::LD + 16 * i, S::LD, lane), wf[tb], s);
       m[i] = s;
     }
+    settle();
   }
   for (int i = 0; i < S::RT; ++i)
     for (int e = 0; e < 4; ++e) state[(16 * i + 4 * g + e) * D] = m[i][e];
@@ -345,9 +365,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// Keeps the compiler from moving loads across: registers are what bounds it.
-__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // x, in a register whose value the compiler does not know: addresses derived from
 // it are computed where they are used instead of being kept through the loop over
@@ -525,6 +542,24 @@ struct Rows {
   }
 };
 
+// One word of every 128 bytes of a chunk's rows of x, read while an earlier chunk is
+// computed so that the rows come from L2 when they are staged: two or three
+// registers, where the rows themselves would take 48.
+template <int D, typename T, int THREADS>
+struct Touch {
+  static constexpr int LINES = (2 * D + 127) / 128, L = (C * LINES + THREADS - 1) / THREADS;
+  uint32_t word[L] = {};
+  __device__ __forceinline__ void start(const T* x, int64_t stride, int count, int tid) {
+    for (int j = 0; j < L; ++j) {
+      const int i = tid + j * THREADS;
+      if (i < C * LINES) word[j] = *reinterpret_cast<const uint32_t*>(x + min(i / LINES, count - 1) * stride + i % LINES * 64);
+    }
+  }
+  __device__ __forceinline__ void end() {
+    for (int j = 0; j < L; ++j) asm volatile("" ::"v"(word[j]));
+  }
+};
+
 // What a chunk's retentions and betas come to, in LDS.
 struct Rates {
   double lg[C];      // log2 G
@@ -603,6 +638,7 @@ __device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq
       qk = mma<true>(kj, qi, qk);                            // rows: key token 16 j + 4 g + e, column: query token 16 i + c
       if constexpr (DELTA) kk = mma<true>(ki, kj, kk);       // rows: token 16 i + 4 g + e, column: token 16 j + c
     }
+    settle();
     const double lq_i = r.lg[16 * i + c];
     for (int e = 0; e < 4; ++e) {
       const int t = 16 * j + 4 * g + e;
@@ -659,25 +695,30 @@ __device__ __forceinline__ void store_tiles(uint8_t* to, const ATile (&tiles)[kT
 // Second part, wave i: block row i of T = (I + B)^-1 diag(beta), transposed, from
 // the diagonal leftwards: X_ij = -(sum_{k > j} X_ik B_kj) (I + B_jj)^-1.  Like the
 // substitution it is as stable as solving for U token by token.
-__device__ __forceinline__ void invert_row(const Scratch* sc, const Rates& r, uint8_t* lt, int i, int lane) {
+template <int I>
+__device__ __forceinline__ void invert_row_of(const Scratch* sc, const Rates& r, uint8_t* lt, int lane) {
   const int g = lane >> 4, c = lane & 15;
-  f32x4 x[4] = {};
-  for (int j = 3; j >= 0; --j) {
-    if (j > i) continue;
-    if (j == i) {
-      x[j] = *reinterpret_cast<const f32x4*>(&sc->diag[j][c * 20 + 4 * g]);
-      continue;
-    }
+  f32x4 x[I + 1];
+  x[I] = *reinterpret_cast<const f32x4*>(&sc->diag[I][c * 20 + 4 * g]);
+  for (int j = I - 1; j >= 0; --j) {
     f32x4 d, s = {};
     for (int e = 0; e < 4; ++e) d[e] = -sc->diag[j][(4 * g + e) * 20 + c];
-    for (int k = j + 1; k < 4; ++k)
-      if (k <= i) s = mma16(sc->off[pair(k, j)][lane], x[k], s);
+    for (int k = j + 1; k <= I; ++k) s = mma16(sc->off[pair(k, j)][lane], x[k], s);
     x[j] = mma16(d, s, f32x4{});
   }
-  for (int j = 0; j < 4; ++j) {
-    if (j > (i | 1)) break;
-    const f32x4 s = x[j] * *reinterpret_cast<const f32x4*>(&r.beta[16 * j + 4 * g]);
-    store_parts(lt, lt + kTri, tri(i, j >> 1), j & 1, s, lane);
+  settle();
+  for (int j = 0; j <= (I | 1); ++j) {
+    f32x4 s = {};
+    if (j <= I) s = x[j < I ? j : I] * *reinterpret_cast<const f32x4*>(&r.beta[16 * j + 4 * g]);
+    store_parts(lt, lt + kTri, tri(I, j >> 1), j & 1, s, lane);
+  }
+}
+__device__ __forceinline__ void invert_row(const Scratch* sc, const Rates& r, uint8_t* lt, int i, int lane) {
+  switch (i) {
+    case 0: return invert_row_of<0>(sc, r, lt, lane);
+    case 1: return invert_row_of<1>(sc, r, lt, lane);
+    case 2: return invert_row_of<2>(sc, r, lt, lane);
+    default: return invert_row_of<3>(sc, r, lt, lane);
   }
 }
 
@@ -805,40 +846,30 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
 
   const int64_t base = r.first / C + b;
   constexpr int VU = COLS / 8;      // units of the workgroup's columns
-  Rows<D, T, S::CPR, 64 * NW> kr, qr;
-  Rows<D, T, VU, 64 * NW> vr;
   float gate = 0.0f, beta = 0.0f;
-  // the next chunk's rows are on their way while this one is computed
-  auto fetch = [&](int c) {
-    const int count = min(C, r.count - c * C);
-    const int64_t t0 = static_cast<int64_t>(c) * C;
-    const int t = fresh(tid);
-    kr.load(k + t0 * p.k_stride, p.k_stride, count, 0, t);
-    qr.load(q + t0 * p.q_stride, p.q_stride, count, 0, t);
-    vr.load(v + t0 * p.v_stride, p.v_stride, count, part * VU, t);
-  };
-  // the last wave, which has the fewest blocks, sets the next chunk's rates
-  auto fetch_rates = [&](int c) {
-    const int count = min(C, r.count - c * C);
-    const int64_t token = (r.first + static_cast<int64_t>(c) * C + min(lane, count - 1)) * p.H + h;
+  Touch<D, T, 64 * NW> kt, qt, vt;
+  if (FUSED && r.count > 0 && wave == NW - 1) {
+    const int64_t token = (r.first + min(lane, r.count - 1)) * p.H + h;
     gate = p.gate[token];
     if constexpr (DELTA) beta = p.beta[token];
-  };
-  if (r.count > 0) {
-    fetch(0);
-    if (FUSED && wave == NW - 1) {
-      fetch_rates(0);
-      set_rates(all_rates[0], gate, beta, min(C, r.count), lane);
-    }
+    set_rates(all_rates[0], gate, beta, min(C, r.count), lane);
   }
   for (int c = 0; c * C < r.count; ++c) {
     const int count = min(C, r.count - c * C);
     const int64_t t0 = static_cast<int64_t>(c) * C;
     const bool more = t0 + C < r.count;
     Rates& rates = all_rates[FUSED ? c & 1 : 0];
-    __syncthreads();
+    kt.end();
+    qt.end();
+    vt.end();
     {
+      Rows<D, T, S::CPR, 64 * NW> kr, qr;
+      Rows<D, T, VU, 64 * NW> vr;
       const int t = fresh(tid);
+      kr.load(k + t0 * p.k_stride, p.k_stride, count, 0, t);
+      qr.load(q + t0 * p.q_stride, p.q_stride, count, 0, t);
+      vr.load(v + t0 * p.v_stride, p.v_stride, count, part * VU, t);
+      __syncthreads();
       kr.template store<NP == 2>(lk, count, 0, t);
       qr.template store<NP == 2>(lq, count, 0, t);
       vr.template store<false>(lv, count, part * VU, t);
@@ -846,7 +877,11 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
     ATile tiles[kTiles];
     if constexpr (FUSED) {
       const bool next = more && wave == NW - 1;
-      if (next) fetch_rates(c + 1);
+      if (next) {     // the last wave, which has the fewest blocks, sets the next chunk's rates
+        const int64_t token = (r.first + t0 + C + min(lane, r.count - (c + 1) * C - 1)) * p.H + h;
+        gate = p.gate[token];
+        if constexpr (DELTA) beta = p.beta[token];
+      }
       __syncthreads();
       chunk_tiles<D, T, DELTA>(lk, lq, rates, sc, tiles, wave, fresh(lane));
       store_tiles(la, tiles, false, wave, fresh(lane));
@@ -867,6 +902,13 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
         for (int i = tid * 16; i < 2 * kTri; i += 64 * NW * 16)
           *reinterpret_cast<u32x4*>(lt + i) = *reinterpret_cast<const u32x4*>(ws + 2 * kTri + i);
       __syncthreads();
+    }
+
+    if (more) {
+      const int t = fresh(tid), n = min(C, r.count - (c + 1) * C);
+      kt.start(k + (t0 + C) * p.k_stride, p.k_stride, n, t);
+      qt.start(q + (t0 + C) * p.q_stride, p.q_stride, n, t);
+      vt.start(v + (t0 + C) * p.v_stride, p.v_stride, n, t);
     }
 
     // K M and (transposed: rows value columns, columns tokens, so that a lane stores
@@ -934,6 +976,9 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
           const Parts<2> a = stored_parts(la, lr, tri(i, tb), l);
           for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
         }
+      }
+      settle();
+      for (int i = 0; i < 4; ++i) {
         const int t = 16 * i + cl;
         if (t < count)
           for (int n = 0; n < NCT; ++n) {
@@ -944,7 +989,6 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       }
     }
     in_order();
-    if (more) fetch(c + 1);
     const int l = fresh(lane), g = l >> 4;
     const At at = lane_at<S::RB>(l);
     Parts<2> wf[NCT][2];
@@ -962,6 +1006,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       }
       if (i % 2) in_order();
     }
+    settle();
   }
   const int l = fresh(lane), at = (l >> 4) * 4 * D + (l & 15);
   for (int n = 0; n < NCT; ++n)
@@ -1040,16 +1085,16 @@ __global__ void __launch_bounds__(kThreads) k_linear_step(LinearArgs p) {
     for (int e = 0; e < 4; ++e) o[e] = static_cast<T>(w[e] + qk * x[e]);
 }
 
-template <int D, typename T>
+template <int D, typename T, bool DELTA>
 hipError_t prefill_dt(const LinearArgs& a, hipStream_t s) {
   using S = Dims<D>;
   constexpr int NW = D >= 64 ? 4 : D / 16;
   const int64_t chunks = max_chunks(a.total_tokens, a.batch);
-  k_linear_chunks<D, T><<<dim3(static_cast<uint32_t>(chunks * a.H)), kThreads, 0, s>>>(a);
+  k_linear_chunks<D, T, DELTA><<<dim3(static_cast<uint32_t>(chunks * a.H)), kThreads, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t lds = sizeof(float) * (2 * C * S::LD + (a.beta ? 2 : 1) * C * (C + 4));
-  auto* kern = k_linear_walk<D, T, NW>;
+  const size_t lds = sizeof(float) * (2 * C * S::LD + (DELTA ? 2 : 1) * C * (C + 4));
+  auto* kern = k_linear_walk<D, T, DELTA, NW>;
   e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                           static_cast<int>(lds));
   if (e != hipSuccess) return e;
@@ -1092,7 +1137,7 @@ hipError_t step_dt(const LinearArgs& a, hipStream_t s) {
 
 template <int D, typename T>
 hipError_t prefill_any(const LinearArgs& a, hipStream_t s) {
-  if constexpr (sizeof(T) == 4) return prefill_dt<D, T>(a, s);
+  if constexpr (sizeof(T) == 4) return a.beta ? prefill_dt<D, T, true>(a, s) : prefill_dt<D, T, false>(a, s);
   else return a.beta ? prefill16<D, T, true>(a, s) : prefill16<D, T, false>(a, s);
 }
 template <typename T>
