@@ -12,7 +12,7 @@
 //   u_t = b_t (v_t - G_t M^T k_t - sum_{j < t} (G_t / G_j) (k_j . k_t) u_j),
 // that is (I + B) U = diag(b) (V - diag(G) K M) with the strictly lower
 // triangular B_tj = b_t (G_t / G_j) k_t . k_j.  So, per chunk,
-//   U = T (V - diag(G) K M),  T = (I + B)^-1 diag(b)
+//   U = (I + B)^-1 diag(b) (V - diag(G) K M)
 //   O = diag(G) Q M + A U,    A_tj = (G_t / G_j) q_t . k_j  for j <= t
 //   M <- G_C M + K^T diag(G_C / G) U
 // T and A do not depend on the state: k_linear_chunks computes them for all
@@ -419,14 +419,13 @@ struct Dims16 {
   static constexpr int RB = 2 * DP;              // bytes of a row in LDS
   static constexpr int CPR = RB / 16;            // 16-byte units of a row
   static constexpr int KB = DP / 32;
-  static constexpr int RT = D / 16;
+  static constexpr int RT = DP / 16;              // tiles of 16 key channels of a state
   static constexpr int MAT = C * RB;             // bytes of one part of q, k or v
 };
 
 // A row's 16-byte units are permuted within it (exclusive or with a number that
 // depends on the row), so that the 16 rows an operand takes from a column of
-// units, and the four 8-byte pieces a transposing read takes from each of 16
-// rows, fall on different banks.
+// units fall on different banks.
 template <int RB>
 __device__ __forceinline__ int unit_at(int row, int unit) {
   return row * RB + ((unit ^ ((row / (256 / RB)) & (RB / 16 - 1))) << 4);
@@ -436,35 +435,40 @@ __device__ __forceinline__ int unit_at(int row, int unit) {
 // bytes a lane, 1024 in all, in the order lanes hold it.
 constexpr int kTri = 6 * 1024;
 
-// Where a lane reads the operands of a matrix in LDS: `row` for row_operand and
-// `col` for column_piece with i = kb = t = 0.  Others differ by whole 16 rows and
-// in the bits of the unit, which commute with the permutation.
+// Depth over key channels runs, within every 32, in their own order: a lane's eight
+// values of an operand are 16 consecutive bytes of a row.  So the 16 rows of state
+// tile t that a lane's accumulators hold, 4 g + e, are key channels
+// 32 (t / 2) + 8 g + 4 (t % 2) + e, and two tiles are an operand as they stand.
+//
+// Where a lane reads: `row` for row_operand, `col` for column_operand and `val` for
+// value_piece, of tile 0.  Other tiles differ by whole 16 rows and in the bits of
+// the unit, which commute with the permutation.
 struct At {
-  int row, col;
+  int row, col, val;
 };
 template <int RB>
 __device__ __forceinline__ At lane_at(int lane) {
   const int g = lane >> 4, c = lane & 15;
-  return {unit_at<RB>(c, g >> 1) + (g & 1) * 8, unit_at<RB>(4 * g + (c >> 2), (c & 3) >> 1) + (c & 1) * 8};
+  return {unit_at<RB>(c, g), unit_at<RB>(4 * g + (c >> 2), c & 3), unit_at<RB>(4 * g + (c >> 2), (c & 3) >> 1) + (c & 1) * 8};
 }
 // Operand whose row lane % 16 is row 16 i + lane % 16 of x, depth 32 kb ..
 template <int RB>
 __device__ __forceinline__ bf16x8 row_operand(const uint8_t* x, int i, int kb, At at) {
-  x += 16 * i * RB;
-  return join(*reinterpret_cast<const bf16x4*>(x + (at.row ^ (4 * kb) << 4)),
-              *reinterpret_cast<const bf16x4*>(x + (at.row ^ (4 * kb + 2) << 4)));
+  return *reinterpret_cast<const bf16x8*>(x + 16 * i * RB + (at.row ^ kb << 6));
 }
-// Rows 16 i + 4 g .. + 3 (g = lane / 16) of column 16 t + lane % 16 of x.
-template <int RB>
-__device__ __forceinline__ s16x4 column_piece(const uint8_t* x, int i, int t, At at) {
-  x += 16 * i * RB;
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(const_cast<uint8_t*>(x + (at.col ^ (2 * t) << 4))));
+__device__ __forceinline__ s16x4 read_transposed(const uint8_t* x) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(const_cast<uint8_t*>(x)));
 }
-// Operand whose row lane % 16 is column 16 t + lane % 16 of x, depth rows 32 tb ..
+// Operand whose rows are the key channels of state tile t, depth tokens 32 tb ..
 template <int RB>
 __device__ __forceinline__ bf16x8 column_operand(const uint8_t* x, int tb, int t, At at) {
-  return join(__builtin_bit_cast(bf16x4, column_piece<RB>(x, 2 * tb, t, at)),
-              __builtin_bit_cast(bf16x4, column_piece<RB>(x, 2 * tb + 1, t, at)));
+  x += 32 * tb * RB + (at.col ^ (t >> 1) << 6) + (t & 1) * 8;
+  return join(__builtin_bit_cast(bf16x4, read_transposed(x)), __builtin_bit_cast(bf16x4, read_transposed(x + 16 * RB)));
+}
+// Tokens 16 i + 4 g .. + 3 (g = lane / 16) of value column 16 t + lane % 16 of x.
+template <int RB>
+__device__ __forceinline__ s16x4 value_piece(const uint8_t* x, int i, int t, At at) {
+  return read_transposed(x + 16 * i * RB + (at.val ^ (2 * t) << 4));
 }
 __device__ __forceinline__ bf16x8 stored_operand(const uint8_t* x, int n, int lane) {
   return *reinterpret_cast<const bf16x8*>(x + n * 1024 + lane * 16);
@@ -589,14 +593,10 @@ __device__ __forceinline__ void set_rates(Rates& r, float gate, float beta, int 
   r.beta[lane] = lane < count ? beta : 0.0f;
 }
 
-// Scratch of the chunk matrices: the blocks of B below the diagonal as operands
-// (lane: row lane % 16 of the transposed block, depth 4 g + e), and the diagonal
-// blocks, later their inverses, in rows of 20.
+// Diagonal blocks of B, later their inverses, in rows of 20.
 struct Scratch {
-  f32x4 off[6][64];
   float diag[4][16 * 20];
 };
-__device__ constexpr int pair(int k, int j) { return k * (k - 1) / 2 + j; }
 
 // The ten blocks (i, j), j <= i < 4, of a chunk's lower triangles, dealt out to four
 // waves; a wave's first is the diagonal one of its number.
@@ -609,17 +609,15 @@ __device__ __forceinline__ int tile_of(int wave, int n) {      // 4 i + j, or -1
   }
 }
 
-// A block's A values on their way to LDS.
-struct ATile {
-  bf16x4 hi, lo;
-};
-
-// First part, wave `wave` of four: its blocks of B into the scratch, its blocks of
-// A into registers, and the inverse of its diagonal block of I + B by forward
-// substitution (a column for every lane of 16, the other lanes doing the same).
+// Wave `wave` of four: its blocks of A and of the system for U into LDS, both as
+// operands in two parts (`lt`, `la`: the larger, then the smaller ones).  With
+// B = diag(b) B', U comes from block rows of 16 tokens in turn,
+//   U_i = D_i (R_i - sum_{j < i} B'_ij U_j),  D_i = (I + B_ii)^-1 diag(b_i),
+// so the system is stored as -B'_ij below the diagonal and D_i on it.  The inverse
+// is found by forward substitution, a column for every lane of 16 (four times over).
 template <int D, typename T, bool DELTA>
 __device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq, const Rates& r, Scratch* sc,
-                                            ATile (&tiles)[kTiles], int wave, int lane) {
+                                            uint8_t* la, uint8_t* lt, int wave, int lane) {
   using S = Dims16<D, T>;
   const At at = lane_at<S::RB>(lane);
   const int g = lane >> 4, c = lane & 15;
@@ -627,6 +625,7 @@ __device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq
     const int tile = tile_of(wave, n);
     if (tile < 0) break;
     const int i = tile >> 2, j = tile & 3;
+    // rows: key token 16 j + 4 g + e, column: token 16 i + c
     f32x4 kk = {}, qk = {};
     for (int kb = 0; kb < S::KB; ++kb) {
       Parts<S::NP> ki, qi, kj;
@@ -635,30 +634,25 @@ __device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq
         qi.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
         if constexpr (DELTA) ki.p[x] = n == 0 ? kj.p[x] : row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
       }
-      qk = mma<true>(kj, qi, qk);                            // rows: key token 16 j + 4 g + e, column: query token 16 i + c
-      if constexpr (DELTA) kk = mma<true>(ki, kj, kk);       // rows: token 16 i + 4 g + e, column: token 16 j + c
+      qk = mma<true>(kj, qi, qk);
+      if constexpr (DELTA) kk = mma<true>(kj, ki, kk);
     }
     settle();
-    const double lq_i = r.lg[16 * i + c];
+    const double li = r.lg[16 * i + c];
+    f32x4 ratio;
     for (int e = 0; e < 4; ++e) {
-      const int t = 16 * j + 4 * g + e;
-      const float ratio = __builtin_amdgcn_exp2f(static_cast<float>(lq_i - r.lg[t]));
-      qk[e] = n > 0 || 4 * g + e <= c ? qk[e] * ratio : 0.0f;
+      const float x = __builtin_amdgcn_exp2f(static_cast<float>(li - r.lg[16 * j + 4 * g + e]));
+      ratio[e] = n > 0 || 4 * g + e <= c ? x : 0.0f;
     }
-    tiles[n].hi = rounded(qk);
-    tiles[n].lo = rounded(qk - widened(tiles[n].hi));
+    const int to = tri(i, j >> 1);
+    store_parts(la, la + kTri, to, j & 1, qk * ratio, lane);
     if constexpr (DELTA) {
-      const double lk_j = r.lg[16 * j + c];
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * i + 4 * g + e;
-        kk[e] *= r.beta[t] * __builtin_amdgcn_exp2f(static_cast<float>(r.lg[t] - lk_j));
-      }
       if (n > 0) {
-        sc->off[pair(i, j)][lane] = kk;
+        store_parts(lt, lt + kTri, to, j & 1, -kk * ratio, lane);
       } else {
-        // only what lies below the diagonal is read; a wave's own LDS accesses are in order
+        // the wave's own LDS accesses are in order; of B only what is below the diagonal is read
         float* d = sc->diag[wave];
-        for (int e = 0; e < 4; ++e) d[(4 * g + e) * 20 + c] = kk[e];
+        *reinterpret_cast<f32x4*>(d + c * 20 + 4 * g) = kk * ratio * r.beta[16 * i + c];
         wave_order();
         float x[16];
         for (int q = 0; q < 4; ++q) {
@@ -675,82 +669,47 @@ __device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq
         wave_order();
         if (g == 0)
           for (int ii = 0; ii < 16; ++ii) d[ii * 20 + c] = x[ii];
+        wave_order();
+        const f32x4 inv = *reinterpret_cast<const f32x4*>(d + c * 20 + 4 * g) *
+                          *reinterpret_cast<const f32x4*>(&r.beta[16 * i + 4 * g]);
+        store_parts(lt, lt + kTri, to, j & 1, inv, lane);
       }
     }
     in_order();
   }
-}
-
-// Writes one part of a wave's blocks of A, and the zeros beside its diagonal block.
-__device__ __forceinline__ void store_tiles(uint8_t* to, const ATile (&tiles)[kTiles], bool rest, int wave, int lane) {
-  for (int n = 0; n < kTiles; ++n) {
-    const int tile = tile_of(wave, n);
-    if (tile < 0) break;
-    const int i = tile >> 2, j = tile & 3;
-    *reinterpret_cast<bf16x4*>(to + tri(i, j >> 1) * 1024 + lane * 16 + (j & 1) * 8) = rest ? tiles[n].lo : tiles[n].hi;
-  }
-  if ((wave & 1) == 0) *reinterpret_cast<bf16x4*>(to + tri(wave, wave >> 1) * 1024 + lane * 16 + 8) = bf16x4{};
-}
-
-// Second part, wave i: block row i of T = (I + B)^-1 diag(beta), transposed, from
-// the diagonal leftwards: X_ij = -(sum_{k > j} X_ik B_kj) (I + B_jj)^-1.  Like the
-// substitution it is as stable as solving for U token by token.
-template <int I>
-__device__ __forceinline__ void invert_row_of(const Scratch* sc, const Rates& r, uint8_t* lt, int lane) {
-  const int g = lane >> 4, c = lane & 15;
-  f32x4 x[I + 1];
-  x[I] = *reinterpret_cast<const f32x4*>(&sc->diag[I][c * 20 + 4 * g]);
-  for (int j = I - 1; j >= 0; --j) {
-    f32x4 d, s = {};
-    for (int e = 0; e < 4; ++e) d[e] = -sc->diag[j][(4 * g + e) * 20 + c];
-    for (int k = j + 1; k <= I; ++k) s = mma16(sc->off[pair(k, j)][lane], x[k], s);
-    x[j] = mma16(d, s, f32x4{});
-  }
-  settle();
-  for (int j = 0; j <= (I | 1); ++j) {
-    f32x4 s = {};
-    if (j <= I) s = x[j < I ? j : I] * *reinterpret_cast<const f32x4*>(&r.beta[16 * j + 4 * g]);
-    store_parts(lt, lt + kTri, tri(I, j >> 1), j & 1, s, lane);
-  }
-}
-__device__ __forceinline__ void invert_row(const Scratch* sc, const Rates& r, uint8_t* lt, int i, int lane) {
-  switch (i) {
-    case 0: return invert_row_of<0>(sc, r, lt, lane);
-    case 1: return invert_row_of<1>(sc, r, lt, lane);
-    case 2: return invert_row_of<2>(sc, r, lt, lane);
-    default: return invert_row_of<3>(sc, r, lt, lane);
+  if ((wave & 1) == 0) {      // beside the diagonal
+    store_parts(la, la + kTri, tri(wave, wave >> 1), 1, f32x4{}, lane);
+    if constexpr (DELTA) store_parts(lt, lt + kTri, tri(wave, wave >> 1), 1, f32x4{}, lane);
   }
 }
 
-// A (chunk, head) of the workspace of 16-bit inputs: G, G_C / G, A, T.
+// A (chunk, head) of the workspace of 16-bit inputs: G, G_C / G, A, the system for U.
 __device__ __forceinline__ uint8_t* chunk_ws16(uint8_t* ws, int64_t index, bool delta) {
   return ws + index * (2 * C * 4 + 2 * kTri + (delta ? 2 * kTri : 0));
 }
 
-template <int D, typename T>
+template <int D, typename T, bool DELTA>
 struct Lds16 {
   using S = Dims16<D, T>;
   static constexpr int K = 0;
   static constexpr int Q = K + S::NP * S::MAT;
   static constexpr int V = Q + S::NP * S::MAT;
-  static constexpr int A = V + S::MAT;                                 // the larger part of A
-  static constexpr int RATES = A + kTri;
-  static constexpr int TT = RATES + 2 * static_cast<int>(sizeof(Rates));   // this chunk's and the next one's; T (delta)
-  // the smaller part of A takes the place of the blocks of B, which are done with by then
-  static constexpr int rest(bool delta) { return delta ? TT + 2 * kTri : TT; }
-  static constexpr int fused(bool delta) { return rest(delta) + (delta ? static_cast<int>(sizeof(Scratch)) : kTri); }
-  static constexpr int split(bool delta) { return rest(delta) + kTri; }
+  static constexpr int A = V + S::MAT;
+  static constexpr int RATES = A + 2 * kTri;                           // this chunk's and the next one's
+  static constexpr int TT = RATES + 2 * static_cast<int>(sizeof(Rates));
+  static constexpr int SCRATCH = TT + (DELTA ? 2 * kTri : 0);
+  static constexpr int FUSED = SCRATCH + (DELTA ? static_cast<int>(sizeof(Scratch)) : 0);
+  static constexpr int SPLIT = SCRATCH;
 };
 
 // The chunk matrices of every (chunk, head), for k_linear16_walk<.., false>.
 template <int D, typename T, bool DELTA>
 __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
   using S = Dims16<D, T>;
-  using L = Lds16<D, T>;
+  using L = Lds16<D, T, DELTA>;
   extern __shared__ __align__(16) uint8_t lds16[];
   Rates& rates = *reinterpret_cast<Rates*>(lds16 + L::RATES);
-  uint8_t* lr = lds16 + L::rest(DELTA);
-  Scratch* sc = reinterpret_cast<Scratch*>(lr);
+  Scratch* sc = reinterpret_cast<Scratch*>(lds16 + L::SCRATCH);
   const int h = blockIdx.x % p.H;
   const int64_t w = blockIdx.x / p.H;
   int b = 0;     // the last request with cu[b] / C + b <= w
@@ -777,23 +736,13 @@ __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
   kr.template store<S::NP == 2>(lds16 + L::K, count, 0, tid);
   qr.template store<S::NP == 2>(lds16 + L::Q, count, 0, tid);
   __syncthreads();
-  ATile tiles[kTiles];
-  chunk_tiles<D, T, DELTA>(lds16 + L::K, lds16 + L::Q, rates, sc, tiles, wave, lane);
-  store_tiles(lds16 + L::A, tiles, false, wave, lane);
-  if constexpr (DELTA) {
-    __syncthreads();
-    invert_row(sc, rates, lds16 + L::TT, wave, lane);
-    __syncthreads();
-  }
-  store_tiles(lr, tiles, true, wave, lane);
+  chunk_tiles<D, T, DELTA>(lds16 + L::K, lds16 + L::Q, rates, sc, lds16 + L::A, lds16 + L::TT, wave, lane);
   __syncthreads();
   uint8_t* ws = chunk_ws16(p.workspace, w * p.H + h, DELTA);
   if (tid < 2 * C) reinterpret_cast<float*>(ws)[tid] = (tid < C ? rates.grow : rates.left)[tid % C];
   ws += 2 * C * 4;
-  for (int i = tid * 16; i < kTri; i += kThreads * 16) {
+  for (int i = tid * 16; i < 2 * kTri; i += kThreads * 16)
     *reinterpret_cast<u32x4*>(ws + i) = *reinterpret_cast<const u32x4*>(lds16 + L::A + i);
-    *reinterpret_cast<u32x4*>(ws + kTri + i) = *reinterpret_cast<const u32x4*>(lr + i);
-  }
   if constexpr (DELTA)
     for (int i = tid * 16; i < 2 * kTri; i += kThreads * 16)
       *reinterpret_cast<u32x4*>(ws + 2 * kTri + i) = *reinterpret_cast<const u32x4*>(lds16 + L::TT + i);
@@ -805,7 +754,7 @@ __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
 template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED>
 __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) k_linear16_walk(LinearArgs p) {
   using S = Dims16<D, T>;
-  using L = Lds16<D, T>;
+  using L = Lds16<D, T, DELTA>;
   constexpr int NP = S::NP;
   constexpr int COLS = 16 * NCT * NW;
   constexpr int SPLIT = D / COLS;
@@ -816,8 +765,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
   uint8_t* la = lds16 + L::A;
   uint8_t* lt = lds16 + L::TT;
   Rates* all_rates = reinterpret_cast<Rates*>(lds16 + L::RATES);
-  uint8_t* lr = lds16 + L::rest(DELTA);
-  Scratch* sc = reinterpret_cast<Scratch*>(lr);
+  Scratch* sc = reinterpret_cast<Scratch*>(lds16 + L::SCRATCH);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = blockIdx.x % SPLIT;
   const int h = (blockIdx.x / SPLIT) % p.H;
@@ -836,12 +784,14 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
   const T* q = static_cast<const T*>(p.q) + r.first * p.q_stride + (h / p.rep) * D;
   float* state = p.state + (static_cast<int64_t>(slot) * p.H + h) * D * D + 16 * ct0;
 
-  f32x4 m[NCT][S::RT] = {};    // column 16 (ct0 + n) + lane % 16; tile i holds key channels 16 i + 4 (lane / 16) + e
+  // column 16 (ct0 + n) + lane % 16; tile i holds key channels 32 (i / 2) + 8 g + 4 (i % 2) + e
+  f32x4 m[NCT][S::RT] = {};
   if (p.resume != nullptr && p.resume[b] != 0) {
-    const int l = fresh(lane), at = (l >> 4) * 4 * D + (l & 15);
-    for (int n = 0; n < NCT; ++n)
-      for (int i = 0; i < S::RT; ++i)
-        for (int e = 0; e < 4; ++e) m[n][i][e] = state[at + (16 * i + e) * D + 16 * n];
+    const int l = fresh(lane), g = l >> 4, at = g * 8 * D + (l & 15);
+    if (8 * g < D)
+      for (int n = 0; n < NCT; ++n)
+        for (int i = 0; i < S::RT; ++i)
+          for (int e = 0; e < 4; ++e) m[n][i][e] = state[at + (32 * (i / 2) + 4 * (i % 2) + e) * D + 16 * n];
   }
 
   const int64_t base = r.first / C + b;
@@ -874,7 +824,6 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       qr.template store<NP == 2>(lq, count, 0, t);
       vr.template store<false>(lv, count, part * VU, t);
     }
-    ATile tiles[kTiles];
     if constexpr (FUSED) {
       const bool next = more && wave == NW - 1;
       if (next) {     // the last wave, which has the fewest blocks, sets the next chunk's rates
@@ -883,9 +832,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
         if constexpr (DELTA) beta = p.beta[token];
       }
       __syncthreads();
-      chunk_tiles<D, T, DELTA>(lk, lq, rates, sc, tiles, wave, fresh(lane));
-      store_tiles(la, tiles, false, wave, fresh(lane));
-      if constexpr (!DELTA) store_tiles(lr, tiles, true, wave, fresh(lane));
+      chunk_tiles<D, T, DELTA>(lk, lq, rates, sc, la, lt, wave, fresh(lane));
       if (next) set_rates(all_rates[(c + 1) & 1], gate, beta, min(C, r.count - (c + 1) * C), lane);
     } else {
       const uint8_t* ws = chunk_ws16(p.workspace, (base + c) * p.H + h, DELTA);
@@ -894,10 +841,8 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
         rates.left[i] = reinterpret_cast<const float*>(ws)[C + i];
       }
       ws += 2 * C * 4;
-      for (int i = tid * 16; i < kTri; i += 64 * NW * 16) {
+      for (int i = tid * 16; i < 2 * kTri; i += 64 * NW * 16)
         *reinterpret_cast<u32x4*>(la + i) = *reinterpret_cast<const u32x4*>(ws + i);
-        *reinterpret_cast<u32x4*>(lr + i) = *reinterpret_cast<const u32x4*>(ws + kTri + i);
-      }
       if constexpr (DELTA)
         for (int i = tid * 16; i < 2 * kTri; i += 64 * NW * 16)
           *reinterpret_cast<u32x4*>(lt + i) = *reinterpret_cast<const u32x4*>(ws + 2 * kTri + i);
@@ -919,8 +864,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
     for (int kb = 0; kb < S::KB; ++kb) {
       Parts<2> mf[NCT];
       for (int n = 0; n < NCT; ++n) {
-        const f32x4 zero = {};
-        mf[n] = parts_of<2>(m[n][2 * kb], D < 32 ? zero : m[n][D < 32 ? 0 : 2 * kb + 1]);
+        mf[n] = parts_of<2>(m[n][2 * kb], m[n][2 * kb + 1]);
       }
       for (int i = 0; i < 4; ++i) {
         Parts<NP> a;
@@ -934,46 +878,48 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       in_order();
     }
     }
-    if constexpr (FUSED && DELTA) {
-      __syncthreads();
-      invert_row(sc, rates, lt, wave, fresh(lane));
-      __syncthreads();
-      store_tiles(lr, tiles, true, wave, fresh(lane));
-    }
+    if constexpr (FUSED) __syncthreads();     // A and the system for U
+    Parts<2> uf[NCT][2];
     {
-    const int l = fresh(lane), g = l >> 4;
-    const At at = lane_at<S::RB>(l);
-    for (int n = 0; n < NCT; ++n)
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 x = floats_of(column_piece<S::RB>(lv, i, ct0 + n, at), T{});
-        u[n][i] = DELTA ? x - *reinterpret_cast<const f32x4*>(&rates.grow[16 * i + 4 * g]) * u[n][i] : x;
-      }
-    if constexpr (DELTA) {
-      Parts<2> rf[NCT][2];
+      const int l = fresh(lane), g = l >> 4;
+      const At at = lane_at<S::RB>(l);
       for (int n = 0; n < NCT; ++n)
-        for (int tb = 0; tb < 2; ++tb) rf[n][tb] = parts_of<2>(u[n][2 * tb], u[n][2 * tb + 1]);
-      for (int i = 0; i < 4; ++i) {
-        f32x4 s[NCT] = {};
-        for (int tb = 0; tb <= i / 2; ++tb) {
-          const Parts<2> a = stored_parts(lt, lt + kTri, tri(i, tb), l);
-          for (int n = 0; n < NCT; ++n) s[n] = mma(a, rf[n][tb], s[n]);
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 x = floats_of(value_piece<S::RB>(lv, i, ct0 + n, at), T{});
+          if constexpr (DELTA) u[n][i] = x - *reinterpret_cast<const f32x4*>(&rates.grow[16 * i + 4 * g]) * u[n][i];
+          else u[n][i] = x;
         }
-        for (int n = 0; n < NCT; ++n) u[n][i] = s[n];
+      const f32x4 none = {};
+      if constexpr (DELTA) {
+        Parts<2> s = stored_parts(lt, lt + kTri, tri(0, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][0] = mma(s, parts_of<2>(u[n][0], none), none);
+        s = stored_parts(lt, lt + kTri, tri(1, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(u[n][0], none), u[n][1]);
+        for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(none, u[n][1]), none);
+        for (int n = 0; n < NCT; ++n) uf[n][0] = parts_of<2>(u[n][0], u[n][1]);
+        s = stored_parts(lt, lt + kTri, tri(2, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, uf[n][0], u[n][2]);
+        s = stored_parts(lt, lt + kTri, tri(3, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, uf[n][0], u[n][3]);
+        s = stored_parts(lt, lt + kTri, tri(2, 1), l);
+        for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, parts_of<2>(u[n][2], none), none);
+        s = stored_parts(lt, lt + kTri, tri(3, 1), l);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, parts_of<2>(u[n][2], none), u[n][3]);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, parts_of<2>(none, u[n][3]), none);
+        for (int n = 0; n < NCT; ++n) uf[n][1] = parts_of<2>(u[n][2], u[n][3]);
+      } else {
+        for (int n = 0; n < NCT; ++n)
+          for (int tb = 0; tb < 2; ++tb) uf[n][tb] = parts_of<2>(u[n][2 * tb], u[n][2 * tb + 1]);
       }
       in_order();
     }
-    }
-    if constexpr (FUSED) __syncthreads();     // A
     {
       const int l = fresh(lane), g = l >> 4, cl = l & 15;
-      Parts<2> uf[NCT][2];
-      for (int n = 0; n < NCT; ++n)
-        for (int tb = 0; tb < 2; ++tb) uf[n][tb] = parts_of<2>(u[n][2 * tb], u[n][2 * tb + 1]);
       for (int i = 0; i < 4; ++i) {
         const float grow = rates.grow[16 * i + cl];
         for (int n = 0; n < NCT; ++n) y[n][i] *= grow;
         for (int tb = 0; tb <= i / 2; ++tb) {
-          const Parts<2> a = stored_parts(la, lr, tri(i, tb), l);
+          const Parts<2> a = stored_parts(la, la + kTri, tri(i, tb), l);
           for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
         }
       }
@@ -1008,10 +954,11 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
     }
     settle();
   }
-  const int l = fresh(lane), at = (l >> 4) * 4 * D + (l & 15);
-  for (int n = 0; n < NCT; ++n)
-    for (int i = 0; i < S::RT; ++i)
-      for (int e = 0; e < 4; ++e) state[at + (16 * i + e) * D + 16 * n] = m[n][i][e];
+  const int l = fresh(lane), g = l >> 4, at = g * 8 * D + (l & 15);
+  if (8 * g < D)      // fewer than 32 channels are padded to 32
+    for (int n = 0; n < NCT; ++n)
+      for (int i = 0; i < S::RT; ++i)
+        for (int e = 0; e < 4; ++e) state[at + (32 * (i / 2) + 4 * (i % 2) + e) * D + 16 * n] = m[n][i][e];
 }
 
 // One token: a workgroup owns CW columns of one (request, head) state; a lane
@@ -1113,17 +1060,17 @@ hipError_t launch_lds(K* kern, int64_t grid, int threads, int lds, const LinearA
 
 template <int D, typename T, bool DELTA>
 hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
-  using L = Lds16<D, T>;
+  using L = Lds16<D, T, DELTA>;
   const int64_t tiles = static_cast<int64_t>(a.batch) * a.H;
   if constexpr (D >= 64) {
     if (tiles >= 256)
-      return launch_lds(k_linear16_walk<D, T, DELTA, D / 64, 4, true>, tiles, 256, L::fused(DELTA), a, s);
+      return launch_lds(k_linear16_walk<D, T, DELTA, D / 64, 4, true>, tiles, 256, L::FUSED, a, s);
   }
   const int64_t chunks = max_chunks(a.total_tokens, a.batch);
-  const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, chunks * a.H, kThreads, L::fused(DELTA), a, s);
+  const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, chunks * a.H, kThreads, L::FUSED, a, s);
   if (e != hipSuccess) return e;
   constexpr int NW = D >= 64 ? 2 : 1;
-  return launch_lds(k_linear16_walk<D, T, DELTA, 1, NW, false>, tiles * (D / (16 * NW)), 64 * NW, L::split(DELTA), a, s);
+  return launch_lds(k_linear16_walk<D, T, DELTA, 1, NW, false>, tiles * (D / (16 * NW)), 64 * NW, L::SPLIT, a, s);
 }
 
 template <int D, typename T>
