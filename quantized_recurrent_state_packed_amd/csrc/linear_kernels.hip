@@ -501,7 +501,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // Units u0 .. u0 + N - 1 of the rows of a chunk of x (q, k or v of a head), on the
 // way from memory to LDS in the registers of THREADS threads: all loads are under
 // way before the first is waited for.  A thread has a unit of every THREADS / N'th
-// row, so one 32-bit offset serves all of them (strides are below 2^24 elements).
+// row, 32-bit offsets apart (strides are at most 2^24 elements).
 // Past `count` tokens and past D channels the last valid ones are read, and zeros
 // are stored.
 template <int D, typename T, int N, int THREADS>
@@ -514,13 +514,8 @@ struct Rows {
     const uint8_t* base = reinterpret_cast<const uint8_t*>(x);
     const int unit = min(u0 + tid % N, D / 8 - 1);
     const uint32_t s = static_cast<uint32_t>(stride) * 2;
-    if (count == C) {
-      const uint32_t off = tid / N * s + unit * 16;
-      for (int j = 0; j < L; ++j) raw[j] = *reinterpret_cast<const u32x4*>(base + static_cast<uint64_t>(s) * (j * STEP) + off);
-    } else {
-      for (int j = 0; j < L; ++j)
-        raw[j] = *reinterpret_cast<const u32x4*>(base + (min(tid / N + j * STEP, count - 1) * s + unit * 16));
-    }
+    for (int j = 0; j < L; ++j)
+      raw[j] = *reinterpret_cast<const u32x4*>(base + (min(tid / N + j * STEP, count - 1) * s + unit * 16));
   }
   // SPLIT: in two bfloat16 parts, the second S::MAT bytes after the first.
   template <bool SPLIT>
@@ -812,9 +807,9 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
     kt.end();
     qt.end();
     vt.end();
+    Rows<D, T, VU, 64 * NW> vr;
     {
       Rows<D, T, S::CPR, 64 * NW> kr, qr;
-      Rows<D, T, VU, 64 * NW> vr;
       const int t = fresh(tid);
       kr.load(k + t0 * p.k_stride, p.k_stride, count, 0, t);
       qr.load(q + t0 * p.q_stride, p.q_stride, count, 0, t);
@@ -822,7 +817,6 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       __syncthreads();
       kr.template store<NP == 2>(lk, count, 0, t);
       qr.template store<NP == 2>(lq, count, 0, t);
-      vr.template store<false>(lv, count, part * VU, t);
     }
     if constexpr (FUSED) {
       const bool next = more && wave == NW - 1;
@@ -878,7 +872,8 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       in_order();
     }
     }
-    if constexpr (FUSED) __syncthreads();     // A and the system for U
+    vr.template store<false>(lv, count, part * VU, fresh(tid));
+    __syncthreads();      // V, A and the system for U
     Parts<2> uf[NCT][2];
     {
       const int l = fresh(lane), g = l >> 4;
@@ -897,10 +892,12 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
         for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(u[n][0], none), u[n][1]);
         for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(none, u[n][1]), none);
         for (int n = 0; n < NCT; ++n) uf[n][0] = parts_of<2>(u[n][0], u[n][1]);
+        in_order();
         s = stored_parts(lt, lt + kTri, tri(2, 0), l);
         for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, uf[n][0], u[n][2]);
         s = stored_parts(lt, lt + kTri, tri(3, 0), l);
         for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, uf[n][0], u[n][3]);
+        in_order();
         s = stored_parts(lt, lt + kTri, tri(2, 1), l);
         for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, parts_of<2>(u[n][2], none), none);
         s = stored_parts(lt, lt + kTri, tri(3, 1), l);
@@ -922,6 +919,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
           const Parts<2> a = stored_parts(la, la + kTri, tri(i, tb), l);
           for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
         }
+        if (i & 1) in_order();
       }
       settle();
       for (int i = 0; i < 4; ++i) {
@@ -934,6 +932,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
           }
       }
     }
+    in_order();
     in_order();
     const int l = fresh(lane), g = l >> 4;
     const At at = lane_at<S::RB>(l);
