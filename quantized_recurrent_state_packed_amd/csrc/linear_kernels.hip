@@ -393,12 +393,30 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
 __device__ __forceinline__ bf16x4 rounded(const f32x4& x) { return __builtin_convertvector(x, bf16x4); }
 __device__ __forceinline__ f32x4 widened(const bf16x4& x) { return __builtin_convertvector(x, f32x4); }
 
+// x - hi, where hi is x rounded: a dot product of a pair of hi with (-1, 0) or (0, -1)
+// takes one instruction a value, with no unpacking.  All of its terms are exact.
+// The factors are kept in registers: as an operand of this instruction the constant
+// -1.0 does not mean the pair (-1, 0) that the compiler writes it for.
+__device__ __forceinline__ f32x4 rest_of(const f32x4& x, const bf16x4& hi) {
+  typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  uint32_t f = 0x0000bf80u, s = 0xbf800000u;
+  asm("" : "+s"(f), "+s"(s));
+  const bf16x2 first = __builtin_bit_cast(bf16x2, f), second = __builtin_bit_cast(bf16x2, s);
+  f32x4 r;
+  for (int i = 0; i < 4; i += 2) {
+    const bf16x2 h = {hi[i], hi[i + 1]};
+    r[i] = __builtin_amdgcn_fdot2_f32_bf16(h, first, x[i], false);
+    r[i + 1] = __builtin_amdgcn_fdot2_f32_bf16(h, second, x[i + 1], false);
+  }
+  return r;
+}
+
 template <int NP>
 __device__ __forceinline__ Parts<NP> parts_of(const f32x4& a, const f32x4& b) {
   Parts<NP> r;
   const bf16x4 ah = rounded(a), bh = rounded(b);
   r.p[0] = join(ah, bh);
-  if constexpr (NP == 2) r.p[1] = join(rounded(a - widened(ah)), rounded(b - widened(bh)));
+  if constexpr (NP == 2) r.p[1] = join(rounded(rest_of(a, ah)), rounded(rest_of(b, bh)));
   return r;
 }
 
@@ -440,16 +458,16 @@ constexpr int kTri = 6 * 1024;
 // tile t that a lane's accumulators hold, 4 g + e, are key channels
 // 32 (t / 2) + 8 g + 4 (t % 2) + e, and two tiles are an operand as they stand.
 //
-// Where a lane reads: `row` for row_operand, `col` for column_operand and `val` for
-// value_piece, of tile 0.  Other tiles differ by whole 16 rows and in the bits of
-// the unit, which commute with the permutation.
+// Where a lane reads: `row` for row_operand and `col` for column_operand, of tile 0.
+// Other tiles differ by whole 16 rows and in the bits of the unit, which commute
+// with the permutation.
 struct At {
-  int row, col, val;
+  int row, col;
 };
 template <int RB>
 __device__ __forceinline__ At lane_at(int lane) {
   const int g = lane >> 4, c = lane & 15;
-  return {unit_at<RB>(c, g), unit_at<RB>(4 * g + (c >> 2), c & 3), unit_at<RB>(4 * g + (c >> 2), (c & 3) >> 1) + (c & 1) * 8};
+  return {unit_at<RB>(c, g), unit_at<RB>(4 * g + (c >> 2), c & 3)};
 }
 // Operand whose row lane % 16 is row 16 i + lane % 16 of x, depth 32 kb ..
 template <int RB>
@@ -467,8 +485,9 @@ __device__ __forceinline__ bf16x8 column_operand(const uint8_t* x, int tb, int t
 }
 // Tokens 16 i + 4 g .. + 3 (g = lane / 16) of value column 16 t + lane % 16 of x.
 template <int RB>
-__device__ __forceinline__ s16x4 value_piece(const uint8_t* x, int i, int t, At at) {
-  return read_transposed(x + 16 * i * RB + (at.val ^ (2 * t) << 4));
+__device__ __forceinline__ s16x4 value_piece(const uint8_t* x, int i, int t, int lane) {
+  const int g = lane >> 4, c = lane & 15;
+  return read_transposed(x + 16 * i * RB + (unit_at<RB>(4 * g + (c >> 2), (c & 3) >> 1) ^ (2 * t) << 4) + (c & 1) * 8);
 }
 __device__ __forceinline__ bf16x8 stored_operand(const uint8_t* x, int n, int lane) {
   return *reinterpret_cast<const bf16x8*>(x + n * 1024 + lane * 16);
@@ -481,7 +500,7 @@ __device__ __forceinline__ void store_parts(uint8_t* hi, uint8_t* lo, int n, int
   const int at = n * 1024 + lane * 16 + half * 8;
   const bf16x4 h = rounded(x);
   *reinterpret_cast<bf16x4*>(hi + at) = h;
-  *reinterpret_cast<bf16x4*>(lo + at) = rounded(x - widened(h));
+  *reinterpret_cast<bf16x4*>(lo + at) = rounded(rest_of(x, h));
 }
 // Operand n of a triangle.
 __device__ __forceinline__ Parts<2> stored_parts(const uint8_t* hi, const uint8_t* lo, int n, int lane) {
@@ -504,9 +523,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // row, 32-bit offsets apart (strides are at most 2^24 elements).
 // Past `count` tokens and past D channels the last valid ones are read, and zeros
 // are stored.
-template <int D, typename T, int N, int THREADS>
+template <int D, typename T, int N, int THREADS, int RB = Dims16<D, T>::RB>
 struct Rows {
   using S = Dims16<D, T>;
+  static constexpr int CPR = RB / 16;
   static constexpr int L = C * N / THREADS;
   static constexpr int STEP = THREADS / N;       // a power of two, as N is
   u32x4 raw[L];
@@ -517,16 +537,17 @@ struct Rows {
     for (int j = 0; j < L; ++j)
       raw[j] = *reinterpret_cast<const u32x4*>(base + (min(tid / N + j * STEP, count - 1) * s + unit * 16));
   }
-  // SPLIT: in two bfloat16 parts, the second S::MAT bytes after the first.
+  // Into rows of RB bytes.  SPLIT: in two bfloat16 parts, the second S::MAT bytes after
+  // the first.
   template <bool SPLIT>
-  __device__ __forceinline__ void store(uint8_t* lds, int count, int u0, int tid) {
-    if (count < C || S::CPR * 8 > D)
+  __device__ __forceinline__ void store(uint8_t* lds, int count, int tid) {
+    if (count < C || N * 8 > D)
       for (int j = 0; j < L; ++j)
-        if (tid / N + j * STEP >= count || u0 + tid % N >= D / 8) raw[j] = u32x4{};
-    const int to0 = unit_at<S::RB>(tid / N, u0 + tid % N);
+        if (tid / N + j * STEP >= count || tid % N * 8 >= D) raw[j] = u32x4{};
+    const int to0 = unit_at<RB>(tid / N, tid % N);
     for (int j = 0; j < L; ++j) {
       // tid / N < STEP, so the row's number in the permutation is that of its two parts, joined
-      uint8_t* to = lds + j * STEP * S::RB + (to0 ^ ((j * STEP / (256 / S::RB)) & (S::CPR - 1)) << 4);
+      uint8_t* to = lds + j * STEP * RB + (to0 ^ ((j * STEP / (256 / RB)) & (CPR - 1)) << 4);
       if constexpr (SPLIT) {
         typedef f16 f16x8 __attribute__((ext_vector_type(8)));
         typedef float f32x8 __attribute__((ext_vector_type(8)));
@@ -593,120 +614,120 @@ struct Scratch {
   float diag[4][16 * 20];
 };
 
-// The ten blocks (i, j), j <= i < 4, of a chunk's lower triangles, dealt out to four
-// waves; a wave's first is the diagonal one of its number.
-constexpr int kTiles = 3;
-__device__ __forceinline__ int tile_of(int wave, int n) {      // 4 i + j, or -1
-  switch (n) {
-    case 0: return 5 * wave;                                              // (w, w)
-    case 1: return wave == 0 ? 12 : wave == 1 ? 4 : wave == 2 ? 9 : 14;   // (3,0) (1,0) (2,1) (3,2)
-    default: return wave == 0 ? 8 : wave == 1 ? 13 : -1;                  // (2,0) (3,1)
-  }
-}
-
-// Wave `wave` of four: its blocks of A and of the system for U into LDS, both as
-// operands in two parts (`lt`, `la`: the larger, then the smaller ones).  With
+// Block (i, j) of A and of the system for U into LDS, one wave, both as operands in
+// two parts (`lt`, `la`: the larger, then the smaller ones).  With
 // B = diag(b) B', U comes from block rows of 16 tokens in turn,
 //   U_i = D_i (R_i - sum_{j < i} B'_ij U_j),  D_i = (I + B_ii)^-1 diag(b_i),
 // so the system is stored as -B'_ij below the diagonal and D_i on it.  The inverse
 // is found by forward substitution, a column for every lane of 16 (four times over).
-template <int D, typename T, bool DELTA>
-__device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq, const Rates& r, Scratch* sc,
-                                            uint8_t* la, uint8_t* lt, int wave, int lane) {
+template <int D, typename T, bool DELTA, bool DIAGONAL>
+__device__ __forceinline__ void chunk_tile(const uint8_t* lk, const uint8_t* lq, const Rates& r, Scratch* sc,
+                                           uint8_t* la, uint8_t* lt, int i, int j, int lane) {
   using S = Dims16<D, T>;
   const At at = lane_at<S::RB>(lane);
   const int g = lane >> 4, c = lane & 15;
-  for (int n = 0; n < kTiles; ++n) {
-    const int tile = tile_of(wave, n);
-    if (tile < 0) break;
-    const int i = tile >> 2, j = tile & 3;
-    // rows: key token 16 j + 4 g + e, column: token 16 i + c
-    f32x4 kk = {}, qk = {};
-    for (int kb = 0; kb < S::KB; ++kb) {
-      Parts<S::NP> ki, qi, kj;
-      for (int x = 0; x < S::NP; ++x) {
-        kj.p[x] = row_operand<S::RB>(lk + x * S::MAT, j, kb, at);
-        qi.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
-        if constexpr (DELTA) ki.p[x] = n == 0 ? kj.p[x] : row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
-      }
-      qk = mma<true>(kj, qi, qk);
-      if constexpr (DELTA) kk = mma<true>(kj, ki, kk);
+  // rows: key token 16 j + 4 g + e, column: token 16 i + c
+  f32x4 kk = {}, qk = {};
+  for (int kb = 0; kb < S::KB; ++kb) {
+    Parts<S::NP> ki, qi, kj;
+    for (int x = 0; x < S::NP; ++x) {
+      kj.p[x] = row_operand<S::RB>(lk + x * S::MAT, j, kb, at);
+      qi.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
+      if constexpr (DELTA) ki.p[x] = DIAGONAL ? kj.p[x] : row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
     }
-    settle();
-    const double li = r.lg[16 * i + c];
-    f32x4 ratio;
-    for (int e = 0; e < 4; ++e) {
-      const float x = __builtin_amdgcn_exp2f(static_cast<float>(li - r.lg[16 * j + 4 * g + e]));
-      ratio[e] = n > 0 || 4 * g + e <= c ? x : 0.0f;
-    }
-    const int to = tri(i, j >> 1);
-    store_parts(la, la + kTri, to, j & 1, qk * ratio, lane);
-    if constexpr (DELTA) {
-      if (n > 0) {
-        store_parts(lt, lt + kTri, to, j & 1, -kk * ratio, lane);
-      } else {
-        // the wave's own LDS accesses are in order; of B only what is below the diagonal is read
-        float* d = sc->diag[wave];
-        *reinterpret_cast<f32x4*>(d + c * 20 + 4 * g) = kk * ratio * r.beta[16 * i + c];
-        wave_order();
-        float x[16];
-        for (int q = 0; q < 4; ++q) {
-          f32x4 row[4][4];
-          for (int ii = 0; ii < 4; ++ii)
-            for (int b = 0; b <= q; ++b) row[ii][b] = *reinterpret_cast<const f32x4*>(d + (4 * q + ii) * 20 + 4 * b);
-          for (int ii = 0; ii < 4; ++ii) {
-            float s = 4 * q + ii == c ? 1.0f : 0.0f;
-            for (int jj = 0; jj < 4 * q + ii; ++jj) s = fmaf(-row[ii][jj >> 2][jj & 3], x[jj], s);
-            x[4 * q + ii] = s;
-          }
-          in_order();
-        }
-        wave_order();
-        if (g == 0)
-          for (int ii = 0; ii < 16; ++ii) d[ii * 20 + c] = x[ii];
-        wave_order();
-        const f32x4 inv = *reinterpret_cast<const f32x4*>(d + c * 20 + 4 * g) *
-                          *reinterpret_cast<const f32x4*>(&r.beta[16 * i + 4 * g]);
-        store_parts(lt, lt + kTri, to, j & 1, inv, lane);
-      }
-    }
-    in_order();
+    qk = mma<true>(kj, qi, qk);
+    if constexpr (DELTA) kk = mma<true>(kj, ki, kk);
   }
-  if ((wave & 1) == 0) {      // beside the diagonal
-    store_parts(la, la + kTri, tri(wave, wave >> 1), 1, f32x4{}, lane);
-    if constexpr (DELTA) store_parts(lt, lt + kTri, tri(wave, wave >> 1), 1, f32x4{}, lane);
+  settle();
+  const double li = r.lg[16 * i + c];
+  f32x4 ratio;
+  for (int e = 0; e < 4; ++e) {
+    const float x = __builtin_amdgcn_exp2f(static_cast<float>(li - r.lg[16 * j + 4 * g + e]));
+    ratio[e] = !DIAGONAL || 4 * g + e <= c ? x : 0.0f;
+  }
+  const int to = tri(i, j >> 1);
+  store_parts(la, la + kTri, to, j & 1, qk * ratio, lane);
+  if constexpr (DELTA && !DIAGONAL) {
+    store_parts(lt, lt + kTri, to, j & 1, -kk * ratio, lane);
+  } else if constexpr (DELTA) {
+    // the wave's own LDS accesses are in order; of B only what is below the diagonal is read
+    float* d = sc->diag[i];
+    *reinterpret_cast<f32x4*>(d + c * 20 + 4 * g) = kk * ratio * r.beta[16 * i + c];
+    wave_order();
+    float x[16];
+    for (int q = 0; q < 8; ++q) {      // two rows at a time: registers
+      f32x4 row[2][4];
+      for (int ii = 0; ii < 2; ++ii)
+        for (int b = 0; b <= q / 2; ++b) row[ii][b] = *reinterpret_cast<const f32x4*>(d + (2 * q + ii) * 20 + 4 * b);
+      for (int ii = 0; ii < 2; ++ii) {
+        float s = 2 * q + ii == c ? 1.0f : 0.0f;
+        for (int jj = 0; jj < 2 * q + ii; ++jj) s = fmaf(-row[ii][jj >> 2][jj & 3], x[jj], s);
+        x[2 * q + ii] = s;
+      }
+      in_order();
+    }
+    wave_order();
+    if (g == 0)
+      for (int ii = 0; ii < 16; ++ii) d[ii * 20 + c] = x[ii];
+    wave_order();
+    const f32x4 inv = *reinterpret_cast<const f32x4*>(d + c * 20 + 4 * g) *
+                      *reinterpret_cast<const f32x4*>(&r.beta[16 * i + 4 * g]);
+    store_parts(lt, lt + kTri, to, j & 1, inv, lane);
+  }
+  if (DIAGONAL && (i & 1) == 0) {      // beside the diagonal
+    store_parts(la, la + kTri, to, 1, f32x4{}, lane);
+    if constexpr (DELTA) store_parts(lt, lt + kTri, to, 1, f32x4{}, lane);
+  }
+  in_order();
+}
+
+// The ten blocks (i, j), j <= i < 4, of a chunk's lower triangles, dealt out to the
+// waves of a workgroup.
+template <int D, typename T, bool DELTA, int NW>
+__device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq, const Rates& r, Scratch* sc,
+                                            uint8_t* la, uint8_t* lt, int wave, int lane) {
+  static_assert(NW == 4 || NW == 8, "four or eight waves");
+  if (wave < 4) chunk_tile<D, T, DELTA, true>(lk, lq, r, sc, la, lt, wave, wave, lane);
+  const int w = NW == 8 ? wave - 4 : wave;
+  if (w >= 0) {
+    const int i = w == 0 ? 3 : w == 1 ? 1 : w == 2 ? 2 : 3, j = w == 0 ? 0 : w == 1 ? 0 : w == 2 ? 1 : 2;
+    chunk_tile<D, T, DELTA, false>(lk, lq, r, sc, la, lt, i, j, lane);
+    if (w < 2) chunk_tile<D, T, DELTA, false>(lk, lq, r, sc, la, lt, w == 0 ? 2 : 3, w, lane);
   }
 }
 
 // A (chunk, head) of the workspace of 16-bit inputs: G, G_C / G, A, the system for U.
-__device__ __forceinline__ uint8_t* chunk_ws16(uint8_t* ws, int64_t index, bool delta) {
-  return ws + index * (2 * C * 4 + 2 * kTri + (delta ? 2 * kTri : 0));
-}
+constexpr int block_bytes(bool delta) { return 2 * C * 4 + (delta ? 4 : 2) * kTri; }
 
-template <int D, typename T, bool DELTA>
+// LDS.  FUSED: `rates` for this chunk and the next one; HEAD: G, G_C / G, A and the
+// system lie as they do in the workspace.  For bfloat16 at D = 128 two FUSED
+// workgroups fit a compute unit with nothing to spare.
+template <int D, typename T, bool DELTA, int COLS, bool FUSED, bool HEAD = !FUSED>
 struct Lds16 {
   using S = Dims16<D, T>;
+  static constexpr int RBV = 2 * COLS < 64 ? 64 : 2 * COLS;      // bytes of a row of v
   static constexpr int K = 0;
   static constexpr int Q = K + S::NP * S::MAT;
   static constexpr int V = Q + S::NP * S::MAT;
-  static constexpr int A = V + S::MAT;
-  static constexpr int RATES = A + 2 * kTri;                           // this chunk's and the next one's
-  static constexpr int TT = RATES + 2 * static_cast<int>(sizeof(Rates));
-  static constexpr int SCRATCH = TT + (DELTA ? 2 * kTri : 0);
-  static constexpr int FUSED = SCRATCH + (DELTA ? static_cast<int>(sizeof(Scratch)) : 0);
-  static constexpr int SPLIT = SCRATCH;
+  static constexpr int BLOCK = V + C * RBV;
+  static constexpr int A = BLOCK + (HEAD ? 2 * C * 4 : 0);
+  static constexpr int TT = A + 2 * kTri;
+  static constexpr int RATES = TT + (DELTA ? 2 * kTri : 0);
+  static constexpr int SCRATCH = RATES + 2 * static_cast<int>(sizeof(Rates));
+  static constexpr int BYTES = FUSED ? SCRATCH + (DELTA ? static_cast<int>(sizeof(Scratch)) : 0) : RATES;
 };
 
 // The chunk matrices of every (chunk, head), for k_linear16_walk<.., false>.
 template <int D, typename T, bool DELTA>
 __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
   using S = Dims16<D, T>;
-  using L = Lds16<D, T, DELTA>;
+  using L = Lds16<D, T, DELTA, D, true, true>;
   extern __shared__ __align__(16) uint8_t lds16[];
   Rates& rates = *reinterpret_cast<Rates*>(lds16 + L::RATES);
   Scratch* sc = reinterpret_cast<Scratch*>(lds16 + L::SCRATCH);
-  const int h = blockIdx.x % p.H;
-  const int64_t w = blockIdx.x / p.H;
+  const uint32_t block = die_order(blockIdx.x, gridDim.x, p.rep);
+  const int h = block % p.H;
+  const int64_t w = block / p.H;
   int b = 0;     // the last request with cu[b] / C + b <= w
   for (int lo = 0, hi = p.batch - 1; lo <= hi;) {
     const int mid = (lo + hi) / 2;
@@ -728,30 +749,51 @@ __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
     const int64_t at = (first + min(lane, count - 1)) * p.H + h;
     set_rates(rates, p.gate[at], DELTA ? p.beta[at] : 0.0f, count, lane);
   }
-  kr.template store<S::NP == 2>(lds16 + L::K, count, 0, tid);
-  qr.template store<S::NP == 2>(lds16 + L::Q, count, 0, tid);
+  kr.template store<S::NP == 2>(lds16 + L::K, count, tid);
+  qr.template store<S::NP == 2>(lds16 + L::Q, count, tid);
   __syncthreads();
-  chunk_tiles<D, T, DELTA>(lds16 + L::K, lds16 + L::Q, rates, sc, lds16 + L::A, lds16 + L::TT, wave, lane);
+  chunk_tiles<D, T, DELTA, 4>(lds16 + L::K, lds16 + L::Q, rates, sc, lds16 + L::A, lds16 + L::TT, wave, lane);
   __syncthreads();
-  uint8_t* ws = chunk_ws16(p.workspace, w * p.H + h, DELTA);
-  if (tid < 2 * C) reinterpret_cast<float*>(ws)[tid] = (tid < C ? rates.grow : rates.left)[tid % C];
-  ws += 2 * C * 4;
-  for (int i = tid * 16; i < 2 * kTri; i += kThreads * 16)
-    *reinterpret_cast<u32x4*>(ws + i) = *reinterpret_cast<const u32x4*>(lds16 + L::A + i);
-  if constexpr (DELTA)
-    for (int i = tid * 16; i < 2 * kTri; i += kThreads * 16)
-      *reinterpret_cast<u32x4*>(ws + 2 * kTri + i) = *reinterpret_cast<const u32x4*>(lds16 + L::TT + i);
+  if (tid < 2 * C) reinterpret_cast<float*>(lds16 + L::BLOCK)[tid] = (tid < C ? rates.grow : rates.left)[tid % C];
+  __syncthreads();
+  uint8_t* ws = p.workspace + (w * p.H + h) * block_bytes(DELTA);
+  for (int i = tid * 16; i < block_bytes(DELTA); i += kThreads * 16)
+    *reinterpret_cast<u32x4*>(ws + i) = *reinterpret_cast<const u32x4*>(lds16 + L::BLOCK + i);
+}
+
+// Workgroups are dealt out to the chip's 8 dies in turn, each with an L2 of its own.
+// Those that read the same q and k (`n` of them: value heads of a key head, column
+// parts of a head) are numbered 8 apart, so that they meet in one.
+__device__ __forceinline__ uint32_t die_order(uint32_t block, uint32_t total, uint32_t n) {
+  const uint32_t set = 8 * n, whole = total / set * set, w = block % set;
+  return block < whole ? block - w + (w % 8) * n + w / 8 : block;
+}
+
+// The request that comes `nth` by length, longest first, among up to 64 (beyond
+// that, where a chip full of workgroups evens lengths out by itself, in their own
+// order): 32768 tokens of 16 requests of 500 to 3500 took 0.88 ms in their own order,
+// with long ones starting last, and %LPT% ms so.
+__device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lane) {
+  if (p.batch == 1 || p.batch > 64) return nth;
+  const int n = lane < p.batch ? request_span(p, lane).count : -1;
+  int rank = 0;
+  for (int j = 0; j < p.batch; ++j) {
+    const int m = __builtin_amdgcn_readlane(n, j);
+    rank += m > n || (m == n && j < lane) ? 1 : 0;
+  }
+  return __builtin_ctzll(__ballot(lane < p.batch && rank == nth));
 }
 
 // Walks a request's chunks in order for 16 NCT NW value columns of one head.
 // FUSED: all columns of the head in one workgroup, which computes the chunk
 // matrices itself; otherwise they come from k_linear16_chunks.
 template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED>
-__global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) k_linear16_walk(LinearArgs p) {
+__global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 : 1) k_linear16_walk(LinearArgs p) {
   using S = Dims16<D, T>;
-  using L = Lds16<D, T, DELTA>;
   constexpr int NP = S::NP;
   constexpr int COLS = 16 * NCT * NW;
+  constexpr int THREADS = 64 * NW;
+  using L = Lds16<D, T, DELTA, COLS, FUSED>;
   constexpr int SPLIT = D / COLS;
   extern __shared__ __align__(16) uint8_t lds16[];
   uint8_t* lk = lds16 + L::K;
@@ -762,16 +804,17 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
   Rates* all_rates = reinterpret_cast<Rates*>(lds16 + L::RATES);
   Scratch* sc = reinterpret_cast<Scratch*>(lds16 + L::SCRATCH);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int part = blockIdx.x % SPLIT;
-  const int h = (blockIdx.x / SPLIT) % p.H;
-  const int b = blockIdx.x / (SPLIT * p.H);
+  const uint32_t block = die_order(blockIdx.x, gridDim.x, p.rep * SPLIT);
+  const int part = block % SPLIT;
+  const int h = (block / SPLIT) % p.H;
+  const int b = nth_longest(p, block / (SPLIT * p.H), lane);
   const int ct0 = part * (COLS / 16) + wave * NCT;      // first column tile of the wave
   const Span r = request_span(p, b);
   const int slot = p.slot_ids[b];
   T* o = static_cast<T*>(p.o) + r.first * p.o_stride + h * D;
   if (slot < 0 || slot >= p.num_slots) {
-    for (int t = tid / COLS; t < r.count; t += 64 * NW / COLS > 0 ? 64 * NW / COLS : 1)
-      for (int j = tid % COLS; j < COLS; j += 64 * NW) o[t * p.o_stride + part * COLS + j] = static_cast<T>(__builtin_nanf(""));
+    for (int t = tid / COLS; t < r.count; t += THREADS / COLS > 0 ? THREADS / COLS : 1)
+      for (int j = tid % COLS; j < COLS; j += THREADS) o[t * p.o_stride + part * COLS + j] = static_cast<T>(__builtin_nanf(""));
     return;
   }
   const T* v = static_cast<const T*>(p.v) + r.first * p.v_stride + h * D;
@@ -789,11 +832,28 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
           for (int e = 0; e < 4; ++e) m[n][i][e] = state[at + (32 * (i / 2) + 4 * (i % 2) + e) * D + 16 * n];
   }
 
-  const int64_t base = r.first / C + b;
   constexpr int VU = COLS / 8;      // units of the workgroup's columns
   float gate = 0.0f, beta = 0.0f;
-  Touch<D, T, 64 * NW> kt, qt, vt;
-  if (FUSED && r.count > 0 && wave == NW - 1) {
+  // FUSED: the next chunk's rows are touched while this one is computed.  Otherwise a
+  // wave has registers enough to hold all of the next chunk's data.
+  Touch<D, T, THREADS> kt, qt, vt;
+  Rows<D, T, S::CPR, THREADS> kr, qr;
+  Rows<D, T, VU, THREADS, L::RBV> vr;
+  constexpr int BU = block_bytes(DELTA) / 16, BL = (BU + THREADS - 1) / THREADS;
+  u32x4 br[BL];
+  const uint8_t* ws = p.workspace + ((r.first / C + b) * p.H + h) * block_bytes(DELTA);
+  auto load_rows = [&](int64_t t0) __attribute__((always_inline)) {
+    const int t = fresh(tid), n = static_cast<int>(min(static_cast<int64_t>(C), r.count - t0));
+    kr.load(k + t0 * p.k_stride, p.k_stride, n, 0, t);
+    qr.load(q + t0 * p.q_stride, p.q_stride, n, 0, t);
+    vr.load(v + t0 * p.v_stride, p.v_stride, n, part * VU, t);
+    if constexpr (!FUSED)
+      for (int j = 0; j < BL; ++j)
+        br[j] = *reinterpret_cast<const u32x4*>(ws + t0 / C * p.H * block_bytes(DELTA) + min(t + j * THREADS, BU - 1) * 16);
+  };
+  if (!FUSED && r.count > 0) load_rows(0);
+  constexpr int RATES_WAVE = NW - 2;      // a wave with few blocks sets the next chunk's rates
+  if (FUSED && r.count > 0 && wave == RATES_WAVE) {
     const int64_t token = (r.first + min(lane, r.count - 1)) * p.H + h;
     gate = p.gate[token];
     if constexpr (DELTA) beta = p.beta[token];
@@ -803,51 +863,45 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
     const int count = min(C, r.count - c * C);
     const int64_t t0 = static_cast<int64_t>(c) * C;
     const bool more = t0 + C < r.count;
-    Rates& rates = all_rates[FUSED ? c & 1 : 0];
-    kt.end();
-    qt.end();
-    vt.end();
-    Rows<D, T, VU, 64 * NW> vr;
+    Rates& rates = all_rates[c & 1];
+    const float* grow = FUSED ? rates.grow : reinterpret_cast<const float*>(lds16 + L::BLOCK);
+    const float* left = FUSED ? rates.left : grow + C;
+    if constexpr (FUSED) {
+      kt.end();
+      qt.end();
+      vt.end();
+      load_rows(t0);
+    }
+    __syncthreads();
     {
-      Rows<D, T, S::CPR, 64 * NW> kr, qr;
       const int t = fresh(tid);
-      kr.load(k + t0 * p.k_stride, p.k_stride, count, 0, t);
-      qr.load(q + t0 * p.q_stride, p.q_stride, count, 0, t);
-      vr.load(v + t0 * p.v_stride, p.v_stride, count, part * VU, t);
-      __syncthreads();
-      kr.template store<NP == 2>(lk, count, 0, t);
-      qr.template store<NP == 2>(lq, count, 0, t);
+      kr.template store<NP == 2>(lk, count, t);
+      qr.template store<NP == 2>(lq, count, t);
+      if constexpr (!FUSED) {
+        vr.template store<false>(lv, count, t);
+        for (int j = 0; j < BL; ++j)
+          if (t + j * THREADS < BU) *reinterpret_cast<u32x4*>(lds16 + L::BLOCK + (t + j * THREADS) * 16) = br[j];
+      }
     }
     if constexpr (FUSED) {
-      const bool next = more && wave == NW - 1;
-      if (next) {     // the last wave, which has the fewest blocks, sets the next chunk's rates
+      const bool next = more && wave == RATES_WAVE;
+      if (next) {
         const int64_t token = (r.first + t0 + C + min(lane, r.count - (c + 1) * C - 1)) * p.H + h;
         gate = p.gate[token];
         if constexpr (DELTA) beta = p.beta[token];
       }
       __syncthreads();
-      chunk_tiles<D, T, DELTA>(lk, lq, rates, sc, la, lt, wave, fresh(lane));
+      chunk_tiles<D, T, DELTA, NW>(lk, lq, rates, sc, la, lt, wave, fresh(lane));
       if (next) set_rates(all_rates[(c + 1) & 1], gate, beta, min(C, r.count - (c + 1) * C), lane);
-    } else {
-      const uint8_t* ws = chunk_ws16(p.workspace, (base + c) * p.H + h, DELTA);
-      for (int i = tid; i < C; i += 64 * NW) {
-        rates.grow[i] = reinterpret_cast<const float*>(ws)[i];
-        rates.left[i] = reinterpret_cast<const float*>(ws)[C + i];
+      if (more) {
+        const int t = fresh(tid), n = min(C, r.count - (c + 1) * C);
+        kt.start(k + (t0 + C) * p.k_stride, p.k_stride, n, t);
+        qt.start(q + (t0 + C) * p.q_stride, p.q_stride, n, t);
+        vt.start(v + (t0 + C) * p.v_stride, p.v_stride, n, t);
       }
-      ws += 2 * C * 4;
-      for (int i = tid * 16; i < 2 * kTri; i += 64 * NW * 16)
-        *reinterpret_cast<u32x4*>(la + i) = *reinterpret_cast<const u32x4*>(ws + i);
-      if constexpr (DELTA)
-        for (int i = tid * 16; i < 2 * kTri; i += 64 * NW * 16)
-          *reinterpret_cast<u32x4*>(lt + i) = *reinterpret_cast<const u32x4*>(ws + 2 * kTri + i);
+    } else {
       __syncthreads();
-    }
-
-    if (more) {
-      const int t = fresh(tid), n = min(C, r.count - (c + 1) * C);
-      kt.start(k + (t0 + C) * p.k_stride, p.k_stride, n, t);
-      qt.start(q + (t0 + C) * p.q_stride, p.q_stride, n, t);
-      vt.start(v + (t0 + C) * p.v_stride, p.v_stride, n, t);
+      if (more) load_rows(t0 + C);
     }
 
     // K M and (transposed: rows value columns, columns tokens, so that a lane stores
@@ -872,16 +926,18 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       in_order();
     }
     }
-    vr.template store<false>(lv, count, part * VU, fresh(tid));
-    __syncthreads();      // V, A and the system for U
+    settle();
+    if constexpr (FUSED) {
+      vr.template store<false>(lv, count, fresh(tid));
+      __syncthreads();      // V, A and the system for U
+    }
     Parts<2> uf[NCT][2];
     {
       const int l = fresh(lane), g = l >> 4;
-      const At at = lane_at<S::RB>(l);
       for (int n = 0; n < NCT; ++n)
         for (int i = 0; i < 4; ++i) {
-          const f32x4 x = floats_of(value_piece<S::RB>(lv, i, ct0 + n, at), T{});
-          if constexpr (DELTA) u[n][i] = x - *reinterpret_cast<const f32x4*>(&rates.grow[16 * i + 4 * g]) * u[n][i];
+          const f32x4 x = floats_of(value_piece<L::RBV>(lv, i, wave * NCT + n, l), T{});
+          if constexpr (DELTA) u[n][i] = x - *reinterpret_cast<const f32x4*>(&grow[16 * i + 4 * g]) * u[n][i];
           else u[n][i] = x;
         }
       const f32x4 none = {};
@@ -913,8 +969,8 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
     {
       const int l = fresh(lane), g = l >> 4, cl = l & 15;
       for (int i = 0; i < 4; ++i) {
-        const float grow = rates.grow[16 * i + cl];
-        for (int n = 0; n < NCT; ++n) y[n][i] *= grow;
+        const float f = grow[16 * i + cl];
+        for (int n = 0; n < NCT; ++n) y[n][i] *= f;
         for (int tb = 0; tb <= i / 2; ++tb) {
           const Parts<2> a = stored_parts(la, la + kTri, tri(i, tb), l);
           for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
@@ -933,15 +989,14 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? 2 : 1) 
       }
     }
     in_order();
-    in_order();
     const int l = fresh(lane), g = l >> 4;
     const At at = lane_at<S::RB>(l);
     Parts<2> wf[NCT][2];
-    const float all = rates.grow[C - 1];
+    const float all = grow[C - 1];
     for (int n = 0; n < NCT; ++n)
       for (int tb = 0; tb < 2; ++tb)
-        wf[n][tb] = parts_of<2>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&rates.left[32 * tb + 4 * g]),
-                                u[n][2 * tb + 1] * *reinterpret_cast<const f32x4*>(&rates.left[32 * tb + 16 + 4 * g]));
+        wf[n][tb] = parts_of<2>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 4 * g]),
+                                u[n][2 * tb + 1] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 16 + 4 * g]));
     for (int i = 0; i < S::RT; ++i) {
       for (int n = 0; n < NCT; ++n) m[n][i] *= all;
       for (int tb = 0; tb < 2; ++tb) {
@@ -1057,19 +1112,26 @@ hipError_t launch_lds(K* kern, int64_t grid, int threads, int lds, const LinearA
   return hipGetLastError();
 }
 
+template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED>
+hipError_t walk16(const LinearArgs& a, hipStream_t s) {
+  constexpr int COLS = 16 * NCT * NW;
+  return launch_lds(k_linear16_walk<D, T, DELTA, NCT, NW, FUSED>, static_cast<int64_t>(a.batch) * a.H * (D / COLS), 64 * NW,
+                    Lds16<D, T, DELTA, COLS, FUSED>::BYTES, a, s);
+}
+
 template <int D, typename T, bool DELTA>
 hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
-  using L = Lds16<D, T, DELTA>;
   const int64_t tiles = static_cast<int64_t>(a.batch) * a.H;
   if constexpr (D >= 64) {
-    if (tiles >= 256)
-      return launch_lds(k_linear16_walk<D, T, DELTA, D / 64, 4, true>, tiles, 256, L::FUSED, a, s);
+    if (tiles >= 256) return walk16<D, T, DELTA, DELTA ? D / 64 : 1, DELTA ? 4 : D / 16, true>(a, s);
   }
-  const int64_t chunks = max_chunks(a.total_tokens, a.batch);
-  const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, chunks * a.H, kThreads, L::FUSED, a, s);
+  const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, max_chunks(a.total_tokens, a.batch) * a.H, kThreads,
+                                  Lds16<D, T, DELTA, D, true, true>::BYTES, a, s);
   if (e != hipSuccess) return e;
-  constexpr int NW = D >= 64 ? 2 : 1;
-  return launch_lds(k_linear16_walk<D, T, DELTA, 1, NW, false>, tiles * (D / (16 * NW)), 64 * NW, L::SPLIT, a, s);
+  if constexpr (D >= 32) {
+    if (tiles * (D / 32) >= 256) return walk16<D, T, DELTA, 1, 2, false>(a, s);
+  }
+  return walk16<D, T, DELTA, 1, 1, false>(a, s);
 }
 
 template <int D, typename T>
@@ -1110,7 +1172,7 @@ hipError_t step_t(int d, const LinearArgs& a, hipStream_t s) {
 size_t chunk_bytes(int rule, int dtype) {
   const bool delta = rule == STEPQ_RULE_DELTA;
   if (dtype == STEPQ_F32) return sizeof(float) * ((delta ? 2 : 1) * C * C + 2 * C);
-  return 2 * C * sizeof(float) + (delta ? 4 : 2) * kTri;
+  return block_bytes(delta);
 }
 
 hipError_t launch_linear_prefill(const stepq_linear_desc& d, const LinearArgs& a, hipStream_t s) {
