@@ -54,15 +54,28 @@ __device__ __forceinline__ void insert(List& l, float x, int32_t i, int lane) {
   }
 }
 
-// Offers every lane's (x, i) to the list, which keeps `n` entries that matter.
-__device__ __forceinline__ void offer(List& l, float x, int32_t i, int n, int lane) {
-  uint64_t m = __ballot(better(x, i, lane_value(l.x, n - 1), __builtin_amdgcn_readlane(l.i, n - 1)));
+// Offers every lane's (x, i), x >= floor, to the list, which keeps `n` entries that matter.
+__device__ __forceinline__ void offer(List& l, float x, int32_t i, float floor, int n, int lane) {
+  uint64_t m = __ballot(x >= floor && better(x, i, lane_value(l.x, n - 1), __builtin_amdgcn_readlane(l.i, n - 1)));
   while (m) {
     const int from = __builtin_ctzll(m);
     insert(l, lane_value(x, from), __builtin_amdgcn_readlane(i, from), lane);
     m &= m - 1;
     m &= __ballot(better(x, i, lane_value(l.x, n - 1), __builtin_amdgcn_readlane(l.i, n - 1)));
   }
+}
+
+// The n-th largest of the lanes' x, found bit by bit in the order of floats as
+// integers.  Whatever is below it is not among the n largest of a set that x is part
+// of: an empty list filled without it would take n (1 + ln(m / n)) insertions from m
+// candidates, with it a few more than n.
+__device__ __forceinline__ float nth_largest(float x, int n) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const uint32_t key = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  uint32_t t = 0;
+  for (uint32_t bit = 0x80000000u; bit; bit >>= 1)
+    if (__popcll(__ballot(key >= (t | bit))) >= n) t |= bit;
+  return __builtin_bit_cast(float, t ^ (t >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
 // exp(x - m) for x <= m; 1 where both are the same infinity.
@@ -129,19 +142,28 @@ __global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
         } else {
           for (int i = 0; i < V; ++i) z[i] = at + i >= 0 && at + i < p.vocab ? L::one(x + at + i) : -kInf;
         }
-        for (int i = 0; i < V; ++i) y[e + i] = fmaxf(z[i], -kInf);   // NaN: banned
+        for (int i = 0; i < V; ++i) y[e + i] = z[i];
       }
-      float top = y[0];
+      float top = fmaxf(y[0], -kInf);             // not NaN
       for (int e = 1; e < kPer; ++e) top = fmaxf(top, y[e]);
-      if (top > -kInf) {
-        const float now = fmaxf(m, top);
-        sum *= exp_below(m, now);
-        for (int e = 0; e < kPer; ++e) sum += exp_below(y[e], now);
-        m = now;
+      float now = fmaxf(m, top), add = 0.0f;
+      const float from = now > -kInf ? now : 0.0f;
+      for (int e = 0; e < kPer; ++e) add += __builtin_amdgcn_exp2f((y[e] - from) * kLog2e);
+      if (__ballot(!(add < kInf))) {              // a NaN, or an infinity, among the logits
+        add = 0.0f;
+        for (int e = 0; e < kPer; ++e) {
+          y[e] = fmaxf(y[e], -kInf);
+          add += y[e] > -kInf ? exp_below(y[e], now) : 0.0f;
+        }
       }
+      sum = (now > -kInf ? sum * exp_below(m, now) : 0.0f) + add;
+      m = now;
       // tiles come in ascending order, so a tie with an entry of an earlier tile is lost
-      if (__ballot(top > lane_value(list.x, p.num_out - 1)))
-        for (int e = 0; e < kPer; ++e) offer(list, y[e], base + (e / V) * V * 64 + lane * V + e % V, p.num_out, lane);
+      if (__ballot(top > lane_value(list.x, p.num_out - 1))) {
+        const float floor = tile == part * p.tiles ? nth_largest(top, p.num_out) : -kInf;
+        for (int e = 0; e < kPer; ++e)
+          offer(list, y[e], base + (e / V) * V * 64 + lane * V + e % V, floor, p.num_out, lane);
+      }
     }
     for (int s = 1; s < 64; s <<= 1) {
       const float om = __shfl_xor(m, s), os = __shfl_xor(sum, s);
@@ -158,12 +180,15 @@ __global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads) k_select_merge(SelectArgs p) {
+// A wave per beam joins the lists of the beam's parts, all of whose entries are
+// loaded at once, and the first wave orders the beams' candidates.
+__global__ void __launch_bounds__(1024) k_select_merge(SelectArgs p) {
   __shared__ float sx[kMaxBeams][64];
   __shared__ int32_t si[kMaxBeams][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = p.num_out;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = p.num_out;
   const int64_t b = blockIdx.x;
-  for (int beam = wave; beam < p.beams; beam += kWaves) {
+  const size_t part_bytes = select_part_bytes(n);
+  for (int beam = wave; beam < p.beams; beam += static_cast<int>(blockDim.x >> 6)) {
     const int64_t row = b * p.beams + beam;
     const float start = p.scores[row];
     float score = -kInf;
@@ -171,17 +196,38 @@ __global__ void __launch_bounds__(kThreads) k_select_merge(SelectArgs p) {
     if (p.finished != nullptr && p.finished[row] != 0) {
       if (lane == 0) score = start, token = p.eos;
     } else {
-      List list;
+      const uint8_t* in = p.workspace + row * p.parts * part_bytes;
       float m = -kInf, sum = 0.0f;
-      for (int part = 0; part < p.parts; ++part) {
-        const float* in = reinterpret_cast<const float*>(p.workspace + (row * p.parts + part) * select_part_bytes(n));
-        const float om = in[0], os = in[1], now = fmaxf(m, om);
+      if (lane < p.parts) {
+        const float* head = reinterpret_cast<const float*>(in + lane * part_bytes);
+        m = head[0], sum = head[1];
+      }
+      List list;
+      constexpr int kAhead = 4;       // entries a lane loads at a time
+      for (int first = 0; first < p.parts * n; first += 64 * kAhead) {
+        float x[kAhead];
+        int32_t i[kAhead];
+        for (int a = 0; a < kAhead; ++a) {
+          const int at = first + a * 64 + lane, part = at / n;
+          const float* entry = reinterpret_cast<const float*>(in + min(part, p.parts - 1) * part_bytes) + 2 + at % n;
+          x[a] = part < p.parts ? entry[0] : -kInf;
+          i[a] = part < p.parts ? reinterpret_cast<const int32_t*>(entry)[n] : -1;
+        }
+        float floor = -kInf;
+        if (first == 0) {
+          float top = x[0];
+          for (int a = 1; a < kAhead; ++a) top = fmaxf(top, x[a]);
+          floor = nth_largest(top, n);
+        }
+        for (int a = 0; a < kAhead; ++a) offer(list, x[a], i[a], floor, n, lane);
+      }
+      for (int s = 1; s < 64; s <<= 1) {
+        const float om = __shfl_xor(m, s), os = __shfl_xor(sum, s);
+        const float now = fmaxf(m, om);
         if (now > -kInf) sum = sum * exp_below(m, now) + os * exp_below(om, now);
         m = now;
-        const float x = lane < n ? in[2 + lane] : -kInf;
-        const int32_t i = lane < n ? reinterpret_cast<const int32_t*>(in)[2 + n + lane] : -1;
-        offer(list, x, i, n, lane);
       }
+      m = lane_value(m, 0), sum = lane_value(sum, 0);     // the lanes added in different orders
       if (list.x > -kInf) {
         score = start + ((list.x == m ? 0.0f : list.x - m) - logf(sum));
         token = list.i;
@@ -193,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) k_select_merge(SelectArgs p) {
   __syncthreads();
   if (wave != 0) return;
   List best;      // by score, then by place beam * 64 + rank
-  for (int beam = 0; beam < p.beams; ++beam) offer(best, sx[beam][lane], beam * 64 + lane, n, lane);
+  for (int beam = 0; beam < p.beams; ++beam) offer(best, sx[beam][lane], beam * 64 + lane, -kInf, n, lane);
   if (lane < n) {
     const bool some = best.x > -kInf;
     p.tokens[b * n + lane] = some ? si[best.i >> 6][best.i & 63] : -1;
@@ -264,7 +310,8 @@ hipError_t launch_beam_select(const SelectArgs& a, int dtype, hipStream_t s) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_select_merge<<<dim3(static_cast<uint32_t>(a.batch)), kThreads, 0, s>>>(a);
+  const int waves = a.beams < 16 ? a.beams : 16;
+  k_select_merge<<<dim3(static_cast<uint32_t>(a.batch)), 64 * waves, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -717,6 +717,14 @@ struct Lds16 {
   static constexpr int BYTES = FUSED ? SCRATCH + (DELTA ? static_cast<int>(sizeof(Scratch)) : 0) : RATES;
 };
 
+// Workgroups are dealt out to the chip's 8 dies in turn, each with an L2 of its own.
+// Those that read the same q and k (`n` of them: value heads of a key head, column
+// parts of a head) are numbered 8 apart, so that they meet in one.
+__device__ __forceinline__ uint32_t die_order(uint32_t block, uint32_t total, uint32_t n) {
+  const uint32_t set = 8 * n, whole = total / set * set, w = block % set;
+  return block < whole ? block - w + (w % 8) * n + w / 8 : block;
+}
+
 // The chunk matrices of every (chunk, head), for k_linear16_walk<.., false>.
 template <int D, typename T, bool DELTA>
 __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
@@ -759,14 +767,6 @@ __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
   uint8_t* ws = p.workspace + (w * p.H + h) * block_bytes(DELTA);
   for (int i = tid * 16; i < block_bytes(DELTA); i += kThreads * 16)
     *reinterpret_cast<u32x4*>(ws + i) = *reinterpret_cast<const u32x4*>(lds16 + L::BLOCK + i);
-}
-
-// Workgroups are dealt out to the chip's 8 dies in turn, each with an L2 of its own.
-// Those that read the same q and k (`n` of them: value heads of a key head, column
-// parts of a head) are numbered 8 apart, so that they meet in one.
-__device__ __forceinline__ uint32_t die_order(uint32_t block, uint32_t total, uint32_t n) {
-  const uint32_t set = 8 * n, whole = total / set * set, w = block % set;
-  return block < whole ? block - w + (w % 8) * n + w / 8 : block;
 }
 
 // The request that comes `nth` by length, longest first, among up to 64 (beyond
