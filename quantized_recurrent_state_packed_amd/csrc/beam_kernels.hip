@@ -83,100 +83,118 @@ __device__ __forceinline__ float exp_below(float x, float m) {
   return x == m ? 1.0f : __builtin_amdgcn_exp2f((x - m) * kLog2e);
 }
 
-// kVec consecutive logits from a 16-byte boundary, and a single one.
+// kVec consecutive logits from a 16-byte boundary, as they lie in memory.
 template <typename T>
 struct Loader;
 template <>
 struct Loader<float> {
   static constexpr int kVec = 4;
-  static __device__ __forceinline__ void load(const void* p, float (&x)[kVec]) {
-    const f32x4 a = *static_cast<const f32x4*>(p);
-    for (int i = 0; i < 4; ++i) x[i] = a[i];
-  }
-  static __device__ __forceinline__ float one(const void* p) { return *static_cast<const float*>(p); }
+  typedef f32x4 Raw;
+  typedef float One;
+  static constexpr One kNone = -kInf;
+  static __device__ __forceinline__ float value(const Raw& r, int i) { return r[i]; }
 };
 template <>
 struct Loader<__bf16> {
   static constexpr int kVec = 8;
-  static __device__ __forceinline__ void load(const void* p, float (&x)[kVec]) {
-    const u16x8 a = *static_cast<const u16x8*>(p);
-    for (int i = 0; i < 8; ++i) x[i] = __builtin_bit_cast(float, static_cast<uint32_t>(a[i]) << 16);
-  }
-  static __device__ __forceinline__ float one(const void* p) {
-    return __builtin_bit_cast(float, static_cast<uint32_t>(*static_cast<const uint16_t*>(p)) << 16);
+  typedef u16x8 Raw;
+  typedef uint16_t One;
+  static constexpr One kNone = 0xff80;
+  static __device__ __forceinline__ float value(const Raw& r, int i) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(r[i]) << 16);
   }
 };
 template <>
 struct Loader<_Float16> {
   static constexpr int kVec = 8;
-  static __device__ __forceinline__ void load(const void* p, float (&x)[kVec]) {
-    const u16x8 a = *static_cast<const u16x8*>(p);
-    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(a[i])));
+  typedef u16x8 Raw;
+  typedef uint16_t One;
+  static constexpr One kNone = 0xfc00;
+  static __device__ __forceinline__ float value(const Raw& r, int i) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(r[i])));
   }
-  static __device__ __forceinline__ float one(const void* p) { return static_cast<float>(*static_cast<const _Float16*>(p)); }
+};
+
+// A tile of a row, -inf outside of it: a lane holds kVec neighbours from every 64 kVec.
+template <typename T>
+struct Tile {
+  using L = Loader<T>;
+  static constexpr int V = L::kVec;
+  typename L::Raw raw[kPer / V];
+  __device__ __forceinline__ void load(const T* row, int base, int vocab, int lane) {
+    for (int e = 0; e < kPer / V; ++e) {
+      const int at = base + (e * 64 + lane) * V;
+      if (at >= 0 && at + V <= vocab) {
+        raw[e] = *reinterpret_cast<const typename L::Raw*>(row + at);
+      } else {
+        for (int i = 0; i < V; ++i)
+          raw[e][i] = at + i >= 0 && at + i < vocab ? reinterpret_cast<const typename L::One*>(row)[at + i] : L::kNone;
+      }
+    }
+  }
 };
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
   using L = Loader<T>;
   constexpr int V = L::kVec;
-  const int lane = threadIdx.x & 63;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, n = p.num_out;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (unit >= static_cast<int64_t>(p.batch) * p.beams * p.parts) return;
   const int64_t row = unit / p.parts;
   const int part = static_cast<int>(unit % p.parts);
   const T* x = static_cast<const T*>(p.logits) + row * p.stride;
   // tiles begin at the 16-byte boundary at or below the row's start
   const int before = static_cast<int>((reinterpret_cast<uintptr_t>(x) % 16) / sizeof(T));
+  const int tiles = static_cast<int>((static_cast<int64_t>(p.vocab) + before + kTile - 1) / kTile);
+  const int begin = part * p.tiles, end = min(begin + p.tiles, tiles);
   List list;
-  float m = -kInf, sum = 0.0f;
-  if (p.finished == nullptr || p.finished[row] == 0) {
-    for (int tile = part * p.tiles; tile < (part + 1) * p.tiles && static_cast<int64_t>(tile) * kTile < p.vocab + before; ++tile) {
+  float m = -kInf, sum = 0.0f, last = -kInf;     // last: the list's n-th entry
+  if (begin < end && (p.finished == nullptr || p.finished[row] == 0)) {
+    Tile<T> next;
+    next.load(x, begin * kTile - before, p.vocab, lane);
+    for (int tile = begin; tile < end; ++tile) {
       const int base = tile * kTile - before;
+      const Tile<T> now = next;
+      if (tile + 1 < end) next.load(x, base + kTile, p.vocab, lane);
       float y[kPer];
-      for (int e = 0; e < kPer; e += V) {
-        const int at = base + e * 64 + lane * V;
-        float z[V];
-        if (at >= 0 && at + V <= p.vocab) {
-          L::load(x + at, z);
-        } else {
-          for (int i = 0; i < V; ++i) z[i] = at + i >= 0 && at + i < p.vocab ? L::one(x + at + i) : -kInf;
-        }
-        for (int i = 0; i < V; ++i) y[e + i] = z[i];
-      }
+      for (int e = 0; e < kPer; ++e) y[e] = L::value(now.raw[e / V], e % V);
       float top = fmaxf(y[0], -kInf);             // not NaN
       for (int e = 1; e < kPer; ++e) top = fmaxf(top, y[e]);
-      float now = fmaxf(m, top), add = 0.0f;
-      const float from = now > -kInf ? now : 0.0f;
+      const float most = fmaxf(m, top), from = most > -kInf ? most : 0.0f;
+      float add = 0.0f;
       for (int e = 0; e < kPer; ++e) add += __builtin_amdgcn_exp2f((y[e] - from) * kLog2e);
       if (__ballot(!(add < kInf))) {              // a NaN, or an infinity, among the logits
         add = 0.0f;
         for (int e = 0; e < kPer; ++e) {
           y[e] = fmaxf(y[e], -kInf);
-          add += y[e] > -kInf ? exp_below(y[e], now) : 0.0f;
+          add += y[e] > -kInf ? exp_below(y[e], most) : 0.0f;
         }
       }
-      sum = (now > -kInf ? sum * exp_below(m, now) : 0.0f) + add;
-      m = now;
+      sum = (most > -kInf ? sum * exp_below(m, most) : 0.0f) + add;
+      m = most;
       // tiles come in ascending order, so a tie with an entry of an earlier tile is lost
-      if (__ballot(top > lane_value(list.x, p.num_out - 1))) {
-        const float floor = tile == part * p.tiles ? nth_largest(top, p.num_out) : -kInf;
+      if (__ballot(top > last)) {
+        const float floor = tile == begin ? nth_largest(top, n) : last;
         for (int e = 0; e < kPer; ++e)
-          offer(list, y[e], base + (e / V) * V * 64 + lane * V + e % V, floor, p.num_out, lane);
+          if (__ballot(y[e] >= fmaxf(floor, last))) {
+            offer(list, y[e], base + (e / V) * V * 64 + lane * V + e % V, floor, n, lane);
+            last = lane_value(list.x, n - 1);
+          }
       }
     }
     for (int s = 1; s < 64; s <<= 1) {
       const float om = __shfl_xor(m, s), os = __shfl_xor(sum, s);
-      const float now = fmaxf(m, om);
-      if (now > -kInf) sum = sum * exp_below(m, now) + os * exp_below(om, now);
-      m = now;
+      const float most = fmaxf(m, om);
+      if (most > -kInf) sum = sum * exp_below(m, most) + os * exp_below(om, most);
+      m = most;
     }
   }
-  float* out = reinterpret_cast<float*>(p.workspace + unit * select_part_bytes(p.num_out));
+  float* out = reinterpret_cast<float*>(p.workspace + unit * select_part_bytes(n));
   if (lane == 0) out[0] = m, out[1] = sum;
-  if (lane < p.num_out) {
+  if (lane < n) {
     out[2 + lane] = list.x;
-    reinterpret_cast<int32_t*>(out)[2 + p.num_out + lane] = list.i;
+    reinterpret_cast<int32_t*>(out)[2 + n + lane] = list.i;
   }
 }
 
@@ -239,7 +257,10 @@ __global__ void __launch_bounds__(1024) k_select_merge(SelectArgs p) {
   __syncthreads();
   if (wave != 0) return;
   List best;      // by score, then by place beam * 64 + rank
-  for (int beam = 0; beam < p.beams; ++beam) offer(best, sx[beam][lane], beam * 64 + lane, -kInf, n, lane);
+  float top = -kInf;
+  for (int beam = 0; beam < p.beams; ++beam) top = fmaxf(top, sx[beam][lane]);
+  const float floor = nth_largest(top, n);
+  for (int beam = 0; beam < p.beams; ++beam) offer(best, sx[beam][lane], beam * 64 + lane, floor, n, lane);
   if (lane < n) {
     const bool some = best.x > -kInf;
     p.tokens[b * n + lane] = some ? si[best.i >> 6][best.i & 63] : -1;
