@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 
 from . import stepq as _s
-from .linear import check_dense, dtype_code
+from .linear import check_dense, dense, dtype_code, stream_of
 from .stepq import STEPQ_ERR_INVALID_ARG, STEPQ_ERR_UNSUPPORTED, StepqError
 
 EXPORTED = ("stepq_beam_workspace_bytes", "stepq_beam_select", "stepq_beam_reorder")
@@ -62,6 +62,7 @@ class BeamSelect:
             raise StepqError(STEPQ_ERR_UNSUPPORTED, "BeamSelect", "too many rows")
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
+        self._index = self.workspace.get_device()
         self.tokens = torch.empty(self.batch, self.num_out, dtype=torch.int32, device=device)
         self.parents = torch.empty_like(self.tokens)
         self.scores = torch.empty(self.batch, self.num_out, dtype=torch.float32, device=device)
@@ -74,20 +75,22 @@ class BeamSelect:
         rows = self.batch * self.beams
         if _s._checks:
             import torch
-            if not isinstance(logits, torch.Tensor) or logits.device != self.device or logits.dtype != self.dtype:
+            i = self._index
+            if not isinstance(logits, torch.Tensor) or logits.get_device() != i or logits.dtype is not self.dtype:
                 raise StepqError(STEPQ_ERR_INVALID_ARG, where, f"logits must be a {self.dtype} tensor on {self.device}")
             if logits.shape != (rows, self.vocab) or (self.vocab > 1 and logits.stride(1) != 1):
                 raise StepqError(STEPQ_ERR_INVALID_ARG, where, f"logits must be [{rows}, {self.vocab}] with rows in one "
                                  f"piece (got {list(logits.shape)}, strides {list(logits.stride())})")
-            check_dense(where, "scores", scores, (rows,), torch.float32, self.device)
-            if finished is not None:
+            if not dense(scores, torch.float32, (rows,), i) or i < 0:
+                check_dense(where, "scores", scores, (rows,), torch.float32, self.device)
+            if finished is not None and not dense(finished, torch.uint8, (rows,), i):
                 check_dense(where, "finished", finished, (rows,), torch.uint8, self.device)
         stride = logits.stride(0) if rows > 1 else self.vocab      # the only row's stride says nothing
         p = _s._ptr
         _s._check(lib().stepq_beam_select(self.batch, self.beams, self.vocab, self.num_out, p(logits), self._code, stride,
                                           p(scores), p(finished), self.eos_token, p(self.tokens), p(self.parents),
-                                          p(self.scores), p(self.workspace), self.workspace.numel(), _s._stream(stream)),
-                  where)
+                                          p(self.scores), p(self.workspace), self.workspace.numel(),
+                                          stream_of(stream, self._index)), where)
         return self.tokens, self.parents, self.scores
 
 
@@ -108,16 +111,17 @@ def reorder(beams: int, slot_ids, parents, buffers, new_slot_ids, num_slots: int
         raise StepqError(STEPQ_ERR_INVALID_ARG, where, "beams and num_slots must be at least 1")
     if _s._checks:
         import torch
-        dev = slot_ids.device
+        dev, i = slot_ids.device, slot_ids.get_device()
         for name, t in (("slot_ids", slot_ids), ("parents", parents), ("new_slot_ids", new_slot_ids)):
-            check_dense(where, name, t, (n,), torch.int32, dev)
+            if i < 0 or not dense(t, torch.int32, (n,), i):
+                check_dense(where, name, t, (n,), torch.int32, dev)
         if n % beams:
             raise StepqError(STEPQ_ERR_INVALID_ARG, where, f"{n} slots are no whole number of requests of {beams} beams")
         for t in buffers:
-            if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous() or t.nbytes % num_slots:
+            if not isinstance(t, torch.Tensor) or t.get_device() != i or not t.is_contiguous() or t.nbytes % num_slots:
                 raise StepqError(STEPQ_ERR_INVALID_ARG, where,
                                  f"a buffer must be a contiguous tensor on {dev} of {num_slots} equal slots")
     regions = (stepq_region * len(buffers))(*((t.data_ptr(), t.nbytes // num_slots) for t in buffers))
     p = _s._ptr
     _s._check(lib().stepq_beam_reorder(n // beams, int(beams), p(slot_ids), p(parents), int(num_slots), regions, len(buffers),
-                                       p(new_slot_ids), _s._stream(stream)), where)
+                                       p(new_slot_ids), stream_of(stream, slot_ids.get_device())), where)

@@ -57,6 +57,26 @@ def dtype_code(dtype) -> int:
     return codes[dtype]
 
 
+def current_stream(device_index: int) -> int:
+    """The handle of torch's current stream on this device, without building a stream object."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device_index) if raw is not None else torch.cuda.current_stream(device_index).cuda_stream
+
+
+def stream_of(stream, device_index: int) -> int:
+    return current_stream(device_index) if stream is None else _s._stream(stream)
+
+
+def dense(t, dtype, shape, device_index: int) -> bool:
+    """Whether t is a contiguous tensor of this dtype and shape on this GPU (what
+    check_dense explains when it is not)."""
+    try:
+        return t.dtype is dtype and t.shape == shape and t.get_device() == device_index and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
 def _refuse(where: str, detail: str):
     raise StepqError(STEPQ_ERR_INVALID_ARG, where, detail)
 
@@ -96,6 +116,7 @@ class LinearAttention:
         _s._check(lib().stepq_linear_step(self._desc, 0, null, 1, null, 0, null, 0, null, 0, null, null, null, null, 0,
                                           null), "LinearAttention")
         self._qk_row, self._v_row = self.Hk * self.D, self.H * self.D
+        self._state = (self.H, self.D, self.D)
 
     def workspace_bytes(self, batch: int, total_tokens: int) -> int:
         return int(lib().stepq_linear_workspace_bytes(self._desc, int(batch), int(total_tokens)))
@@ -127,17 +148,27 @@ class LinearAttention:
         return n
 
     def _common(self, where, q, k, v, beta, gate, slot_ids, state, o, batch, tokens):
+        """Checks what prompts and tokens have in common; returns the strides of q, k, v and o."""
         import torch
-        dev = state.device if isinstance(state, torch.Tensor) else None
-        check_dense(where, "state", state, (None, self.H, self.D, self.D), torch.float32, dev)
-        check_dense(where, "slot_ids", slot_ids, (batch,), torch.int32, dev)
-        check_dense(where, "gate", gate, (tokens, self.H), torch.float32, dev)
+        f32 = torch.float32
+        i = state.get_device() if isinstance(state, torch.Tensor) else -1
+        dev = state.device if i >= 0 else None
+        per_head = (tokens, self.H)
+        if not (i >= 0 and state.dtype is f32 and state.shape[1:] == self._state and state.is_contiguous()):
+            check_dense(where, "state", state, (None,) + self._state, f32, dev)
+        if not dense(slot_ids, torch.int32, (batch,), i):
+            check_dense(where, "slot_ids", slot_ids, (batch,), torch.int32, dev)
+        if not dense(gate, f32, per_head, i):
+            check_dense(where, "gate", gate, per_head, f32, dev)
         if (beta is None) != (self.rule == "additive"):
             _refuse(where, "beta belongs to the delta rule alone")
-        if beta is not None:
-            check_dense(where, "beta", beta, (tokens, self.H), torch.float32, dev)
-        return (self._strided(where, "q", q, tokens, self.Hk, dev), self._strided(where, "k", k, tokens, self.Hk, dev),
-                self._strided(where, "v", v, tokens, self.H, dev), self._strided(where, "o", o, tokens, self.H, dev))
+        if beta is not None and not dense(beta, f32, per_head, i):
+            check_dense(where, "beta", beta, per_head, f32, dev)
+        qk, vo = (tokens, self.Hk, self.D), (tokens, self.H, self.D)
+        return (self._qk_row if dense(q, self.dtype, qk, i) else self._strided(where, "q", q, tokens, self.Hk, dev),
+                self._qk_row if dense(k, self.dtype, qk, i) else self._strided(where, "k", k, tokens, self.Hk, dev),
+                self._v_row if dense(v, self.dtype, vo, i) else self._strided(where, "v", v, tokens, self.H, dev),
+                self._v_row if dense(o, self.dtype, vo, i) else self._strided(where, "o", o, tokens, self.H, dev))
 
     def _strides(self, *tensors):
         return tuple(t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.D for t in tensors)
@@ -153,10 +184,13 @@ class LinearAttention:
         batch, tokens = slot_ids.shape[0], v.shape[0]
         if _s._checks:
             qs, ks, vs, os_ = self._common(where, q, k, v, beta, gate, slot_ids, state, o, batch, tokens)
-            check_dense(where, "cu_seqlens", cu_seqlens, (batch + 1,), torch.int32, state.device)
-            if resume is not None:
+            i = state.get_device()
+            if not dense(cu_seqlens, torch.int32, (batch + 1,), i):
+                check_dense(where, "cu_seqlens", cu_seqlens, (batch + 1,), torch.int32, state.device)
+            if resume is not None and not dense(resume, torch.uint8, (batch,), i):
                 check_dense(where, "resume", resume, (batch,), torch.uint8, state.device)
-            if workspace is not None:
+            if workspace is not None and not (workspace.dtype is torch.uint8 and workspace.get_device() == i and
+                                              workspace.dim() == 1 and workspace.is_contiguous()):
                 check_dense(where, "workspace", workspace, (None,), torch.uint8, state.device)
         else:
             qs, ks, vs, os_ = self._strides(q, k, v, o)
@@ -174,7 +208,8 @@ class LinearAttention:
         p = _s._ptr
         _s._check(lib().stepq_linear_prefill(self._desc, batch, tokens, p(cu_seqlens), p(q), qs, p(k), ks, p(v), vs,
                                              p(beta), p(gate), p(slot_ids), state.shape[0], p(resume), p(state), p(o),
-                                             os_, p(workspace), workspace.numel(), _s._stream(stream)), where)
+                                             os_, p(workspace), workspace.numel(),
+                                             stream_of(stream, state.get_device())), where)
 
     def step(self, slot_ids, q, k, v, beta, gate, state, o, stream=None) -> None:
         """stepq_linear_step: one token of every request, updating the slots of state."""
@@ -186,4 +221,5 @@ class LinearAttention:
             qs, ks, vs, os_ = self._strides(q, k, v, o)
         p = _s._ptr
         _s._check(lib().stepq_linear_step(self._desc, batch, p(slot_ids), state.shape[0], p(q), qs, p(k), ks, p(v), vs,
-                                          p(beta), p(gate), p(state), p(o), os_, _s._stream(stream)), where)
+                                          p(beta), p(gate), p(state), p(o), os_, stream_of(stream, state.get_device())),
+                  where)
