@@ -46,8 +46,10 @@ extern "C" {
 
 size_t stepq_linear_workspace_bytes(const stepq_linear_desc* d, int32_t batch, int64_t total_tokens) {
   if (check_desc(d) != STEPQ_OK || batch < 0 || total_tokens < 0 || total_tokens > 0x7fffffffLL) return 0;
-  return static_cast<size_t>(stepq::max_chunks(total_tokens, batch)) * d->num_heads *
-         stepq::chunk_bytes(d->rule, d->dtype);
+  const size_t chunks = static_cast<size_t>(stepq::max_chunks(total_tokens, batch)) * d->num_heads *
+                        stepq::chunk_bytes(d->rule, d->dtype);
+  const size_t segments = stepq::segment_workspace_bytes(*d, total_tokens, batch);
+  return chunks > segments ? chunks : segments;
 }
 
 stepq_status stepq_linear_prefill(const stepq_linear_desc* d, int32_t batch, int64_t total_tokens,
@@ -80,6 +82,7 @@ stepq_status stepq_linear_prefill(const stepq_linear_desc* d, int32_t batch, int
   a.total_tokens = total_tokens; a.batch = batch; a.num_slots = num_slots;
   a.H = d->num_heads; a.rep = d->num_heads / d->num_qk_heads;
   a.workspace = static_cast<uint8_t*>(workspace);
+  a.segment = stepq::segment_chunks(*d, total_tokens, batch);
   return from_hip(stepq::launch_linear_prefill(*d, a, static_cast<hipStream_t>(stream)));
 }
 

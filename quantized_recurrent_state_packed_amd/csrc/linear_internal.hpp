@@ -34,6 +34,7 @@ struct LinearArgs {
   int32_t H;
   int32_t rep;                 // value heads per key head
   uint8_t* workspace;
+  int32_t segment;             // prefill: chunks of a segment, 0: none (see segment_chunks)
 };
 
 // Chunks of all requests together: request b's chunks start at index
@@ -41,6 +42,33 @@ struct LinearArgs {
 // + 1 never falls below the ceil((y - x) / 64) chunks of the tokens x .. y-1 by
 // more than what floor(y / 64) makes up for, so ranges do not overlap.
 inline int64_t max_chunks(int64_t total_tokens, int32_t batch) { return total_tokens / kChunk + batch; }
+
+// (request, head) pairs from which one workgroup for each fills the chip.
+constexpr int kFullChip = 256;
+
+// Segments a long prompt of few heads is walked in (additive rule, 16-bit inputs, D >=
+// 64, an average of 512 tokens or more): at least 4 chunks each, and so long that the
+// heads' segments are some 768 workgroups.  The same index rule as for chunks.
+inline int32_t segment_chunks(const stepq_linear_desc& d, int64_t total_tokens, int32_t batch) {
+  if (d.rule != STEPQ_RULE_ADDITIVE || d.dtype == STEPQ_F32 || d.d < 64) return 0;
+  if (static_cast<int64_t>(batch) * d.num_heads >= kFullChip || total_tokens < static_cast<int64_t>(batch) * 512) return 0;
+  const int64_t wanted = (768 + d.num_heads - 1) / d.num_heads, chunks = total_tokens / kChunk;
+  const int64_t n = (chunks + wanted - 1) / wanted;
+  return static_cast<int32_t>(n < 4 ? 4 : n);
+}
+inline int64_t max_segments(int64_t total_tokens, int32_t batch, int32_t segment) {
+  return total_tokens / (static_cast<int64_t>(segment) * kChunk) + batch;
+}
+constexpr int kSegmentHead = 16;   // floats after a segment's state: its retention, and padding
+
+// Workspace bytes for segments of any call of up to these sizes.
+inline size_t segment_workspace_bytes(const stepq_linear_desc& d, int64_t total_tokens, int32_t batch) {
+  if (d.rule != STEPQ_RULE_ADDITIVE || d.dtype == STEPQ_F32 || d.d < 64) return 0;
+  const int64_t wanted = (768 + d.num_heads - 1) / d.num_heads, all = total_tokens / (4 * kChunk);
+  const int64_t few = kFullChip / d.num_heads + 1;
+  const int64_t segments = (all < wanted ? all : wanted) + (batch < few ? batch : few);
+  return static_cast<size_t>(segments) * d.num_heads * (static_cast<size_t>(d.d) * d.d + kSegmentHead) * sizeof(float);
+}
 
 // Workspace bytes of one (chunk, value head).
 size_t chunk_bytes(int rule, int dtype);

@@ -112,6 +112,18 @@ __device__ __forceinline__ Span request_span(const LinearArgs& a, int b) {
   return {lo, static_cast<int32_t>(hi - lo)};
 }
 
+// The request whose range of indices of `tokens`-token pieces holds w: the last b with
+// cu_seqlens[b] / tokens + b <= w.
+__device__ __forceinline__ int owner(const LinearArgs& p, int64_t w, int tokens) {
+  int b = 0;
+  for (int lo = 0, hi = p.batch - 1; lo <= hi;) {
+    const int mid = (lo + hi) / 2;
+    if (request_span(p, mid).first / tokens + mid <= w) b = mid, lo = mid + 1;
+    else hi = mid - 1;
+  }
+  return b;
+}
+
 // One (chunk, head) of the workspace: T and A (row-major C x C), then the
 // retentions G_t and G_C / G_t.
 struct ChunkWs {
@@ -132,16 +144,25 @@ __device__ __forceinline__ ChunkWs chunk_ws(uint8_t* ws, int64_t index, bool del
 
 // Rows first .. first+C-1 of a head of q or k into LDS as floats, zeros past
 // `count` tokens and past D channels.
-template <int D, typename T>
+template <int D, typename T, int THREADS>
 __device__ __forceinline__ void stage(float* lds, const T* x, int64_t stride, int count) {
-  constexpr int DP = Dims<D>::DP, LD = Dims<D>::LD, PR = DP / 8;
-  for (int i = threadIdx.x; i < C * PR; i += blockDim.x) {
-    const int row = i / PR, col = (i % PR) * 8;
-    float x8[8] = {};
-    if (row < count && col < D) load8(x + row * stride + col, x8);
-    float* p = lds + row * LD + col;
-    *reinterpret_cast<f32x4*>(p) = f32x4{x8[0], x8[1], x8[2], x8[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{x8[4], x8[5], x8[6], x8[7]};
+  constexpr int DP = Dims<D>::DP, LD = Dims<D>::LD, PR = DP / 8, N = C * PR / THREADS;
+  constexpr int AHEAD = N < 4 ? N : 4;      // loads under way at once
+  for (int first = 0; first < N; first += AHEAD) {
+    float x8[AHEAD][8];
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = threadIdx.x + (first + j) * THREADS, row = min(i / PR, count - 1), col = min(i % PR * 8, D - 8);
+      load8(x + row * stride + col, x8[j]);
+    }
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = threadIdx.x + (first + j) * THREADS, row = i / PR, col = i % PR * 8;
+      const bool real = row < count && col < D;
+      float* p = lds + row * LD + col;
+      for (int e = 0; e < 8; e += 4) {
+        const f32x4 y = {x8[j][e], x8[j][e + 1], x8[j][e + 2], x8[j][e + 3]};
+        *reinterpret_cast<f32x4*>(p + e) = real ? y : f32x4{};
+      }
+    }
   }
 }
 
@@ -174,13 +195,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
   __shared__ float bt[C];
   const int h = blockIdx.x % p.H;
   const int64_t w = blockIdx.x / p.H;
-  // the request whose range of chunk indices holds w: the last b with cu[b] / C + b <= w
-  int b = 0;
-  for (int lo = 0, hi = p.batch - 1; lo <= hi;) {
-    const int mid = (lo + hi) / 2;
-    if (request_span(p, mid).first / C + mid <= w) b = mid, lo = mid + 1;
-    else hi = mid - 1;
-  }
+  const int b = owner(p, w, C);
   const Span r = request_span(p, b);
   const int64_t c = w - (r.first / C + b);
   if (c < 0 || c * C >= r.count) return;
@@ -188,8 +203,8 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
   const int count = min(C, static_cast<int>(r.count - c * C));
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
 
-  stage<D>(kq[0], static_cast<const T*>(p.k) + first * p.k_stride + (h / p.rep) * D, p.k_stride, count);
-  stage<D>(kq[1], static_cast<const T*>(p.q) + first * p.q_stride + (h / p.rep) * D, p.q_stride, count);
+  stage<D, T, kThreads>(kq[0], static_cast<const T*>(p.k) + first * p.k_stride + (h / p.rep) * D, p.k_stride, count);
+  stage<D, T, kThreads>(kq[1], static_cast<const T*>(p.q) + first * p.q_stride + (h / p.rep) * D, p.q_stride, count);
   const ChunkWs ws = chunk_ws(p.workspace, w * p.H + h, DELTA);
   if (wave == 0) {
     // log2 G as a running sum in binary64, so that ratios of retentions far
@@ -292,12 +307,21 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
     const int64_t t0 = static_cast<int64_t>(c) * C;
     const ChunkWs ws = chunk_ws(p.workspace, (base + c) * p.H + h, DELTA);
     __syncthreads();
-    stage<D>(lk, k + t0 * p.k_stride, p.k_stride, count);
-    stage<D>(lq, q + t0 * p.q_stride, p.q_stride, count);
-    for (int i = tid; i < C * C / 4; i += 64 * NW) {
-      const int row = i / (C / 4), col = i % (C / 4) * 4;
-      *reinterpret_cast<f32x4*>(la + row * LA + col) = reinterpret_cast<const f32x4*>(ws.a)[i];
-      if constexpr (DELTA) *reinterpret_cast<f32x4*>(lt + row * LA + col) = reinterpret_cast<const f32x4*>(ws.t)[i];
+    stage<D, T, 64 * NW>(lk, k + t0 * p.k_stride, p.k_stride, count);
+    stage<D, T, 64 * NW>(lq, q + t0 * p.q_stride, p.q_stride, count);
+    constexpr int N = C * C / 4 / (64 * NW), AHEAD = N < 4 ? N : 4;
+    for (int first = 0; first < N; first += AHEAD) {
+      f32x4 xa[AHEAD], xt[AHEAD];
+      for (int j = 0; j < AHEAD; ++j) {
+        const int i = tid + (first + j) * 64 * NW;
+        xa[j] = reinterpret_cast<const f32x4*>(ws.a)[i];
+        if constexpr (DELTA) xt[j] = reinterpret_cast<const f32x4*>(ws.t)[i];
+      }
+      for (int j = 0; j < AHEAD; ++j) {
+        const int i = tid + (first + j) * 64 * NW, to = i / (C / 4) * LA + i % (C / 4) * 4;
+        *reinterpret_cast<f32x4*>(la + to) = xa[j];
+        if constexpr (DELTA) *reinterpret_cast<f32x4*>(lt + to) = xt[j];
+      }
     }
     for (int i = tid; i < C; i += 64 * NW) grow[i] = ws.grow[i], left[i] = ws.left[i];
     f32x4 u[4];
@@ -736,12 +760,7 @@ __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
   const uint32_t block = die_order(blockIdx.x, gridDim.x, p.rep);
   const int h = block % p.H;
   const int64_t w = block / p.H;
-  int b = 0;     // the last request with cu[b] / C + b <= w
-  for (int lo = 0, hi = p.batch - 1; lo <= hi;) {
-    const int mid = (lo + hi) / 2;
-    if (request_span(p, mid).first / C + mid <= w) b = mid, lo = mid + 1;
-    else hi = mid - 1;
-  }
+  const int b = owner(p, w, C);
   const Span r = request_span(p, b);
   const int64_t c = w - (r.first / C + b);
   if (c < 0 || c * C >= r.count) return;
@@ -771,8 +790,8 @@ __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
 
 // The request that comes `nth` by length, longest first, among up to 64 (beyond
 // that, where a chip full of workgroups evens lengths out by itself, in their own
-// order): 32768 tokens of 16 requests of 500 to 3500 took 0.88 ms in their own order,
-// with long ones starting last, and %LPT% ms so.
+// order): 32768 tokens of 16 requests of 500 to 3500 took 0.91 ms in their own order,
+// with long ones starting last, and 0.74 ms so.
 __device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lane) {
   if (p.batch == 1 || p.batch > 64) return nth;
   const int n = lane < p.batch ? request_span(p, lane).count : -1;
@@ -787,7 +806,14 @@ __device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lan
 // Walks a request's chunks in order for 16 NCT NW value columns of one head.
 // FUSED: all columns of the head in one workgroup, which computes the chunk
 // matrices itself; otherwise they come from k_linear16_chunks.
-template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED>
+//
+// A long prompt of few heads under the additive rule is walked in segments of
+// p.segment chunks at once: what a segment adds to the state does not depend on the
+// state it starts from, which only fades.  PASS 1 leaves every segment's own state
+// and retention in the workspace, k_linear_join turns them into the states that
+// segments start from, and PASS 2 computes the outputs.  One 16384-token prompt of
+// 32 heads: 983 us in 256 chunks one after another, 261 us in segments.
+template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED, int PASS>
 __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 : 1) k_linear16_walk(LinearArgs p) {
   using S = Dims16<D, T>;
   constexpr int NP = S::NP;
@@ -807,12 +833,24 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
   const uint32_t block = die_order(blockIdx.x, gridDim.x, p.rep * SPLIT);
   const int part = block % SPLIT;
   const int h = (block / SPLIT) % p.H;
-  const int b = nth_longest(p, block / (SPLIT * p.H), lane);
+  int b = 0;
+  int64_t segment = block / (SPLIT * p.H);
+  if constexpr (PASS == 0) {
+    b = nth_longest(p, static_cast<int>(segment), lane);
+  } else {
+    b = owner(p, segment, p.segment * C);
+  }
   const int ct0 = part * (COLS / 16) + wave * NCT;      // first column tile of the wave
-  const Span r = request_span(p, b);
+  Span r = request_span(p, b);
+  if constexpr (PASS != 0) {
+    const int64_t skip = (segment - (r.first / (p.segment * C) + b)) * p.segment * C;
+    if (skip < 0 || skip >= r.count) return;
+    r = {r.first + skip, static_cast<int32_t>(min(r.count - skip, static_cast<int64_t>(p.segment) * C))};
+  }
   const int slot = p.slot_ids[b];
   T* o = static_cast<T*>(p.o) + r.first * p.o_stride + h * D;
   if (slot < 0 || slot >= p.num_slots) {
+    if constexpr (PASS == 1) return;
     for (int t = tid / COLS; t < r.count; t += THREADS / COLS > 0 ? THREADS / COLS : 1)
       for (int j = tid % COLS; j < COLS; j += THREADS) o[t * p.o_stride + part * COLS + j] = static_cast<T>(__builtin_nanf(""));
     return;
@@ -820,11 +858,12 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
   const T* v = static_cast<const T*>(p.v) + r.first * p.v_stride + h * D;
   const T* k = static_cast<const T*>(p.k) + r.first * p.k_stride + (h / p.rep) * D;
   const T* q = static_cast<const T*>(p.q) + r.first * p.q_stride + (h / p.rep) * D;
-  float* state = p.state + (static_cast<int64_t>(slot) * p.H + h) * D * D + 16 * ct0;
+  float* state = (PASS == 0 ? p.state + (static_cast<int64_t>(slot) * p.H + h) * D * D
+                            : reinterpret_cast<float*>(p.workspace) + (segment * p.H + h) * (D * D + kSegmentHead)) + 16 * ct0;
 
   // column 16 (ct0 + n) + lane % 16; tile i holds key channels 32 (i / 2) + 8 g + 4 (i % 2) + e
   f32x4 m[NCT][S::RT] = {};
-  if (p.resume != nullptr && p.resume[b] != 0) {
+  if (PASS == 2 || (PASS == 0 && p.resume != nullptr && p.resume[b] != 0)) {
     const int l = fresh(lane), g = l >> 4, at = g * 8 * D + (l & 15);
     if (8 * g < D)
       for (int n = 0; n < NCT; ++n)
@@ -845,7 +884,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
   auto load_rows = [&](int64_t t0) __attribute__((always_inline)) {
     const int t = fresh(tid), n = static_cast<int>(min(static_cast<int64_t>(C), r.count - t0));
     kr.load(k + t0 * p.k_stride, p.k_stride, n, 0, t);
-    qr.load(q + t0 * p.q_stride, p.q_stride, n, 0, t);
+    if constexpr (PASS != 1) qr.load(q + t0 * p.q_stride, p.q_stride, n, 0, t);
     vr.load(v + t0 * p.v_stride, p.v_stride, n, part * VU, t);
     if constexpr (!FUSED)
       for (int j = 0; j < BL; ++j)
@@ -859,6 +898,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     if constexpr (DELTA) beta = p.beta[token];
     set_rates(all_rates[0], gate, beta, min(C, r.count), lane);
   }
+  float faded = 1.0f;     // the product of the retentions so far
   for (int c = 0; c * C < r.count; ++c) {
     const int count = min(C, r.count - c * C);
     const int64_t t0 = static_cast<int64_t>(c) * C;
@@ -876,7 +916,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     {
       const int t = fresh(tid);
       kr.template store<NP == 2>(lk, count, t);
-      qr.template store<NP == 2>(lq, count, t);
+      if constexpr (PASS != 1) qr.template store<NP == 2>(lq, count, t);
       if constexpr (!FUSED) {
         vr.template store<false>(lv, count, t);
         for (int j = 0; j < BL; ++j)
@@ -891,12 +931,12 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
         if constexpr (DELTA) beta = p.beta[token];
       }
       __syncthreads();
-      chunk_tiles<D, T, DELTA, NW>(lk, lq, rates, sc, la, lt, wave, fresh(lane));
+      if constexpr (PASS != 1) chunk_tiles<D, T, DELTA, NW>(lk, lq, rates, sc, la, lt, wave, fresh(lane));
       if (next) set_rates(all_rates[(c + 1) & 1], gate, beta, min(C, r.count - (c + 1) * C), lane);
       if (more) {
         const int t = fresh(tid), n = min(C, r.count - (c + 1) * C);
         kt.start(k + (t0 + C) * p.k_stride, p.k_stride, n, t);
-        qt.start(q + (t0 + C) * p.q_stride, p.q_stride, n, t);
+        if constexpr (PASS != 1) qt.start(q + (t0 + C) * p.q_stride, p.q_stride, n, t);
         vt.start(v + (t0 + C) * p.v_stride, p.v_stride, n, t);
       }
     } else {
@@ -907,7 +947,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     // K M and (transposed: rows value columns, columns tokens, so that a lane stores
     // 4 neighbours) Q M, the state split into its parts once for both
     f32x4 u[NCT][4] = {}, y[NCT][4] = {};
-    {
+    if constexpr (PASS != 1) {
     const At at = lane_at<S::RB>(fresh(lane));
     for (int kb = 0; kb < S::KB; ++kb) {
       Parts<2> mf[NCT];
@@ -966,7 +1006,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
       }
       in_order();
     }
-    {
+    if constexpr (PASS != 1) {
       const int l = fresh(lane), g = l >> 4, cl = l & 15;
       for (int i = 0; i < 4; ++i) {
         const float f = grow[16 * i + cl];
@@ -993,6 +1033,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     const At at = lane_at<S::RB>(l);
     Parts<2> wf[NCT][2];
     const float all = grow[C - 1];
+    faded *= all;
     for (int n = 0; n < NCT; ++n)
       for (int tb = 0; tb < 2; ++tb)
         wf[n][tb] = parts_of<2>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 4 * g]),
@@ -1008,11 +1049,36 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     }
     settle();
   }
+  if constexpr (PASS == 2) return;
+  if (PASS == 1 && tid == 0) state[D * D - 16 * ct0] = faded;
   const int l = fresh(lane), g = l >> 4, at = g * 8 * D + (l & 15);
   if (8 * g < D)      // fewer than 32 channels are padded to 32
     for (int n = 0; n < NCT; ++n)
       for (int i = 0; i < S::RT; ++i)
         for (int e = 0; e < 4; ++e) state[at + (32 * (i / 2) + 4 * (i % 2) + e) * D + 16 * n] = m[n][i][e];
+}
+
+// Four neighbouring state values of one (request, head): the states its segments start
+// from, in place of their own, and the final state.
+template <int D>
+__global__ void __launch_bounds__(kThreads) k_linear_join(LinearArgs p) {
+  constexpr int PARTS = D * D / (4 * kThreads);
+  const int part = blockIdx.x % PARTS, h = blockIdx.x / PARTS % p.H, b = blockIdx.x / PARTS / p.H;
+  const Span r = request_span(p, b);
+  const int slot = p.slot_ids[b];
+  if (slot < 0 || slot >= p.num_slots) return;
+  const int at = (part * kThreads + threadIdx.x) * 4;
+  float* state = p.state + (static_cast<int64_t>(slot) * p.H + h) * D * D + at;
+  f32x4 m = {};
+  if (p.resume != nullptr && p.resume[b] != 0) m = *reinterpret_cast<const f32x4*>(state);
+  const int64_t base = r.first / (p.segment * C) + b, step = static_cast<int64_t>(p.H) * (D * D + kSegmentHead);
+  float* own = reinterpret_cast<float*>(p.workspace) + (base * p.H + h) * (D * D + kSegmentHead);
+  for (int64_t s = 0; s * p.segment * C < r.count; ++s, own += step) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(own + at);
+    *reinterpret_cast<f32x4*>(own + at) = m;
+    m = m * own[D * D] + x;
+  }
+  *reinterpret_cast<f32x4*>(state) = m;
 }
 
 // One token: a workgroup owns CW columns of one (request, head) state; a lane
@@ -1086,23 +1152,6 @@ __global__ void __launch_bounds__(kThreads) k_linear_step(LinearArgs p) {
     for (int e = 0; e < 4; ++e) o[e] = static_cast<T>(w[e] + qk * x[e]);
 }
 
-template <int D, typename T, bool DELTA>
-hipError_t prefill_dt(const LinearArgs& a, hipStream_t s) {
-  using S = Dims<D>;
-  constexpr int NW = D >= 64 ? 4 : D / 16;
-  const int64_t chunks = max_chunks(a.total_tokens, a.batch);
-  k_linear_chunks<D, T, DELTA><<<dim3(static_cast<uint32_t>(chunks * a.H)), kThreads, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const size_t lds = sizeof(float) * (2 * C * S::LD + (DELTA ? 2 : 1) * C * (C + 4));
-  auto* kern = k_linear_walk<D, T, DELTA, NW>;
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                          static_cast<int>(lds));
-  if (e != hipSuccess) return e;
-  kern<<<dim3(static_cast<uint32_t>(a.batch * a.H * (D / (16 * NW)))), 64 * NW, lds, s>>>(a);
-  return hipGetLastError();
-}
-
 template <typename K>
 hipError_t launch_lds(K* kern, int64_t grid, int threads, int lds, const LinearArgs& a, hipStream_t s) {
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -1112,10 +1161,33 @@ hipError_t launch_lds(K* kern, int64_t grid, int threads, int lds, const LinearA
   return hipGetLastError();
 }
 
-template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED>
+template <int D, typename T, bool DELTA, int NW>
+hipError_t walk32(const LinearArgs& a, hipStream_t s) {
+  const int lds = sizeof(float) * (2 * C * Dims<D>::LD + (DELTA ? 2 : 1) * C * (C + 4));
+  return launch_lds(k_linear_walk<D, T, DELTA, NW>, static_cast<int64_t>(a.batch) * a.H * (D / (16 * NW)), 64 * NW, lds, a, s);
+}
+
+// Heads are split over workgroups of fewer columns where there are few of them.
+template <int D, typename T, bool DELTA>
+hipError_t prefill_dt(const LinearArgs& a, hipStream_t s) {
+  const int64_t tiles = static_cast<int64_t>(a.batch) * a.H;
+  k_linear_chunks<D, T, DELTA><<<dim3(static_cast<uint32_t>(max_chunks(a.total_tokens, a.batch) * a.H)), kThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if constexpr (D >= 64) {
+    if (tiles >= kFullChip) return walk32<D, T, DELTA, 4>(a, s);
+  }
+  if constexpr (D >= 32) {
+    if (tiles * (D / 32) >= kFullChip) return walk32<D, T, DELTA, 2>(a, s);
+  }
+  return walk32<D, T, DELTA, 1>(a, s);
+}
+
+template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED, int PASS = 0>
 hipError_t walk16(const LinearArgs& a, hipStream_t s) {
   constexpr int COLS = 16 * NCT * NW;
-  return launch_lds(k_linear16_walk<D, T, DELTA, NCT, NW, FUSED>, static_cast<int64_t>(a.batch) * a.H * (D / COLS), 64 * NW,
+  const int64_t rows = PASS == 0 ? a.batch : max_segments(a.total_tokens, a.batch, a.segment);
+  return launch_lds(k_linear16_walk<D, T, DELTA, NCT, NW, FUSED, PASS>, rows * a.H * (D / COLS), 64 * NW,
                     Lds16<D, T, DELTA, COLS, FUSED>::BYTES, a, s);
 }
 
@@ -1123,7 +1195,16 @@ template <int D, typename T, bool DELTA>
 hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
   const int64_t tiles = static_cast<int64_t>(a.batch) * a.H;
   if constexpr (D >= 64) {
-    if (tiles >= 256) return walk16<D, T, DELTA, DELTA ? D / 64 : 1, DELTA ? 4 : D / 16, true>(a, s);
+    if (tiles >= kFullChip) return walk16<D, T, DELTA, DELTA ? D / 64 : 1, DELTA ? 4 : D / 16, true>(a, s);
+  }
+  if constexpr (D >= 64 && !DELTA) {
+    if (a.segment > 0) {
+      hipError_t e = walk16<D, T, false, 1, D / 16, true, 1>(a, s);
+      if (e != hipSuccess) return e;
+      k_linear_join<D><<<dim3(static_cast<uint32_t>(tiles * (D * D / (4 * kThreads)))), kThreads, 0, s>>>(a);
+      e = hipGetLastError();
+      return e != hipSuccess ? e : walk16<D, T, false, 1, D / 16, true, 2>(a, s);
+    }
   }
   const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, max_chunks(a.total_tokens, a.batch) * a.H, kThreads,
                                   Lds16<D, T, DELTA, D, true, true>::BYTES, a, s);

@@ -316,6 +316,38 @@ def test_many_requests(dtype, rule, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("gates", ["mixed", "strong"])
+@pytest.mark.parametrize("rule", ["additive", "delta"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_long_prompts_of_few_heads(dtype, rule, gates, D):
+    """Long on the average, an empty and a short one among them, some resuming, one
+    without a slot: under the additive rule these are walked in segments."""
+    r = Run(dtype, 2, 1, D, rule, [1500, 3, 0, 1023, 256, 700], seed=D, gates=gates)
+    resume = [1, 0, 1, 0, 1, 1]
+    slots = r.slots.copy()
+    slots[4] = -3
+    r.prefill(resume, slots=slots)
+    o = r.o.float().cpu().numpy()
+    lo, hi = r.cu[4], r.cu[5]
+    assert np.isnan(o[lo:hi]).all() and np.array_equal(r.state[int(r.slots[4])].cpu().numpy(), r.before[r.slots[4]])
+    r.prefill(resume=[0, 0, 0, 0, 1, 0], slots=np.where(np.arange(6) == 4, r.slots, -1).astype(np.int32))
+    r.o[:lo], r.o[hi:] = torch_like(o[:lo], r.o), torch_like(o[hi:], r.o)
+    r.check(resume)
+
+
+def torch_like(x, t):
+    import torch
+    return torch.from_numpy(x).to(t.device, t.dtype)
+
+
+def test_workspace_of_segments_grows_with_tokens_and_requests():
+    att = LN.LinearAttention(8, 64, rule="additive", dtype=torch_dtype("bf16"))
+    size = [att.workspace_bytes(b, t) for b, t in ((1, 100), (1, 5000), (3, 5000), (3, 60000), (40, 60000), (40, 10 ** 6))]
+    assert size == sorted(size) and size[0] > 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rule", ["additive", "delta"])
 def test_long_prompt_many_chunks(rule):
     r = Run("bf16", 2, 1, 128, rule, [3001, 5], seed=8)
