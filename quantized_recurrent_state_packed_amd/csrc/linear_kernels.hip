@@ -753,7 +753,7 @@ __device__ __forceinline__ uint32_t die_order(uint32_t block, uint32_t total, ui
 template <int D, typename T, bool DELTA>
 __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
   using S = Dims16<D, T>;
-  using L = Lds16<D, T, DELTA, D, true, true>;
+  using L = Lds16<D, T, DELTA, 16, true, true>;      // no v
   extern __shared__ __align__(16) uint8_t lds16[];
   Rates& rates = *reinterpret_cast<Rates*>(lds16 + L::RATES);
   Scratch* sc = reinterpret_cast<Scratch*>(lds16 + L::SCRATCH);
@@ -1167,20 +1167,11 @@ hipError_t walk32(const LinearArgs& a, hipStream_t s) {
   return launch_lds(k_linear_walk<D, T, DELTA, NW>, static_cast<int64_t>(a.batch) * a.H * (D / (16 * NW)), 64 * NW, lds, a, s);
 }
 
-// Heads are split over workgroups of fewer columns where there are few of them.
 template <int D, typename T, bool DELTA>
 hipError_t prefill_dt(const LinearArgs& a, hipStream_t s) {
-  const int64_t tiles = static_cast<int64_t>(a.batch) * a.H;
   k_linear_chunks<D, T, DELTA><<<dim3(static_cast<uint32_t>(max_chunks(a.total_tokens, a.batch) * a.H)), kThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if constexpr (D >= 64) {
-    if (tiles >= kFullChip) return walk32<D, T, DELTA, 4>(a, s);
-  }
-  if constexpr (D >= 32) {
-    if (tiles * (D / 32) >= kFullChip) return walk32<D, T, DELTA, 2>(a, s);
-  }
-  return walk32<D, T, DELTA, 1>(a, s);
+  return e != hipSuccess ? e : walk32<D, T, DELTA, D >= 64 ? 4 : D / 16>(a, s);
 }
 
 template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED, int PASS = 0>
@@ -1207,12 +1198,16 @@ hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
     }
   }
   const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, max_chunks(a.total_tokens, a.batch) * a.H, kThreads,
-                                  Lds16<D, T, DELTA, D, true, true>::BYTES, a, s);
+                                  Lds16<D, T, DELTA, 16, true, true>::BYTES, a, s);
   if (e != hipSuccess) return e;
-  if constexpr (D >= 32) {
-    if (tiles * (D / 32) >= 256) return walk16<D, T, DELTA, 1, 2, false>(a, s);
+  // as few columns a workgroup as the chip holds workgroups for at once
+  const auto held = [](int lds) { return static_cast<int64_t>(256) * (163840 / lds); };
+  if (D == 16 || tiles * (D / 16) <= held(Lds16<D, T, DELTA, 16, false>::BYTES)) return walk16<D, T, DELTA, 1, 1, false>(a, s);
+  if constexpr (D >= 64) {
+    if (tiles * (D / 32) > held(Lds16<D, T, DELTA, 32, false>::BYTES)) return walk16<D, T, DELTA, 1, 4, false>(a, s);
   }
-  return walk16<D, T, DELTA, 1, 1, false>(a, s);
+  if constexpr (D >= 32) return walk16<D, T, DELTA, 1, 2, false>(a, s);
+  return hipErrorInvalidValue;
 }
 
 template <int D, typename T>
