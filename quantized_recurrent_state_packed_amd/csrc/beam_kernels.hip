@@ -18,7 +18,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kScanWaves = 4096;      // 256 CUs x 16 waves
+constexpr int kScanWaves = 4096;      // 256 compute units x 16 waves
 constexpr int kPer = kTile / 64;      // logits a lane holds
 constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.4426950408889634f;
@@ -134,6 +134,10 @@ struct Tile {
   }
 };
 
+// Bound by the vector units: 13 or so instruction slots a logit (four of them the
+// exponential's) and some 50 insertions of about 120 cycles a wave.  32 x 8 rows of
+// 131072 bfloat16 logits take 44 us, 1.5 TB/s; copying their bytes takes 13.  With half
+// as many waves 46.5 us, with twice as many 50 (every wave fills a list of its own).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
   using L = Loader<T>;
@@ -199,7 +203,9 @@ __global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
 }
 
 // A wave per beam joins the lists of the beam's parts, all of whose entries are
-// loaded at once, and the first wave orders the beams' candidates.
+// loaded at once, and the first wave orders the beams' candidates.  Bound by the
+// latency of its insertions: 17 us for 8 beams of 16 parts and 16 candidates, 5.6 us
+// for 4 beams of 32 parts and 4.
 __global__ void __launch_bounds__(1024) k_select_merge(SelectArgs p) {
   __shared__ float sx[kMaxBeams][64];
   __shared__ int32_t si[kMaxBeams][64];
@@ -271,7 +277,9 @@ __global__ void __launch_bounds__(1024) k_select_merge(SelectArgs p) {
 
 // One workgroup per (new beam, segment of a slot).  Every wave works out the
 // request's assignment from its parents: bit j of `first` says that new beam j
-// is its parent's first child, bit i of `dead` that old beam i has none.
+// is its parent's first child, bit i of `dead` that old beam i has none.  Only the
+// states of beams that split are moved, each read and written once: 192 slots of
+// 614 KB take 48.7 us, 4.85 TB/s, of the 45.7 that a copy takes.
 __global__ void __launch_bounds__(kThreads) k_beam_reorder(ReorderArgs p) {
   const int lane = threadIdx.x & 63;
   const int j = blockIdx.x % p.beams;

@@ -38,9 +38,8 @@ struct LinearArgs {
 };
 
 // Chunks of all requests together: request b's chunks start at index
-// cu_seqlens[b] / 64 + b, so that no table of chunks is needed.  floor(x / 64)
-// + 1 never falls below the ceil((y - x) / 64) chunks of the tokens x .. y-1 by
-// more than what floor(y / 64) makes up for, so ranges do not overlap.
+// cu_seqlens[b] / 64 + b, so that no table of them is needed.  From b to b + 1 the
+// index grows by at least the ceil((cu[b + 1] - cu[b]) / 64) chunks of request b.
 inline int64_t max_chunks(int64_t total_tokens, int32_t batch) { return total_tokens / kChunk + batch; }
 
 // (request, head) pairs from which one workgroup for each fills the chip.

@@ -15,9 +15,18 @@
 //   U = (I + B)^-1 diag(b) (V - diag(G) K M)
 //   O = diag(G) Q M + A U,    A_tj = (G_t / G_j) q_t . k_j  for j <= t
 //   M <- G_C M + K^T diag(G_C / G) U
-// T and A do not depend on the state: k_linear_chunks computes them for all
-// chunks at once.  k_linear_walk then walks a request's chunks in order; value
-// columns are independent there, so a workgroup owns some columns of one head.
+// A and B do not depend on the state, and value columns are independent of each
+// other.  So a request's chunks are walked in order by workgroups that own some
+// columns of one head, either with A and B from a kernel that computes them for all
+// chunks at once (few heads: many workgroups a head), or, where there are heads
+// enough to fill the chip, computing them as they go (no 25 KB of them a chunk and
+// head through memory): 8192 tokens of 8 requests and 48 heads, delta rule, bfloat16,
+// 308 us the first way and 248 us the second; 32768 tokens of 16, 1050 and 715 us.
+//
+// Binary32 inputs run on binary32 matrix instructions (k_linear_chunks,
+// k_linear_walk), 16-bit inputs on bfloat16 ones (k_linear16_*).  MI355X copies at
+// 5160 GB/s and multiplies large matrices at 1226 (bfloat16) and 153 (binary32)
+// TFLOP/s; what each kernel reaches stands beside it.
 #include "linear_internal.hpp"
 
 namespace stepq {
@@ -26,25 +35,15 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16;
 typedef _Float16 f16;
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int C = kChunk;
 constexpr int kThreads = 256;
 
-// Eight consecutive elements of a 16-byte aligned row, as floats.
+// Eight consecutive elements of a 16-byte aligned row.
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
   for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
 }
-__device__ __forceinline__ void load8(const bf16* p, float (&x)[8]) {
-  const u16x8 a = *reinterpret_cast<const u16x8*>(p);
-  for (int i = 0; i < 8; ++i) x[i] = __builtin_bit_cast(float, static_cast<uint32_t>(a[i]) << 16);
-}
-__device__ __forceinline__ void load8(const f16* p, float (&x)[8]) {
-  const u16x8 a = *reinterpret_cast<const u16x8*>(p);
-  for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(__builtin_bit_cast(f16, static_cast<uint16_t>(a[i])));
-}
-
 // Product of a 16 x 32 and a 32 x 16 block in binary32.  A lane's eight values
 // of either operand belong to depth 4 g + j (j < 4) and 16 + 4 g + j - 4, with
 // g = lane / 16: in this order the two accumulator tiles that make up 32 rows
@@ -269,6 +268,10 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
   }
 }
 
+// A workgroup of up to four waves for 64 columns of a head.  Bound by the latency of a
+// chunk's chain of staging and dependent products: 3001 tokens of 5 requests, 12 heads
+// of 64, 134 us in all, some 6 us a chunk of the longest; one wave for 16 columns
+// instead, in four times as many workgroups, 172 against 167 us for this kernel.
 template <int D, typename T, bool DELTA, int NW>
 __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
   using S = Dims<D>;
@@ -749,7 +752,8 @@ __device__ __forceinline__ uint32_t die_order(uint32_t block, uint32_t total, ui
   return block < whole ? block - w + (w % 8) * n + w / 8 : block;
 }
 
-// The chunk matrices of every (chunk, head), for k_linear16_walk<.., false>.
+// The chunk matrices of every (chunk, head), for k_linear16_walk<.., false>.  Bound by
+// latency; two workgroups a compute unit (one for binary16, whose parts take the LDS).
 template <int D, typename T, bool DELTA>
 __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
   using S = Dims16<D, T>;
@@ -813,6 +817,16 @@ __device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lan
 // and retention in the workspace, k_linear_join turns them into the states that
 // segments start from, and PASS 2 computes the outputs.  One 16384-token prompt of
 // 32 heads: 983 us in 256 chunks one after another, 261 us in segments.
+//
+// At D = 128 the delta rule takes 276 matrix instructions of 16 cycles a chunk from
+// each of four waves with 32 columns (fewer, wider waves read q and k from LDS half as
+// often as eight with 16, and those spilled: 381 us against 225 for 512 pairs of 1024
+// tokens); the additive rule fits 128 registers with eight waves (157 against 162 us).
+// Bound by latency: with two workgroups a compute unit the matrix units are busy 36 %
+// and the vector units 47 % of the time, memory 18 % of its rate; the chain of a chunk
+// (staging, blocks and their inverses, K M and Q M, U, O, the state) has five barriers
+// and leaves two waves a SIMD too little to overlap.  32768 tokens of 16 requests and
+// 48 heads take 600 to 640 us, 2.8 times what copying their bytes takes.
 template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED, int PASS>
 __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 : 1) k_linear16_walk(LinearArgs p) {
   using S = Dims16<D, T>;
@@ -988,12 +1002,10 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
         for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(u[n][0], none), u[n][1]);
         for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(none, u[n][1]), none);
         for (int n = 0; n < NCT; ++n) uf[n][0] = parts_of<2>(u[n][0], u[n][1]);
-        in_order();
         s = stored_parts(lt, lt + kTri, tri(2, 0), l);
         for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, uf[n][0], u[n][2]);
         s = stored_parts(lt, lt + kTri, tri(3, 0), l);
         for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, uf[n][0], u[n][3]);
-        in_order();
         s = stored_parts(lt, lt + kTri, tri(2, 1), l);
         for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, parts_of<2>(u[n][2], none), none);
         s = stored_parts(lt, lt + kTri, tri(3, 1), l);
@@ -1015,7 +1027,6 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
           const Parts<2> a = stored_parts(la, la + kTri, tri(i, tb), l);
           for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
         }
-        if (i & 1) in_order();
       }
       settle();
       for (int i = 0; i < 4; ++i) {
@@ -1081,25 +1092,29 @@ __global__ void __launch_bounds__(kThreads) k_linear_join(LinearArgs p) {
   *reinterpret_cast<f32x4*>(state) = m;
 }
 
-// One token: a workgroup owns CW columns of one (request, head) state; a lane
-// holds 4 columns of D / RG rows in registers.  With the decayed state M~,
+constexpr int step_threads(int d) { return d * d / 4 < kThreads ? d * d / 4 : kThreads; }
+
+// One token: a workgroup owns one (request, head) state; a lane holds 4 columns of
+// D / RG rows in registers.  With the decayed state M~,
 // u = M~^T k and w = M~^T q (one reduction for both) the new state's readout is
 // o = w + (q . k) x with x = b (v - u), or v for the additive rule, so the state
-// is read and written once.
-template <int D, typename T, int CW>
+// is read and written once.  Bound by memory: 512 requests of 48 heads of 128 take
+// 635 us, 5150 GB/s, what a copy reaches; one request's 48 states take 5.3 us of which
+// 1.2 us are its bytes, the rest the latency of one load, two sums and a store.
+template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) k_linear_step(LinearArgs p) {
-  constexpr int LPR = CW / 4;
-  constexpr int NT = D * LPR < kThreads ? (D * LPR < 64 ? 64 : D * LPR) : kThreads;
+  constexpr int LPR = D / 4;
+  constexpr int NT = step_threads(D);
   constexpr int RG = NT / LPR;                 // row groups
-  constexpr int RPT = (D + RG - 1) / RG;       // rows per lane; row groups past D idle
+  constexpr int RPT = D / RG;                  // rows per lane
+  static_assert(RPT * RG == D && NT >= D, "every lane has whole rows");
   constexpr int NW = NT / 64;
-  constexpr int SPLIT = D / CW;
   __shared__ float qs[D], ks[D];
   __shared__ __align__(16) f32x4 part[NW][2][LPR < 64 ? LPR : 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = (blockIdx.x / SPLIT) % p.H;
-  const int64_t b = blockIdx.x / (SPLIT * p.H);
-  const int j0 = (blockIdx.x % SPLIT) * CW + 4 * (tid % LPR);
+  const int h = blockIdx.x % p.H;
+  const int64_t b = blockIdx.x / p.H;
+  const int j0 = 4 * (tid % LPR);
   const int rg = tid / LPR;
   const int slot = p.slot_ids[b];
   T* o = static_cast<T*>(p.o) + b * p.o_stride + h * D + j0;
@@ -1110,8 +1125,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_step(LinearArgs p) {
   }
   float* state = p.state + (static_cast<int64_t>(slot) * p.H + h) * D * D + j0;
   f32x4 m[RPT];
-  for (int i = 0; i < RPT; ++i)
-    if (rg + i * RG < D) m[i] = *reinterpret_cast<const f32x4*>(state + (rg + i * RG) * D);
+  for (int i = 0; i < RPT; ++i) m[i] = *reinterpret_cast<const f32x4*>(state + (rg + i * RG) * D);
   if (tid < D) {
     qs[tid] = static_cast<float>(static_cast<const T*>(p.q)[b * p.q_stride + (h / p.rep) * D + tid]);
     ks[tid] = static_cast<float>(static_cast<const T*>(p.k)[b * p.k_stride + (h / p.rep) * D + tid]);
@@ -1122,12 +1136,11 @@ __global__ void __launch_bounds__(kThreads) k_linear_step(LinearArgs p) {
   for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(static_cast<const T*>(p.v)[b * p.v_stride + h * D + j0 + e]);
   __syncthreads();
   f32x4 u = {}, w = {};
-  for (int i = 0; i < RPT; ++i)
-    if (rg + i * RG < D) {
-      m[i] *= a;
-      u += m[i] * ks[rg + i * RG];
-      w += m[i] * qs[rg + i * RG];
-    }
+  for (int i = 0; i < RPT; ++i) {
+    m[i] *= a;
+    u += m[i] * ks[rg + i * RG];
+    w += m[i] * qs[rg + i * RG];
+  }
   float qk = 0.0f;
   for (int i = lane; i < D; i += 64) qk = fmaf(qs[i], ks[i], qk);
   for (int s = 1; s < 64; s <<= 1) qk += __shfl_xor(qk, s);
@@ -1146,8 +1159,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_step(LinearArgs p) {
     }
   }
   const f32x4 x = p.beta ? beta * (v - u) : v;
-  for (int i = 0; i < RPT; ++i)
-    if (rg + i * RG < D) *reinterpret_cast<f32x4*>(state + (rg + i * RG) * D) = m[i] + ks[rg + i * RG] * x;
+  for (int i = 0; i < RPT; ++i) *reinterpret_cast<f32x4*>(state + (rg + i * RG) * D) = m[i] + ks[rg + i * RG] * x;
   if (tid < LPR)
     for (int e = 0; e < 4; ++e) o[e] = static_cast<T>(w[e] + qk * x[e]);
 }
@@ -1212,10 +1224,7 @@ hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
 
 template <int D, typename T>
 hipError_t step_dt(const LinearArgs& a, hipStream_t s) {
-  constexpr int CW = D;
-  constexpr int LPR = CW / 4;
-  constexpr int NT = D * LPR < kThreads ? (D * LPR < 64 ? 64 : D * LPR) : kThreads;
-  k_linear_step<D, T, CW><<<dim3(static_cast<uint32_t>(a.batch * a.H * (D / CW))), NT, 0, s>>>(a);
+  k_linear_step<D, T><<<dim3(static_cast<uint32_t>(a.batch * a.H)), step_threads(D), 0, s>>>(a);
   return hipGetLastError();
 }
 
