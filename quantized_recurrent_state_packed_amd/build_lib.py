@@ -27,14 +27,17 @@ SOURCES = ["stepq_kernels.hip", "stepq_api.cpp", "linear_kernels.hip", "linear_a
 def build(verbose: bool = False) -> Path:
     """Compile every source and link libstepq.so (always rebuilds)."""
     with tempfile.TemporaryDirectory(prefix="stepq_build_") as tmp:
-        objs = []
-        for src in SOURCES:
+        objs, running = [], []
+        for src in SOURCES:          # one compiler for each source at a time
             obj = Path(tmp) / (src + ".o")
             cmd = [HIPCC, *FLAGS, "-c", str(CSRC / src), "-o", str(obj)]
             if verbose:
                 print(" ".join(cmd), flush=True)
-            subprocess.run(cmd, check=True)
+            running.append((cmd, subprocess.Popen(cmd)))
             objs.append(str(obj))
+        failed = [cmd for cmd, p in running if p.wait() != 0]
+        if failed:
+            raise subprocess.CalledProcessError(1, failed[0])
         out = Path(tmp) / "libstepq.so"
         cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", str(out)]
         if verbose:

@@ -383,11 +383,14 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
 // Matrix products of 16-bit inputs run on bfloat16 matrix instructions, which
 // multiply exactly and add in binary32, sixteen times as fast as the binary32
 // ones.  A bfloat16 q, k or v is its own operand; a binary16 q or k is the sum of
-// two bfloat16 parts exactly (11 bits in 8 + 8).  Computed operands (state, T, R,
-// U) are split into a part of 8 bits and a rest of 8, 2^-17 of the value at
-// worst, wherever they lead into the state, which lives long; products take the
-// terms above 2^-16.  What only leads into a bfloat16 o (the state under q, A, U
-// under A) is one part: a single rounding of each, not larger than o's own.
+// two bfloat16 parts exactly (11 bits in 8 + 8).  Computed operands (state, A, the
+// system for U, its right sides) are split into two parts of 8 bits, which leaves
+// 2^-16 of the value at worst, 2^-18.7 on the average; what the additive rule adds to
+// the state, its only such rounding, is split into three, which leaves that of
+// binary32.  States come out within 6e-6 (delta) and 4e-7 (additive) of the recurrence
+// in 64 bits in the 2-norm, a tenth of what their 6- and 8-bit storage rounds away at
+// the least; three parts throughout do not fit the LDS of two workgroups.  One part
+// would do for most of a bfloat16 o, but not where its terms all but cancel.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -443,17 +446,22 @@ __device__ __forceinline__ Parts<NP> parts_of(const f32x4& a, const f32x4& b) {
   Parts<NP> r;
   const bf16x4 ah = rounded(a), bh = rounded(b);
   r.p[0] = join(ah, bh);
-  if constexpr (NP == 2) r.p[1] = join(rounded(rest_of(a, ah)), rounded(rest_of(b, bh)));
+  if constexpr (NP >= 2) {
+    const f32x4 ar = rest_of(a, ah), br = rest_of(b, bh);
+    const bf16x4 am = rounded(ar), bm = rounded(br);
+    r.p[1] = join(am, bm);
+    if constexpr (NP == 3) r.p[2] = join(rounded(rest_of(ar, am)), rounded(rest_of(br, bm)));
+  }
   return r;
 }
 
-// Product of operands in NA and NB parts.  FULL: with the product of two rests
-// (q . k and k . k, whose parts are exact and whose sums may all but cancel).
-template <bool FULL = false, int NA, int NB>
+// Product of operands in NA and NB parts, every part 2^-8 of the one before, with the
+// terms above 2^(-8 ORDER).
+template <int ORDER, int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const Parts<NA>& a, const Parts<NB>& b, f32x4 c) {
   for (int i = NA - 1; i >= 0; --i)
     for (int j = NB - 1; j >= 0; --j)
-      if (FULL || i + j < 2) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
+      if (i + j < ORDER) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
   return c;
 }
 
@@ -662,8 +670,8 @@ __device__ __forceinline__ void chunk_tile(const uint8_t* lk, const uint8_t* lq,
       qi.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
       if constexpr (DELTA) ki.p[x] = DIAGONAL ? kj.p[x] : row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
     }
-    qk = mma<true>(kj, qi, qk);
-    if constexpr (DELTA) kk = mma<true>(kj, ki, kk);
+    qk = mma<3>(kj, qi, qk);
+    if constexpr (DELTA) kk = mma<3>(kj, ki, kk);
   }
   settle();
   const double li = r.lg[16 * i + c];
@@ -818,7 +826,7 @@ __device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lan
 // segments start from, and PASS 2 computes the outputs.  One 16384-token prompt of
 // 32 heads: 983 us in 256 chunks one after another, 261 us in segments.
 //
-// At D = 128 the delta rule takes 276 matrix instructions of 16 cycles a chunk from
+// At D = 128 the delta rule takes 292 matrix instructions of 16 cycles a chunk from
 // each of four waves with 32 columns (fewer, wider waves read q and k from LDS half as
 // often as eight with 16, and those spilled: 381 us against 225 for 512 pairs of 1024
 // tokens); the additive rule fits 128 registers with eight waves (157 against 162 us).
@@ -972,10 +980,10 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
         Parts<NP> a;
         if constexpr (DELTA) {
           for (int x = 0; x < NP; ++x) a.p[x] = row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
-          for (int n = 0; n < NCT; ++n) u[n][i] = mma(a, mf[n], u[n][i]);
+          for (int n = 0; n < NCT; ++n) u[n][i] = mma<3>(a, mf[n], u[n][i]);
         }
         for (int x = 0; x < NP; ++x) a.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
-        for (int n = 0; n < NCT; ++n) y[n][i] = mma(mf[n], a, y[n][i]);
+        for (int n = 0; n < NCT; ++n) y[n][i] = mma<2>(mf[n], a, y[n][i]);
       }
       in_order();
     }
@@ -997,20 +1005,20 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
       const f32x4 none = {};
       if constexpr (DELTA) {
         Parts<2> s = stored_parts(lt, lt + kTri, tri(0, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][0] = mma(s, parts_of<2>(u[n][0], none), none);
+        for (int n = 0; n < NCT; ++n) u[n][0] = mma<3>(s, parts_of<2>(u[n][0], none), none);
         s = stored_parts(lt, lt + kTri, tri(1, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(u[n][0], none), u[n][1]);
-        for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<2>(none, u[n][1]), none);
+        for (int n = 0; n < NCT; ++n) u[n][1] = mma<3>(s, parts_of<2>(u[n][0], none), u[n][1]);
+        for (int n = 0; n < NCT; ++n) u[n][1] = mma<3>(s, parts_of<2>(none, u[n][1]), none);
         for (int n = 0; n < NCT; ++n) uf[n][0] = parts_of<2>(u[n][0], u[n][1]);
         s = stored_parts(lt, lt + kTri, tri(2, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, uf[n][0], u[n][2]);
+        for (int n = 0; n < NCT; ++n) u[n][2] = mma<3>(s, uf[n][0], u[n][2]);
         s = stored_parts(lt, lt + kTri, tri(3, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, uf[n][0], u[n][3]);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma<3>(s, uf[n][0], u[n][3]);
         s = stored_parts(lt, lt + kTri, tri(2, 1), l);
-        for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, parts_of<2>(u[n][2], none), none);
+        for (int n = 0; n < NCT; ++n) u[n][2] = mma<3>(s, parts_of<2>(u[n][2], none), none);
         s = stored_parts(lt, lt + kTri, tri(3, 1), l);
-        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, parts_of<2>(u[n][2], none), u[n][3]);
-        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, parts_of<2>(none, u[n][3]), none);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma<3>(s, parts_of<2>(u[n][2], none), u[n][3]);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma<3>(s, parts_of<2>(none, u[n][3]), none);
         for (int n = 0; n < NCT; ++n) uf[n][1] = parts_of<2>(u[n][2], u[n][3]);
       } else {
         for (int n = 0; n < NCT; ++n)
@@ -1025,7 +1033,7 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
         for (int n = 0; n < NCT; ++n) y[n][i] *= f;
         for (int tb = 0; tb <= i / 2; ++tb) {
           const Parts<2> a = stored_parts(la, la + kTri, tri(i, tb), l);
-          for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
+          for (int n = 0; n < NCT; ++n) y[n][i] = mma<2>(uf[n][tb], a, y[n][i]);
         }
       }
       settle();
@@ -1042,19 +1050,20 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     in_order();
     const int l = fresh(lane), g = l >> 4;
     const At at = lane_at<S::RB>(l);
-    Parts<2> wf[NCT][2];
+    constexpr int WP = DELTA ? 2 : 3;
+    Parts<WP> wf[NCT][2];
     const float all = grow[C - 1];
     faded *= all;
     for (int n = 0; n < NCT; ++n)
       for (int tb = 0; tb < 2; ++tb)
-        wf[n][tb] = parts_of<2>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 4 * g]),
+        wf[n][tb] = parts_of<WP>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 4 * g]),
                                 u[n][2 * tb + 1] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 16 + 4 * g]));
     for (int i = 0; i < S::RT; ++i) {
       for (int n = 0; n < NCT; ++n) m[n][i] *= all;
       for (int tb = 0; tb < 2; ++tb) {
         Parts<NP> a;
         for (int x = 0; x < NP; ++x) a.p[x] = column_operand<S::RB>(lk + x * S::MAT, tb, i, at);
-        for (int n = 0; n < NCT; ++n) m[n][i] = mma(a, wf[n][tb], m[n][i]);
+        for (int n = 0; n < NCT; ++n) m[n][i] = mma<3>(a, wf[n][tb], m[n][i]);
       }
       if (i % 2) in_order();
     }

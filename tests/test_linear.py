@@ -6,8 +6,9 @@ Tolerances, as relative 2-norms of every (request, head)'s outputs and state:
    value passes at most four products of depth <= 192, each within about
    sqrt(192) * 2^-24 in the 2-norm of values without cancellation: 3.3e-6, and
    cancellation in v - M^T k costs a factor of up to 3: 1e-5;
- * states of 16-bit inputs: an operand may be held as two bfloat16 parts, 2^-17
-   of its size at worst, in at most three chained products: 2.3e-5;
+ * states of 16-bit inputs: an operand may be held as two bfloat16 parts, which
+   leaves about 2^-17 of its size (2^-16 at the bottom of a binade), in at most
+   three chained products: 2.3e-5;
  * binary16 outputs: one rounding, at most 2^-11, on top: 5e-4;
  * bfloat16 outputs: one rounding of the result and one of each of three
    operands of the readout, each uniform within 2^-9: sqrt(4 / 3) * 2^-9 =
