@@ -6,11 +6,13 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+constexpr int64_t kMostRows = 1 << 23;    // beams of a call: a grid holds fewer than 2^32 threads
+
 stepq_status check_sizes(int32_t batch, int32_t beams, int32_t vocab, int32_t num_out) {
   if (batch < 0 || beams < 1 || vocab < 1 || num_out < 1) return STEPQ_ERR_INVALID_ARG;
   if (beams > stepq::kMaxBeams || num_out > 64) return STEPQ_ERR_UNSUPPORTED;
   if (vocab > 0x7fffffff - stepq::kTile) return STEPQ_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(batch) * beams > (1 << 24)) return STEPQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * beams > kMostRows) return STEPQ_ERR_UNSUPPORTED;
   return STEPQ_OK;
 }
 
@@ -67,7 +69,7 @@ stepq_status stepq_beam_reorder(int32_t batch, int32_t beams, const int32_t* slo
                                 int32_t* new_slot_ids, void* stream) {
   if (batch < 0 || beams < 1 || num_slots < 1 || num_regions < 0) return STEPQ_ERR_INVALID_ARG;
   if (beams > stepq::kMaxBeams || num_regions > STEPQ_MAX_REGIONS) return STEPQ_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(batch) * beams > (1 << 24)) return STEPQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * beams > kMostRows) return STEPQ_ERR_UNSUPPORTED;
   if (batch == 0) return STEPQ_OK;
   if (!slot_ids || !parents || !new_slot_ids || (num_regions > 0 && !regions)) return STEPQ_ERR_INVALID_ARG;
   if (!aligned(slot_ids, 4) || !aligned(parents, 4) || !aligned(new_slot_ids, 4)) return STEPQ_ERR_INVALID_ARG;

@@ -6,6 +6,9 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+constexpr int64_t kMostHeads = (1 << 23) - 1;        // (request, head) pairs of a call
+constexpr int64_t kMostChunkHeads = (1 << 24) - 1;   // (chunk, head) pairs of a call
+
 int elem_bytes(int dtype) { return dtype == STEPQ_F32 ? 4 : 2; }
 
 stepq_status check_desc(const stepq_linear_desc* d) {
@@ -64,10 +67,11 @@ stepq_status stepq_linear_prefill(const stepq_linear_desc* d, int32_t batch, int
   if (batch == 0) return STEPQ_OK;
   if (!cu_seqlens || !slot_ids || !aligned(cu_seqlens, 4) || !aligned(slot_ids, 4))
     return STEPQ_ERR_INVALID_ARG;
-  // int32 cu_seqlens, and one grid index per (chunk, head) and per (request, head, column tile)
+  // int32 cu_seqlens; grids of fewer than 2^32 threads: 256 for every (chunk, head), up to
+  // 512 for every (request, head)
   if (total_tokens > 0x7fffffffLL) return STEPQ_ERR_UNSUPPORTED;
-  if (stepq::max_chunks(total_tokens, batch) * d->num_heads > 0x7fffffffLL) return STEPQ_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(batch) * d->num_heads * (d->d / 16) > 0x7fffffffLL) return STEPQ_ERR_UNSUPPORTED;
+  if (stepq::max_chunks(total_tokens, batch) > kMostChunkHeads / d->num_heads) return STEPQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * d->num_heads > kMostHeads) return STEPQ_ERR_UNSUPPORTED;
   st = check_tensors(*d, q, q_stride, k, k_stride, v, v_stride, beta, gate, state, o, o_stride);
   if (st != STEPQ_OK) return st;
   if (!workspace || !aligned(workspace, 16) ||
@@ -95,7 +99,7 @@ stepq_status stepq_linear_step(const stepq_linear_desc* d, int32_t batch, const 
   if (batch < 0 || num_slots < 1) return STEPQ_ERR_INVALID_ARG;
   if (batch == 0) return STEPQ_OK;
   if (!slot_ids || !aligned(slot_ids, 4)) return STEPQ_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(batch) * d->num_heads * (d->d / 16) > 0x7fffffffLL) return STEPQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * d->num_heads > kMostHeads) return STEPQ_ERR_UNSUPPORTED;
   st = check_tensors(*d, q, q_stride, k, k_stride, v, v_stride, beta, gate, state, o, o_stride);
   if (st != STEPQ_OK) return st;
   stepq::LinearArgs a{};

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_chunks(LinearArgs p) {
 // A workgroup of up to four waves for 64 columns of a head.  Bound by the latency of a
 // chunk's chain of staging and dependent products: 3001 tokens of 5 requests, 12 heads
 // of 64, 134 us in all, some 6 us a chunk of the longest; one wave for 16 columns
-// instead, in four times as many workgroups, 172 against 167 us for this kernel.
+// instead, in four times as many workgroups, 172 against 131 us for this kernel.
 template <int D, typename T, bool DELTA, int NW>
 __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
   using S = Dims<D>;

@@ -107,6 +107,7 @@ def select_status(lib, batch=2, beams=4, vocab=100, n=4, logits=GOOD, dtype=0, s
     (dict(ws=None), 1), (dict(logits=GOOD + 2), 1), (dict(tokens=GOOD + 2), 1), (dict(stride=99), 1),
     (dict(dtype=1, logits=GOOD + 1), 1), (dict(nbytes=0), 1), (dict(nbytes=2 * 4 * 40 - 1), 1),
     (dict(beams=65), 2), (dict(n=65), 2), (dict(vocab=2 ** 31 - 1), 2), (dict(batch=2 ** 22, beams=8), 2),
+    (dict(batch=2 ** 23 + 1, beams=1), 2),
 ])
 def test_selection_arguments_that_are_refused(lib, bad, status):
     assert select_status(lib, **bad) == status

@@ -106,6 +106,9 @@ def test_prefill_sizes_beyond_the_grid_are_refused(lib):
     assert prefill_status(lib, desc(), tokens=1 << 31, nbytes=1 << 60) == S.STEPQ_ERR_UNSUPPORTED
     assert prefill_status(lib, desc(H=1 << 16, Hk=1), tokens=(1 << 31) - 1, nbytes=1 << 60) == S.STEPQ_ERR_UNSUPPORTED
     assert prefill_status(lib, desc(H=1 << 16, Hk=1, d=128), batch=1 << 13, tokens=0) == S.STEPQ_ERR_UNSUPPORTED
+    assert prefill_status(lib, desc(), tokens=1 << 28, nbytes=1 << 60) == S.STEPQ_ERR_UNSUPPORTED
+    assert step_status(lib, desc(H=1 << 10, Hk=1), batch=1 << 13, vs=1 << 15, os_=1 << 15) == S.STEPQ_ERR_UNSUPPORTED
+    assert prefill_status(lib, desc(), qs=(1 << 24) + 64, nbytes=1 << 60) == S.STEPQ_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad", [
