@@ -382,15 +382,13 @@ __global__ void __launch_bounds__(64 * NW) k_linear_walk(LinearArgs p) {
 //
 // Matrix products of 16-bit inputs run on bfloat16 matrix instructions, which
 // multiply exactly and add in binary32, sixteen times as fast as the binary32
-// ones.  A bfloat16 q, k or v is its own operand; a binary16 q or k is the sum of
+// ones.  A bfloat16 q, k or v is its own operand; a binary16 one is the sum of
 // two bfloat16 parts exactly (11 bits in 8 + 8).  Computed operands (state, A, the
-// system for U, its right sides) are split into two parts of 8 bits, which leaves
-// 2^-16 of the value at worst, 2^-18.7 on the average; what the additive rule adds to
-// the state, its only such rounding, is split into three, which leaves that of
-// binary32.  States come out within 6e-6 (delta) and 4e-7 (additive) of the recurrence
-// in 64 bits in the 2-norm, a tenth of what their 6- and 8-bit storage rounds away at
-// the least; three parts throughout do not fit the LDS of two workgroups.  One part
-// would do for most of a bfloat16 o, but not where its terms all but cancel.
+// system for U, U, what is added to the state) are binary32 values, the sum of
+// three parts exactly (24 bits in 8 + 8 + 8), and of a product of two such operands
+// the terms from 2^-24 on are left out: products are as good as binary32 ones.
+// (Two parts, 2^-18.7 of the value on the average, took 0.80 to 0.98 of the time and
+// left states of the delta rule 3e-6 to 5e-6 off in the 2-norm.)
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -411,6 +409,8 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
+
+constexpr int kParts = 3;      // of a binary32 value
 
 template <int NP>
 struct Parts {
@@ -456,12 +456,12 @@ __device__ __forceinline__ Parts<NP> parts_of(const f32x4& a, const f32x4& b) {
 }
 
 // Product of operands in NA and NB parts, every part 2^-8 of the one before, with the
-// terms above 2^(-8 ORDER).
-template <int ORDER, int NA, int NB>
+// terms above 2^-24.
+template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const Parts<NA>& a, const Parts<NB>& b, f32x4 c) {
   for (int i = NA - 1; i >= 0; --i)
     for (int j = NB - 1; j >= 0; --j)
-      if (i + j < ORDER) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
+      if (i + j < kParts) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
   return c;
 }
 
@@ -487,6 +487,7 @@ __device__ __forceinline__ int unit_at(int row, int unit) {
 // An operand (i, tb) of a lower triangle, i = 0 .. 3, tb <= i / 2, is 16 x 32: 16
 // bytes a lane, 1024 in all, in the order lanes hold it.
 constexpr int kTri = 6 * 1024;
+constexpr int kLds = 163840;      // bytes of a compute unit
 
 // Depth over key channels runs, within every 32, in their own order: a lane's eight
 // values of an operand are 16 consecutive bytes of a row.  So the 16 rows of state
@@ -530,16 +531,20 @@ __device__ __forceinline__ bf16x8 stored_operand(const uint8_t* x, int n, int la
 // Index of operand (i, tb) of a lower triangle.
 __device__ constexpr int tri(int i, int tb) { return i < 2 ? i : 2 * (i - 1) + tb; }
 
-// Half `half` of operand n of a triangle, in two parts.
-__device__ __forceinline__ void store_parts(uint8_t* hi, uint8_t* lo, int n, int half, const f32x4& x, int lane) {
+// Half `half` of operand n of a triangle, its parts kTri bytes apart.
+__device__ __forceinline__ void store_parts(uint8_t* x, int n, int half, f32x4 y, int lane) {
   const int at = n * 1024 + lane * 16 + half * 8;
-  const bf16x4 h = rounded(x);
-  *reinterpret_cast<bf16x4*>(hi + at) = h;
-  *reinterpret_cast<bf16x4*>(lo + at) = rounded(rest_of(x, h));
+  for (int p = 0; p < kParts; ++p) {
+    const bf16x4 h = rounded(y);
+    *reinterpret_cast<bf16x4*>(x + p * kTri + at) = h;
+    if (p + 1 < kParts) y = rest_of(y, h);
+  }
 }
 // Operand n of a triangle.
-__device__ __forceinline__ Parts<2> stored_parts(const uint8_t* hi, const uint8_t* lo, int n, int lane) {
-  return {{stored_operand(hi, n, lane), stored_operand(lo, n, lane)}};
+__device__ __forceinline__ Parts<kParts> stored_parts(const uint8_t* x, int n, int lane) {
+  Parts<kParts> r;
+  for (int p = 0; p < kParts; ++p) r.p[p] = stored_operand(x + p * kTri, n, lane);
+  return r;
 }
 
 __device__ __forceinline__ f32x4 floats_of(const s16x4& x, bf16) {
@@ -650,7 +655,7 @@ struct Scratch {
 };
 
 // Block (i, j) of A and of the system for U into LDS, one wave, both as operands in
-// two parts (`lt`, `la`: the larger, then the smaller ones).  With
+// parts (`lt`, `la`).  With
 // B = diag(b) B', U comes from block rows of 16 tokens in turn,
 //   U_i = D_i (R_i - sum_{j < i} B'_ij U_j),  D_i = (I + B_ii)^-1 diag(b_i),
 // so the system is stored as -B'_ij below the diagonal and D_i on it.  The inverse
@@ -670,8 +675,8 @@ __device__ __forceinline__ void chunk_tile(const uint8_t* lk, const uint8_t* lq,
       qi.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
       if constexpr (DELTA) ki.p[x] = DIAGONAL ? kj.p[x] : row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
     }
-    qk = mma<3>(kj, qi, qk);
-    if constexpr (DELTA) kk = mma<3>(kj, ki, kk);
+    qk = mma(kj, qi, qk);
+    if constexpr (DELTA) kk = mma(kj, ki, kk);
   }
   settle();
   const double li = r.lg[16 * i + c];
@@ -681,9 +686,9 @@ __device__ __forceinline__ void chunk_tile(const uint8_t* lk, const uint8_t* lq,
     ratio[e] = !DIAGONAL || 4 * g + e <= c ? x : 0.0f;
   }
   const int to = tri(i, j >> 1);
-  store_parts(la, la + kTri, to, j & 1, qk * ratio, lane);
+  store_parts(la, to, j & 1, qk * ratio, lane);
   if constexpr (DELTA && !DIAGONAL) {
-    store_parts(lt, lt + kTri, to, j & 1, -kk * ratio, lane);
+    store_parts(lt, to, j & 1, -kk * ratio, lane);
   } else if constexpr (DELTA) {
     // the wave's own LDS accesses are in order; of B only what is below the diagonal is read
     float* d = sc->diag[i];
@@ -707,11 +712,11 @@ __device__ __forceinline__ void chunk_tile(const uint8_t* lk, const uint8_t* lq,
     wave_order();
     const f32x4 inv = *reinterpret_cast<const f32x4*>(d + c * 20 + 4 * g) *
                       *reinterpret_cast<const f32x4*>(&r.beta[16 * i + 4 * g]);
-    store_parts(lt, lt + kTri, to, j & 1, inv, lane);
+    store_parts(lt, to, j & 1, inv, lane);
   }
   if (DIAGONAL && (i & 1) == 0) {      // beside the diagonal
-    store_parts(la, la + kTri, to, 1, f32x4{}, lane);
-    if constexpr (DELTA) store_parts(lt, lt + kTri, to, 1, f32x4{}, lane);
+    store_parts(la, to, 1, f32x4{}, lane);
+    if constexpr (DELTA) store_parts(lt, to, 1, f32x4{}, lane);
   }
   in_order();
 }
@@ -732,24 +737,29 @@ __device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq
 }
 
 // A (chunk, head) of the workspace of 16-bit inputs: G, G_C / G, A, the system for U.
-constexpr int block_bytes(bool delta) { return 2 * C * 4 + (delta ? 4 : 2) * kTri; }
+constexpr int block_bytes(bool delta) { return 2 * C * 4 + (delta ? 2 : 1) * kParts * kTri; }
 
 // LDS.  FUSED: `rates` for this chunk and the next one; HEAD: G, G_C / G, A and the
-// system lie as they do in the workspace.  For bfloat16 at D = 128 two FUSED
-// workgroups fit a compute unit with nothing to spare.
+// system lie as they do in the workspace.  V takes the place of Q, at the price of a
+// barrier, where two workgroups fit a compute unit only so (FUSED, delta rule: bfloat16
+// at D = 128, binary16 at D = 64).
 template <int D, typename T, bool DELTA, int COLS, bool FUSED, bool HEAD = !FUSED>
 struct Lds16 {
   using S = Dims16<D, T>;
   static constexpr int RBV = 2 * COLS < 64 ? 64 : 2 * COLS;      // bytes of a row of v
   static constexpr int K = 0;
   static constexpr int Q = K + S::NP * S::MAT;
-  static constexpr int V = Q + S::NP * S::MAT;
-  static constexpr int BLOCK = V + C * RBV;
+  static constexpr int REST = (HEAD ? 2 * C * 4 : 0) + (DELTA ? 2 : 1) * kParts * kTri +
+                              (FUSED ? 2 * static_cast<int>(sizeof(Rates)) + (DELTA ? static_cast<int>(sizeof(Scratch)) : 0) : 0);
+  static constexpr bool V_OVER_Q = FUSED && !HEAD && C * RBV <= S::NP * S::MAT &&
+                                   Q + S::NP * S::MAT + C * RBV + REST > kLds / 2 && Q + S::NP * S::MAT + REST <= kLds / 2;
+  static constexpr int V = V_OVER_Q ? Q : Q + S::NP * S::MAT;
+  static constexpr int BLOCK = Q + S::NP * S::MAT + (V_OVER_Q ? 0 : C * RBV);
   static constexpr int A = BLOCK + (HEAD ? 2 * C * 4 : 0);
-  static constexpr int TT = A + 2 * kTri;
-  static constexpr int RATES = TT + (DELTA ? 2 * kTri : 0);
+  static constexpr int TT = A + kParts * kTri;
+  static constexpr int RATES = TT + (DELTA ? kParts * kTri : 0);
   static constexpr int SCRATCH = RATES + 2 * static_cast<int>(sizeof(Rates));
-  static constexpr int BYTES = FUSED ? SCRATCH + (DELTA ? static_cast<int>(sizeof(Scratch)) : 0) : RATES;
+  static constexpr int BYTES = BLOCK + REST;
 };
 
 // Workgroups are dealt out to the chip's 8 dies in turn, each with an L2 of its own.
@@ -826,7 +836,7 @@ __device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lan
 // segments start from, and PASS 2 computes the outputs.  One 16384-token prompt of
 // 32 heads: 983 us in 256 chunks one after another, 261 us in segments.
 //
-// At D = 128 the delta rule takes 292 matrix instructions of 16 cycles a chunk from
+// At D = 128 the delta rule takes 456 matrix instructions of 16 cycles a chunk from
 // each of four waves with 32 columns (fewer, wider waves read q and k from LDS half as
 // often as eight with 16, and those spilled: 381 us against 225 for 512 pairs of 1024
 // tokens); the additive rule fits 128 registers with eight waves (157 against 162 us).
@@ -839,6 +849,7 @@ template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED, int PASS>
 __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 : 1) k_linear16_walk(LinearArgs p) {
   using S = Dims16<D, T>;
   constexpr int NP = S::NP;
+  constexpr int UP = DELTA ? kParts : NP;      // the additive rule's U is V as it came
   constexpr int COLS = 16 * NCT * NW;
   constexpr int THREADS = 64 * NW;
   using L = Lds16<D, T, DELTA, COLS, FUSED>;
@@ -972,28 +983,27 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     if constexpr (PASS != 1) {
     const At at = lane_at<S::RB>(fresh(lane));
     for (int kb = 0; kb < S::KB; ++kb) {
-      Parts<2> mf[NCT];
-      for (int n = 0; n < NCT; ++n) {
-        mf[n] = parts_of<2>(m[n][2 * kb], m[n][2 * kb + 1]);
-      }
+      Parts<kParts> mf[NCT];
+      for (int n = 0; n < NCT; ++n) mf[n] = parts_of<kParts>(m[n][2 * kb], m[n][2 * kb + 1]);
       for (int i = 0; i < 4; ++i) {
         Parts<NP> a;
         if constexpr (DELTA) {
           for (int x = 0; x < NP; ++x) a.p[x] = row_operand<S::RB>(lk + x * S::MAT, i, kb, at);
-          for (int n = 0; n < NCT; ++n) u[n][i] = mma<3>(a, mf[n], u[n][i]);
+          for (int n = 0; n < NCT; ++n) u[n][i] = mma(a, mf[n], u[n][i]);
         }
         for (int x = 0; x < NP; ++x) a.p[x] = row_operand<S::RB>(lq + x * S::MAT, i, kb, at);
-        for (int n = 0; n < NCT; ++n) y[n][i] = mma<2>(mf[n], a, y[n][i]);
+        for (int n = 0; n < NCT; ++n) y[n][i] = mma(mf[n], a, y[n][i]);
       }
       in_order();
     }
     }
     settle();
     if constexpr (FUSED) {
+      if constexpr (L::V_OVER_Q) __syncthreads();      // Q has been read
       vr.template store<false>(lv, count, fresh(tid));
       __syncthreads();      // V, A and the system for U
     }
-    Parts<2> uf[NCT][2];
+    Parts<UP> uf[NCT][2];
     {
       const int l = fresh(lane), g = l >> 4;
       for (int n = 0; n < NCT; ++n)
@@ -1004,25 +1014,25 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
         }
       const f32x4 none = {};
       if constexpr (DELTA) {
-        Parts<2> s = stored_parts(lt, lt + kTri, tri(0, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][0] = mma<3>(s, parts_of<2>(u[n][0], none), none);
-        s = stored_parts(lt, lt + kTri, tri(1, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][1] = mma<3>(s, parts_of<2>(u[n][0], none), u[n][1]);
-        for (int n = 0; n < NCT; ++n) u[n][1] = mma<3>(s, parts_of<2>(none, u[n][1]), none);
-        for (int n = 0; n < NCT; ++n) uf[n][0] = parts_of<2>(u[n][0], u[n][1]);
-        s = stored_parts(lt, lt + kTri, tri(2, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][2] = mma<3>(s, uf[n][0], u[n][2]);
-        s = stored_parts(lt, lt + kTri, tri(3, 0), l);
-        for (int n = 0; n < NCT; ++n) u[n][3] = mma<3>(s, uf[n][0], u[n][3]);
-        s = stored_parts(lt, lt + kTri, tri(2, 1), l);
-        for (int n = 0; n < NCT; ++n) u[n][2] = mma<3>(s, parts_of<2>(u[n][2], none), none);
-        s = stored_parts(lt, lt + kTri, tri(3, 1), l);
-        for (int n = 0; n < NCT; ++n) u[n][3] = mma<3>(s, parts_of<2>(u[n][2], none), u[n][3]);
-        for (int n = 0; n < NCT; ++n) u[n][3] = mma<3>(s, parts_of<2>(none, u[n][3]), none);
-        for (int n = 0; n < NCT; ++n) uf[n][1] = parts_of<2>(u[n][2], u[n][3]);
+        Parts<kParts> s = stored_parts(lt, tri(0, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][0] = mma(s, parts_of<kParts>(u[n][0], none), none);
+        s = stored_parts(lt, tri(1, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<kParts>(u[n][0], none), u[n][1]);
+        for (int n = 0; n < NCT; ++n) u[n][1] = mma(s, parts_of<kParts>(none, u[n][1]), none);
+        for (int n = 0; n < NCT; ++n) uf[n][0] = parts_of<kParts>(u[n][0], u[n][1]);
+        s = stored_parts(lt, tri(2, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, uf[n][0], u[n][2]);
+        s = stored_parts(lt, tri(3, 0), l);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, uf[n][0], u[n][3]);
+        s = stored_parts(lt, tri(2, 1), l);
+        for (int n = 0; n < NCT; ++n) u[n][2] = mma(s, parts_of<kParts>(u[n][2], none), none);
+        s = stored_parts(lt, tri(3, 1), l);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, parts_of<kParts>(u[n][2], none), u[n][3]);
+        for (int n = 0; n < NCT; ++n) u[n][3] = mma(s, parts_of<kParts>(none, u[n][3]), none);
+        for (int n = 0; n < NCT; ++n) uf[n][1] = parts_of<kParts>(u[n][2], u[n][3]);
       } else {
         for (int n = 0; n < NCT; ++n)
-          for (int tb = 0; tb < 2; ++tb) uf[n][tb] = parts_of<2>(u[n][2 * tb], u[n][2 * tb + 1]);
+          for (int tb = 0; tb < 2; ++tb) uf[n][tb] = parts_of<UP>(u[n][2 * tb], u[n][2 * tb + 1]);
       }
       in_order();
     }
@@ -1032,8 +1042,8 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
         const float f = grow[16 * i + cl];
         for (int n = 0; n < NCT; ++n) y[n][i] *= f;
         for (int tb = 0; tb <= i / 2; ++tb) {
-          const Parts<2> a = stored_parts(la, la + kTri, tri(i, tb), l);
-          for (int n = 0; n < NCT; ++n) y[n][i] = mma<2>(uf[n][tb], a, y[n][i]);
+          const Parts<kParts> a = stored_parts(la, tri(i, tb), l);
+          for (int n = 0; n < NCT; ++n) y[n][i] = mma(uf[n][tb], a, y[n][i]);
         }
       }
       settle();
@@ -1050,20 +1060,19 @@ __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 
     in_order();
     const int l = fresh(lane), g = l >> 4;
     const At at = lane_at<S::RB>(l);
-    constexpr int WP = DELTA ? 2 : 3;
-    Parts<WP> wf[NCT][2];
+    Parts<kParts> wf[NCT][2];
     const float all = grow[C - 1];
     faded *= all;
     for (int n = 0; n < NCT; ++n)
       for (int tb = 0; tb < 2; ++tb)
-        wf[n][tb] = parts_of<WP>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 4 * g]),
+        wf[n][tb] = parts_of<kParts>(u[n][2 * tb] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 4 * g]),
                                 u[n][2 * tb + 1] * *reinterpret_cast<const f32x4*>(&left[32 * tb + 16 + 4 * g]));
     for (int i = 0; i < S::RT; ++i) {
       for (int n = 0; n < NCT; ++n) m[n][i] *= all;
       for (int tb = 0; tb < 2; ++tb) {
         Parts<NP> a;
         for (int x = 0; x < NP; ++x) a.p[x] = column_operand<S::RB>(lk + x * S::MAT, tb, i, at);
-        for (int n = 0; n < NCT; ++n) m[n][i] = mma<3>(a, wf[n][tb], m[n][i]);
+        for (int n = 0; n < NCT; ++n) m[n][i] = mma(a, wf[n][tb], m[n][i]);
       }
       if (i % 2) in_order();
     }
@@ -1225,7 +1234,7 @@ hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
                                   Lds16<D, T, DELTA, 16, true, true>::BYTES, a, s);
   if (e != hipSuccess) return e;
   // as few columns a workgroup as the chip holds workgroups for at once
-  const auto held = [](int lds) { return static_cast<int64_t>(256) * (163840 / lds); };
+  const auto held = [](int lds) { return static_cast<int64_t>(256) * (kLds / lds); };
   if (D == 16 || tiles * (D / 16) <= held(Lds16<D, T, DELTA, 16, false>::BYTES)) return walk16<D, T, DELTA, 1, 1, false>(a, s);
   if constexpr (D >= 64) {
     if (tiles * (D / 32) > held(Lds16<D, T, DELTA, 32, false>::BYTES)) return walk16<D, T, DELTA, 1, 4, false>(a, s);
