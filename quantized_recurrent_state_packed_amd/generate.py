@@ -68,9 +68,23 @@ class BeamGenerator:
         self.pools = [layout.alloc(batch * beams, device=device) for _ in range(model.layers)]
         self.device = device
 
+    def _check_prompts(self, prompts) -> None:
+        def refuse(detail):
+            raise S.StepqError(S.STEPQ_ERR_INVALID_ARG, "BeamGenerator", detail)
+
+        if len(prompts) != self.batch:
+            refuse(f"{len(prompts)} prompts for a batch of {self.batch}")
+        for b, p in enumerate(prompts):
+            if len(p) == 0:       # the first choice is made from the last token's logits
+                refuse(f"request {b}'s prompt is empty")
+            if min(p) < 0 or max(p) >= self.model.vocab:
+                refuse(f"request {b}'s prompt has tokens outside of the vocabulary of {self.model.vocab}")
+
     def prefill(self, prompts):
-        """Prompts (lists of tokens) into the first slot of every request; the last tokens' logits [batch, vocab]."""
+        """Prompts (non-empty lists of tokens, one a request) into the first slot of every
+        request; the last tokens' logits [batch, vocab]."""
         import torch
+        self._check_prompts(prompts)
         lengths = [len(p) for p in prompts]
         cu = torch.tensor(np.r_[0, np.cumsum(lengths)], dtype=torch.int32, device=self.device)
         tokens = torch.tensor([t for p in prompts for t in p], device=self.device)
