@@ -59,8 +59,8 @@ stepq_status stepq_beam_select(int32_t batch, int32_t beams, int32_t vocab, int3
   a.eos = eos_token;
   a.parts = stepq::select_parts(static_cast<int64_t>(batch) * beams, vocab);
   // a row is read from the 16-byte boundary at or below its start
-  const int32_t all = (vocab + static_cast<int32_t>(16 / e) - 1 + stepq::kTile - 1) / stepq::kTile;
-  a.tiles = (all + a.parts - 1) / a.parts;
+  const int64_t all = (static_cast<int64_t>(vocab) + static_cast<int64_t>(16 / e) - 1 + stepq::kTile - 1) / stepq::kTile;
+  a.tiles = static_cast<int32_t>((all + a.parts - 1) / a.parts);
   return from_hip(stepq::launch_beam_select(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
