@@ -87,6 +87,7 @@ stepq_status stepq_linear_prefill(const stepq_linear_desc* d, int32_t batch, int
   a.H = d->num_heads; a.rep = d->num_heads / d->num_qk_heads;
   a.workspace = static_cast<uint8_t*>(workspace);
   a.segment = stepq::segment_chunks(*d, total_tokens, batch);
+  a.apart = stepq::chunks_apart(*d, total_tokens, batch);
   return from_hip(stepq::launch_linear_prefill(*d, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -410,8 +410,6 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-constexpr int kParts = 3;      // of a binary32 value
-
 template <int NP>
 struct Parts {
   bf16x8 p[NP];
@@ -485,9 +483,7 @@ __device__ __forceinline__ int unit_at(int row, int unit) {
 }
 
 // An operand (i, tb) of a lower triangle, i = 0 .. 3, tb <= i / 2, is 16 x 32: 16
-// bytes a lane, 1024 in all, in the order lanes hold it.
-constexpr int kTri = 6 * 1024;
-constexpr int kLds = 163840;      // bytes of a compute unit
+// bytes a lane, 1024 in all (kTri for a triangle), in the order lanes hold it.
 
 // Depth over key channels runs, within every 32, in their own order: a lane's eight
 // values of an operand are 16 consecutive bytes of a row.  So the 16 rows of state
@@ -735,9 +731,6 @@ __device__ __forceinline__ void chunk_tiles(const uint8_t* lk, const uint8_t* lq
     if (w < 2) chunk_tile<D, T, DELTA, false>(lk, lq, r, sc, la, lt, w == 0 ? 2 : 3, w, lane);
   }
 }
-
-// A (chunk, head) of the workspace of 16-bit inputs: G, G_C / G, A, the system for U.
-constexpr int block_bytes(bool delta) { return 2 * C * 4 + (delta ? 2 : 1) * kParts * kTri; }
 
 // LDS.  FUSED: `rates` for this chunk and the next one; HEAD: G, G_C / G, A and the
 // system lie as they do in the workspace.  V takes the place of Q, at the price of a
@@ -1212,15 +1205,20 @@ hipError_t walk16(const LinearArgs& a, hipStream_t s) {
                     Lds16<D, T, DELTA, COLS, FUSED>::BYTES, a, s);
 }
 
+// The walk apart from its chunk matrices, 16 NW columns a workgroup; `waves` is that NW.
+template <int D, typename T, bool DELTA, int NW>
+hipError_t walk_apart(int waves, const LinearArgs& a, hipStream_t s) {
+  static_assert(Lds16<D, T, DELTA, 16 * NW, false>::BYTES == apart_lds(D, Dims16<D, T>::NP, DELTA, NW), "one rule for both");
+  constexpr int64_t most = D < 64 ? INT32_MAX : kMostApart;
+  if constexpr (apart_waves(D, Dims16<D, T>::NP, DELTA, most) > NW) {
+    if (waves > NW) return walk_apart<D, T, DELTA, 2 * NW>(waves, a, s);
+  }
+  return walk16<D, T, DELTA, 1, NW, false>(a, s);
+}
+
 template <int D, typename T, bool DELTA>
 hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
   const int64_t tiles = static_cast<int64_t>(a.batch) * a.H;
-  if constexpr (D >= 64) {
-    // one launch also for prompts of a chunk or less: 37 tokens of 48 heads 11.5 us a call
-    // against 14.7 in two
-    if (tiles >= kFullChip || a.total_tokens <= static_cast<int64_t>(C) * a.batch)
-      return walk16<D, T, DELTA, DELTA ? D / 64 : 1, DELTA ? 4 : D / 16, true>(a, s);
-  }
   if constexpr (D >= 64 && !DELTA) {
     if (a.segment > 0) {
       hipError_t e = walk16<D, T, false, 1, D / 16, true, 1>(a, s);
@@ -1230,16 +1228,14 @@ hipError_t prefill16(const LinearArgs& a, hipStream_t s) {
       return e != hipSuccess ? e : walk16<D, T, false, 1, D / 16, true, 2>(a, s);
     }
   }
-  const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, max_chunks(a.total_tokens, a.batch) * a.H, kThreads,
-                                  Lds16<D, T, DELTA, 16, true, true>::BYTES, a, s);
-  if (e != hipSuccess) return e;
-  // as few columns a workgroup as the chip holds workgroups for at once
-  const auto held = [](int lds) { return static_cast<int64_t>(256) * (kLds / lds); };
-  if (D == 16 || tiles * (D / 16) <= held(Lds16<D, T, DELTA, 16, false>::BYTES)) return walk16<D, T, DELTA, 1, 1, false>(a, s);
-  if constexpr (D >= 64) {
-    if (tiles * (D / 32) > held(Lds16<D, T, DELTA, 32, false>::BYTES)) return walk16<D, T, DELTA, 1, 4, false>(a, s);
+  if constexpr (ever_apart(D, DELTA)) {
+    if (a.apart) {
+      const hipError_t e = launch_lds(k_linear16_chunks<D, T, DELTA>, max_chunks(a.total_tokens, a.batch) * a.H, kThreads,
+                                      Lds16<D, T, DELTA, 16, true, true>::BYTES, a, s);
+      return e != hipSuccess ? e : walk_apart<D, T, DELTA, 1>(apart_waves(D, Dims16<D, T>::NP, DELTA, tiles), a, s);
+    }
   }
-  if constexpr (D >= 32) return walk16<D, T, DELTA, 1, 2, false>(a, s);
+  if constexpr (D >= 64) return walk16<D, T, DELTA, DELTA ? D / 64 : 1, DELTA ? 4 : D / 16, true>(a, s);
   return hipErrorInvalidValue;
 }
 
@@ -1274,12 +1270,6 @@ hipError_t step_t(int d, const LinearArgs& a, hipStream_t s) {
 }
 
 }  // namespace
-
-size_t chunk_bytes(int rule, int dtype) {
-  const bool delta = rule == STEPQ_RULE_DELTA;
-  if (dtype == STEPQ_F32) return sizeof(float) * ((delta ? 2 : 1) * C * C + 2 * C);
-  return block_bytes(delta);
-}
 
 hipError_t launch_linear_prefill(const stepq_linear_desc& d, const LinearArgs& a, hipStream_t s) {
   switch (d.dtype) {

@@ -1,0 +1,94 @@
+"""The variants of the prefill of 16-bit inputs: each is reached by some call, none
+is built that no call reaches, and each gives the recurrence's result, on both
+sides of every number of (request, head) pairs where another one takes over."""
+import re
+import subprocess
+
+import numpy as np
+import pytest
+
+from quantized_recurrent_state_packed_amd import build_lib
+from quantized_recurrent_state_packed_amd import stepq as S
+from test_linear import OUT_TOL, Run, far
+from test_linear_precision import STATE
+from test_seq_host import run
+
+
+def test_the_library_holds_the_variants_that_calls_reach_and_no_others(tmp_path):
+    reached = set(run(tmp_path, "linear_host.cpp", "linear_api.cpp").splitlines())
+    if not S.LIB_PATH.exists():
+        build_lib.build()
+    names = subprocess.run(["nm", str(S.LIB_PATH)], capture_output=True, text=True, check=True).stdout
+    parts = {"DF16b": 1, "DF16_": 2}
+    built = {f"walk {d} {parts[t]} {delta} {tiles} {waves} {one} {p}" for d, t, delta, tiles, waves, one, p in re.findall(
+        r"k_linear16_walkILi(\d+)E(DF16b|DF16_)Lb([01])ELi(\d+)ELi(\d+)ELb([01])ELi(\d+)E", names)}
+    built |= {f"chunks {d} {parts[t]} {delta}" for d, t, delta in re.findall(
+        r"k_linear16_chunksILi(\d+)E(DF16b|DF16_)Lb([01])E", names)}
+    assert built and built == reached
+
+
+def recurrence64(r, resume):
+    """o and the requests' states by the recurrence in binary64 on the GPU, all requests' tokens in step."""
+    import torch
+    n = torch.tensor(r.lengths, device="cuda")
+    first = torch.from_numpy(r.cu[:-1].astype(np.int64)).cuda()
+    rep = r.H // r.q.shape[1]
+    m = torch.from_numpy(r.before[r.slots]).cuda().double()
+    m *= torch.tensor(resume, device="cuda", dtype=torch.float64)[:, None, None, None]
+    o = torch.zeros(r.v.shape, device="cuda", dtype=torch.float64)
+    for t in range(max(r.lengths)):
+        live = (n > t).nonzero()[:, 0]
+        at = first[live] + t
+        k, q = (x[at].double().repeat_interleave(rep, 1) for x in (r.k, r.q))
+        mt = m[live] * r.gate[at].double()[:, :, None, None]
+        u = r.v[at].double()
+        if r.beta is not None:
+            u = r.beta[at].double()[..., None] * (u - (mt * k[..., None]).sum(-2))
+        mt += k[..., None] * u[:, :, None, :]
+        o[at] = (mt * q[..., None]).sum(-2)
+        m[live] = mt
+    return o, m
+
+
+def check(r, resume):
+    ro, rm = recurrence64(r, resume)
+    r.prefill(resume)
+    slots = r.slots.tolist()
+    state = r.state.double().cpu().numpy()
+    o, ro, rm = r.o.double().cpu().numpy(), ro.cpu().numpy(), rm.cpu().numpy()
+    for b, slot in enumerate(slots):
+        at = slice(r.cu[b], r.cu[b + 1])
+        assert far(state[slot], rm[b]) <= STATE, b
+        for h in range(r.H):
+            if r.lengths[b]:
+                assert far(o[at][:, h], ro[at][:, h]) <= OUT_TOL[r.dtype], (b, h)
+    rest = [s for s in range(r.num_slots) if s not in set(slots)]
+    assert np.array_equal(r.state.cpu().numpy()[rest], r.before[rest])
+    assert bool((r.untouched == 7.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", ["delta", "additive"])
+@pytest.mark.parametrize("dtype,D,heads,batch", [
+    ("bf16", 128, 16, 2), ("bf16", 128, 32, 2), ("bf16", 128, 13, 5), ("bf16", 128, 32, 3), ("bf16", 128, 64, 2),
+    ("bf16", 128, 43, 3), ("bf16", 128, 50, 4),
+    ("f16", 128, 16, 2), ("f16", 128, 11, 3), ("f16", 128, 32, 2), ("f16", 128, 13, 5), ("f16", 128, 32, 3), ("f16", 128, 64, 2),
+    ("f16", 128, 43, 3), ("f16", 128, 50, 4),
+    ("bf16", 64, 40, 1), ("bf16", 64, 43, 3), ("f16", 64, 43, 3), ("f16", 64, 50, 5),
+    ("f16", 32, 64, 4), ("f16", 32, 43, 6), ("bf16", 32, 64, 6), ("bf16", 32, 77, 5), ("bf16", 32, 64, 13), ("f16", 32, 64, 11),
+    ("bf16", 16, 64, 13), ("f16", 16, 43, 3)])
+def test_numbers_of_pairs(dtype, D, heads, batch, rule):
+    g = np.random.default_rng(heads * batch)
+    lengths = [int(x) for x in g.choice([70, 129, 200, 33, 1, 64], size=batch)]
+    lengths[0] = 200
+    r = Run(dtype, heads, heads if heads % 2 else heads // 2, D, rule, lengths, seed=batch, fused=heads == 32)
+    check(r, [b % 2 for b in range(batch)])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,heads,lengths", [(128, 96, [2900]), (64, 128, [2300]), (128, 40, [3000, 10, 5001]), (64, 60, [4001, 0, 700])],
+                         ids=str)
+def test_segments_of_more_than_four_chunks(dtype, D, heads, lengths):
+    r = Run(dtype, heads, heads // 2, D, "additive", lengths, seed=heads)
+    check(r, [1] + [0] * (len(lengths) - 1))
