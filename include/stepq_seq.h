@@ -54,9 +54,15 @@ typedef struct {
   int32_t dtype;         /* stepq_dtype of q, k, v and o */
 } stepq_linear_desc;
 
-/* Bytes stepq_linear_prefill needs as workspace for up to `batch` requests of
- * `total_tokens` tokens together; 0 for an invalid desc or a negative size. */
+/* Bytes that are enough as stepq_linear_prefill's workspace for every call of up to
+ * `batch` requests of up to `total_tokens` tokens together; 0 where no such call
+ * needs one, for an invalid desc or a negative size. */
 size_t stepq_linear_workspace_bytes(const stepq_linear_desc *desc, int32_t batch, int64_t total_tokens);
+
+/* Bytes stepq_linear_prefill asks for in a call of exactly these sizes; 0 for a call
+ * that runs in one launch, as those of 16-bit inputs at d = 64 and 128 with many
+ * (request, head) pairs do (the workspace may then be NULL). */
+size_t stepq_linear_prefill_bytes(const stepq_linear_desc *desc, int32_t batch, int64_t total_tokens);
 
 /* Prompts.  Request b's tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of
  * q, k, v, o, beta and gate (device int32 [batch+1], non-decreasing, within

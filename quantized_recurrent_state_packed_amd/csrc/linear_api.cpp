@@ -49,10 +49,12 @@ extern "C" {
 
 size_t stepq_linear_workspace_bytes(const stepq_linear_desc* d, int32_t batch, int64_t total_tokens) {
   if (check_desc(d) != STEPQ_OK || batch < 0 || total_tokens < 0 || total_tokens > 0x7fffffffLL) return 0;
-  const size_t chunks = static_cast<size_t>(stepq::max_chunks(total_tokens, batch)) * d->num_heads *
-                        stepq::chunk_bytes(d->rule, d->dtype);
-  const size_t segments = stepq::segment_workspace_bytes(*d, total_tokens, batch);
-  return chunks > segments ? chunks : segments;
+  return stepq::most_workspace(*d, total_tokens, batch);
+}
+
+size_t stepq_linear_prefill_bytes(const stepq_linear_desc* d, int32_t batch, int64_t total_tokens) {
+  if (check_desc(d) != STEPQ_OK || batch < 1 || total_tokens < 0 || total_tokens > 0x7fffffffLL) return 0;
+  return stepq::call_workspace(*d, total_tokens, batch);
 }
 
 stepq_status stepq_linear_prefill(const stepq_linear_desc* d, int32_t batch, int64_t total_tokens,
@@ -74,9 +76,8 @@ stepq_status stepq_linear_prefill(const stepq_linear_desc* d, int32_t batch, int
   if (static_cast<int64_t>(batch) * d->num_heads > kMostHeads) return STEPQ_ERR_UNSUPPORTED;
   st = check_tensors(*d, q, q_stride, k, k_stride, v, v_stride, beta, gate, state, o, o_stride);
   if (st != STEPQ_OK) return st;
-  if (!workspace || !aligned(workspace, 16) ||
-      workspace_bytes < stepq_linear_workspace_bytes(d, batch, total_tokens))
-    return STEPQ_ERR_INVALID_ARG;
+  const size_t need = stepq::call_workspace(*d, total_tokens, batch);
+  if ((need > 0 && !workspace) || !aligned(workspace, 16) || workspace_bytes < need) return STEPQ_ERR_INVALID_ARG;
   stepq::LinearArgs a{};
   a.q = q; a.k = k; a.v = v;
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;

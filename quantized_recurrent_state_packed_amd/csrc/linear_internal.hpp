@@ -115,20 +115,37 @@ inline int64_t max_segments(int64_t total_tokens, int32_t batch, int32_t segment
 }
 constexpr int kSegmentHead = 16;   // floats after a segment's state: its retention, and padding
 
-// Workspace bytes for segments of any call of up to these sizes.
-inline size_t segment_workspace_bytes(const stepq_linear_desc& d, int64_t total_tokens, int32_t batch) {
-  if (d.rule != STEPQ_RULE_ADDITIVE || d.dtype == STEPQ_F32 || d.d < 64) return 0;
-  const int64_t wanted = (768 + d.num_heads - 1) / d.num_heads, all = total_tokens / (4 * kChunk);
-  const int64_t few = most_segmented(d.d) / d.num_heads + 1;
-  const int64_t segments = (all < wanted ? all : wanted) + (batch < few ? batch : few);
-  return static_cast<size_t>(segments) * d.num_heads * (static_cast<size_t>(d.d) * d.d + kSegmentHead) * sizeof(float);
-}
-
 // Workspace bytes of one (chunk, value head).
 inline size_t chunk_bytes(int rule, int dtype) {
   const bool delta = rule == STEPQ_RULE_DELTA;
   if (dtype == STEPQ_F32) return sizeof(float) * ((delta ? 2 : 1) * kChunk * kChunk + 2 * kChunk);
   return block_bytes(delta);
+}
+
+inline size_t chunks_workspace(const stepq_linear_desc& d, int64_t total_tokens, int64_t batch) {
+  return static_cast<size_t>(total_tokens / kChunk + batch) * d.num_heads * chunk_bytes(d.rule, d.dtype);
+}
+inline size_t segments_workspace(const stepq_linear_desc& d, int64_t segments) {
+  return static_cast<size_t>(segments) * d.num_heads * (static_cast<size_t>(d.d) * d.d + kSegmentHead) * sizeof(float);
+}
+
+// Workspace bytes of a call of these sizes.
+inline size_t call_workspace(const stepq_linear_desc& d, int64_t total_tokens, int32_t batch) {
+  const int32_t segment = segment_chunks(d, total_tokens, batch);
+  if (segment > 0) return segments_workspace(d, max_segments(total_tokens, batch, segment));
+  return chunks_apart(d, total_tokens, batch) ? chunks_workspace(d, total_tokens, batch) : 0;
+}
+
+// Workspace bytes that are enough for any call of up to these sizes: of those that use
+// one, the one of the most requests.
+inline size_t most_workspace(const stepq_linear_desc& d, int64_t total_tokens, int32_t batch) {
+  const bool delta = d.rule == STEPQ_RULE_DELTA;
+  const auto fewer = [&](int64_t pairs) { return batch < pairs / d.num_heads ? batch : pairs / d.num_heads; };
+  if (d.dtype == STEPQ_F32 || d.d < 64) return chunks_workspace(d, total_tokens, batch);
+  if (delta) return ever_apart(d.d, delta) && fewer(kMostApart) > 0 ? chunks_workspace(d, total_tokens, fewer(kMostApart)) : 0;
+  const int64_t few = fewer(most_segmented(d.d)), wanted = (768 + d.num_heads - 1) / d.num_heads;
+  const int64_t all = total_tokens / (4 * kChunk);
+  return few > 0 ? segments_workspace(d, (all < wanted ? all : wanted) + few) : 0;
 }
 
 hipError_t launch_linear_prefill(const stepq_linear_desc& d, const LinearArgs& a, hipStream_t s);

@@ -19,7 +19,7 @@ STEPQ_F16 = 2
 RULE_ADDITIVE = 0
 RULE_DELTA = 1
 
-EXPORTED = ("stepq_linear_workspace_bytes", "stepq_linear_prefill", "stepq_linear_step")
+EXPORTED = ("stepq_linear_workspace_bytes", "stepq_linear_prefill_bytes", "stepq_linear_prefill", "stepq_linear_step")
 
 _RULES = {"additive": RULE_ADDITIVE, "delta": RULE_DELTA}
 
@@ -39,6 +39,8 @@ def lib() -> ctypes.CDLL:
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         L.stepq_linear_workspace_bytes.restype = sz
         L.stepq_linear_workspace_bytes.argtypes = [P, i32, i64]
+        L.stepq_linear_prefill_bytes.restype = sz
+        L.stepq_linear_prefill_bytes.argtypes = [P, i32, i64]
         L.stepq_linear_prefill.restype = ctypes.c_int
         L.stepq_linear_prefill.argtypes = [P, i32, i64, P, P, i64, P, i64, P, i64, P, P, P, i32, P, P, P, i64, P,
                                            sz, P]
@@ -122,7 +124,7 @@ class LinearAttention:
         return int(lib().stepq_linear_workspace_bytes(self._desc, int(batch), int(total_tokens)))
 
     def workspace(self, batch: int, total_tokens: int, device="cuda"):
-        """A workspace for prompts of up to `total_tokens` tokens of up to `batch` requests."""
+        """A workspace for calls of up to `batch` requests of up to `total_tokens` tokens together."""
         import torch
         return torch.empty(max(16, self.workspace_bytes(batch, total_tokens)), dtype=torch.uint8, device=device)
 
@@ -177,8 +179,8 @@ class LinearAttention:
                 stream=None) -> None:
         """stepq_linear_prefill: prompts of ragged lengths; request b's tokens are rows
         cu_seqlens[b] .. cu_seqlens[b+1]-1.  Writes o and the slots of state.  The
-        workspace may be kept between calls (see workspace()); without one, memory
-        is taken from torch's allocator for this call, on the current stream."""
+        workspace may be kept between calls (see workspace()); without one, what this
+        call needs, if anything, is taken from torch's allocator, on the current stream."""
         import torch
         where = "stepq_linear_prefill"
         batch, tokens = slot_ids.shape[0], v.shape[0]
@@ -197,18 +199,20 @@ class LinearAttention:
         if batch == 0:
             return
         if workspace is None:
-            if stream is not None:
-                _refuse(where, "a call on another stream needs a workspace of its own")
-            workspace = self.workspace(batch, tokens, device=state.device)
+            need = lib().stepq_linear_prefill_bytes(self._desc, batch, tokens)
+            if need > 0:
+                if stream is not None:
+                    _refuse(where, "a call on another stream needs a workspace of its own")
+                workspace = torch.empty(need, dtype=torch.uint8, device=state.device)
         if tokens == 0:          # empty tensors have no address; every request is empty
-            q = k = v = o = gate = workspace
-            beta = None if self.rule == "additive" else workspace
+            q = k = v = o = gate = state
+            beta = None if self.rule == "additive" else state
             qs = ks = self._qk_row
             vs = os_ = self._v_row
         p = _s._ptr
         _s._check(lib().stepq_linear_prefill(self._desc, batch, tokens, p(cu_seqlens), p(q), qs, p(k), ks, p(v), vs,
                                              p(beta), p(gate), p(slot_ids), state.shape[0], p(resume), p(state), p(o),
-                                             os_, p(workspace), workspace.numel(),
+                                             os_, p(workspace), 0 if workspace is None else workspace.numel(),
                                              stream_of(stream, state.get_device())), where)
 
     def step(self, slot_ids, q, k, v, beta, gate, state, o, stream=None) -> None:

@@ -50,10 +50,20 @@ int main() {
             for (int64_t tokens : {0, 37, 64, 65, 700, 5000, 40000, 1000000}) {
               const stepq_linear_desc desc = {heads, heads, d, rule, dtype};
               const int64_t row = static_cast<int64_t>(heads) * d;
-              const size_t bytes = stepq_linear_workspace_bytes(&desc, batch, tokens);
-              const stepq_status s = stepq_linear_prefill(&desc, batch, tokens, ints, any, row, any, row, any, row,
-                                                          rule == STEPQ_RULE_DELTA ? floats : nullptr, floats, ints, batch,
-                                                          nullptr, floats, any, row, any, bytes, nullptr);
+              const auto call = [&](void* workspace, size_t bytes) {
+                return stepq_linear_prefill(&desc, batch, tokens, ints, any, row, any, row, any, row,
+                                            rule == STEPQ_RULE_DELTA ? floats : nullptr, floats, ints, batch, nullptr, floats,
+                                            any, row, workspace, bytes, nullptr);
+              };
+              const size_t bytes = stepq_linear_prefill_bytes(&desc, batch, tokens);
+              const stepq_status s = call(bytes ? any : nullptr, bytes);
+              if (bytes && (call(any, bytes - 1) != STEPQ_ERR_INVALID_ARG || call(nullptr, bytes) != STEPQ_ERR_INVALID_ARG))
+                return std::printf("too little was accepted\n"), 1;
+              for (int b = batch; b <= batch + 40; b += 13)        // a workspace for more is enough
+                for (int64_t t : {tokens, tokens + 1, tokens + 64, tokens + 100000})
+                  if (stepq_linear_workspace_bytes(&desc, b, t) < bytes) return std::printf("not enough for fewer\n"), 1;
+              const bool one_launch = dtype != STEPQ_F32 && d >= 64 && batch * heads > 255;
+              if (one_launch && bytes) return std::printf("one launch asks for %zu bytes\n", bytes), 1;
               const int32_t segment = stepq::segment_chunks(desc, tokens, batch);
               if (s != STEPQ_OK || (segment > 0 && static_cast<size_t>(stepq::max_segments(tokens, batch, segment)) * heads *
                                                            (d * d + stepq::kSegmentHead) * sizeof(float) > bytes))

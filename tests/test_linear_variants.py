@@ -92,3 +92,34 @@ def test_numbers_of_pairs(dtype, D, heads, batch, rule):
 def test_segments_of_more_than_four_chunks(dtype, D, heads, lengths):
     r = Run(dtype, heads, heads // 2, D, "additive", lengths, seed=heads)
     check(r, [1] + [0] * (len(lengths) - 1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", ["delta", "additive"])
+def test_calls_in_one_launch_take_no_workspace(rule):
+    """As many pairs as fill the chip: no memory is taken, on another stream either,
+    and the result is the one with a workspace, bit for bit."""
+    import torch
+    r = Run("bf16", 24, 12, 128, rule, [130, 70, 64, 1, 0, 200, 90, 33], seed=3)
+    assert prefill_bytes(r.att, 8, int(r.cu[-1])) == 0
+    r.prefill()
+    want = [r.o.clone(), r.state.clone()]
+    cu, slots = torch.from_numpy(r.cu).cuda(), torch.from_numpy(r.slots).cuda()
+    side = torch.cuda.Stream()
+    r.o.fill_(7.0)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    r.att.prefill(cu, r.q, r.k, r.v, r.beta, r.gate, slots, r.state, r.o, stream=side)
+    assert torch.cuda.max_memory_allocated() == before
+    torch.cuda.synchronize()
+    assert torch.equal(r.o, want[0]) and torch.equal(r.state, want[1])
+    few = Run("bf16", 2, 1, 128, "delta", [130], seed=3)
+    with pytest.raises(S.StepqError):
+        few.att.prefill(torch.from_numpy(few.cu).cuda(), few.q, few.k, few.v, few.beta, few.gate,
+                        torch.from_numpy(few.slots).cuda(), few.state, few.o, stream=side)
+
+
+def prefill_bytes(att, batch, tokens):
+    from quantized_recurrent_state_packed_amd import linear
+    return linear.lib().stepq_linear_prefill_bytes(att._desc, batch, tokens)
