@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 
 from . import stepq as _s
-from .linear import check_dense, dense, dtype_code, stream_of
+from .linear import check_dense, dense, dtype_code, leading, stream_of
 from .stepq import STEPQ_ERR_INVALID_ARG, STEPQ_ERR_UNSUPPORTED, StepqError
 
 EXPORTED = ("stepq_beam_workspace_bytes", "stepq_beam_select", "stepq_beam_reorder")
@@ -100,17 +100,19 @@ def reorder(beams: int, slot_ids, parents, buffers, new_slot_ids, num_slots: int
     layer, ...; num_slots is the first buffer's leading size where it is not
     given).  slot_ids, parents and new_slot_ids: int32 [batch * beams]."""
     where = "stepq_beam_reorder"
-    n = slot_ids.shape[0]
+    n = leading(where, "slot_ids", slot_ids)
     if num_slots is None:
         if not buffers:
             raise StepqError(STEPQ_ERR_INVALID_ARG, where, "num_slots is needed where there are no buffers")
-        num_slots = buffers[0].shape[0]
+        num_slots = leading(where, "a buffer", buffers[0])
     if len(buffers) > MAX_REGIONS:
         raise StepqError(STEPQ_ERR_UNSUPPORTED, where, f"more than {MAX_REGIONS} buffers")
     if num_slots < 1 or beams < 1:
         raise StepqError(STEPQ_ERR_INVALID_ARG, where, "beams and num_slots must be at least 1")
     if _s._checks:
         import torch
+        if not isinstance(slot_ids, torch.Tensor):
+            check_dense(where, "slot_ids", slot_ids, (n,), torch.int32, None)
         dev, i = slot_ids.device, slot_ids.get_device()
         for name, t in (("slot_ids", slot_ids), ("parents", parents), ("new_slot_ids", new_slot_ids)):
             if i < 0 or not dense(t, torch.int32, (n,), i):

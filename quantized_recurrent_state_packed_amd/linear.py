@@ -83,6 +83,14 @@ def _refuse(where: str, detail: str):
     raise StepqError(STEPQ_ERR_INVALID_ARG, where, detail)
 
 
+def leading(where: str, name: str, t) -> int:
+    """The leading size of a tensor, before anything else is known of it."""
+    try:
+        return t.shape[0]
+    except (AttributeError, IndexError, TypeError):
+        _refuse(where, f"{name} must be a torch tensor with its rows first")
+
+
 def check_dense(where: str, name: str, t, shape: tuple, dtype, device) -> None:
     """A contiguous device tensor of this dtype and shape (None in a shape: any size)."""
     import torch
@@ -183,7 +191,7 @@ class LinearAttention:
         call needs, if anything, is taken from torch's allocator, on the current stream."""
         import torch
         where = "stepq_linear_prefill"
-        batch, tokens = slot_ids.shape[0], v.shape[0]
+        batch, tokens = leading(where, "slot_ids", slot_ids), leading(where, "v", v)
         if _s._checks:
             qs, ks, vs, os_ = self._common(where, q, k, v, beta, gate, slot_ids, state, o, batch, tokens)
             i = state.get_device()
@@ -191,8 +199,9 @@ class LinearAttention:
                 check_dense(where, "cu_seqlens", cu_seqlens, (batch + 1,), torch.int32, state.device)
             if resume is not None and not dense(resume, torch.uint8, (batch,), i):
                 check_dense(where, "resume", resume, (batch,), torch.uint8, state.device)
-            if workspace is not None and not (workspace.dtype is torch.uint8 and workspace.get_device() == i and
-                                              workspace.dim() == 1 and workspace.is_contiguous()):
+            if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and
+                                              workspace.get_device() == i and workspace.dim() == 1 and
+                                              workspace.is_contiguous()):
                 check_dense(where, "workspace", workspace, (None,), torch.uint8, state.device)
         else:
             qs, ks, vs, os_ = self._strides(q, k, v, o)
@@ -218,7 +227,7 @@ class LinearAttention:
     def step(self, slot_ids, q, k, v, beta, gate, state, o, stream=None) -> None:
         """stepq_linear_step: one token of every request, updating the slots of state."""
         where = "stepq_linear_step"
-        batch = slot_ids.shape[0]
+        batch = leading(where, "slot_ids", slot_ids)
         if _s._checks:
             qs, ks, vs, os_ = self._common(where, q, k, v, beta, gate, slot_ids, state, o, batch, batch)
         else:
