@@ -14,8 +14,8 @@
  * enqueue on the caller's stream and return without synchronising, allocating
  * or copying between host and device (they may be captured into a graph),
  * argument checks run before any launch and have no side effects, no exception
- * crosses the ABI, and work runs on the HIP device that is current.  q, k,
- * v, o, states, regions and workspaces are 16-byte aligned, logits and arrays of
+ * crosses the ABI, and work runs on the HIP device that is current, on which every
+ * buffer has to lie (not checked here; the Python bindings do).  q, k, v, o, states, regions and workspaces are 16-byte aligned, logits and arrays of
  * 32-bit values (lengths, ids, beta, gate, scores) as their elements.  Two calls that use one workspace must be
  * ordered; its contents need no initialisation and mean nothing afterwards.
  */

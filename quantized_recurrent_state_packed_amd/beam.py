@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 
 from . import stepq as _s
-from .linear import check_dense, dense, dtype_code, leading, stream_of
+from .linear import check_current, check_dense, dense, dtype_code, leading, stream_of
 from .stepq import STEPQ_ERR_INVALID_ARG, STEPQ_ERR_UNSUPPORTED, StepqError
 
 EXPORTED = ("stepq_beam_workspace_bytes", "stepq_beam_select", "stepq_beam_reorder")
@@ -85,6 +85,7 @@ class BeamSelect:
                 check_dense(where, "scores", scores, (rows,), torch.float32, self.device)
             if finished is not None and not dense(finished, torch.uint8, (rows,), i):
                 check_dense(where, "finished", finished, (rows,), torch.uint8, self.device)
+            check_current(where, i)
         stride = logits.stride(0) if rows > 1 else self.vocab      # the only row's stride says nothing
         p = _s._ptr
         _s._check(lib().stepq_beam_select(self.batch, self.beams, self.vocab, self.num_out, p(logits), self._code, stride,
@@ -123,6 +124,7 @@ def reorder(beams: int, slot_ids, parents, buffers, new_slot_ids, num_slots: int
             if not isinstance(t, torch.Tensor) or t.get_device() != i or not t.is_contiguous() or t.nbytes % num_slots:
                 raise StepqError(STEPQ_ERR_INVALID_ARG, where,
                                  f"a buffer must be a contiguous tensor on {dev} of {num_slots} equal slots")
+        check_current(where, i)
     regions = (stepq_region * len(buffers))(*((t.data_ptr(), t.nbytes // num_slots) for t in buffers))
     p = _s._ptr
     _s._check(lib().stepq_beam_reorder(n // beams, int(beams), p(slot_ids), p(parents), int(num_slots), regions, len(buffers),

@@ -83,6 +83,19 @@ def _refuse(where: str, detail: str):
     raise StepqError(STEPQ_ERR_INVALID_ARG, where, detail)
 
 
+_current_device = None      # torch's, without what it does around the call
+
+
+def check_current(where: str, device_index: int) -> None:
+    """The library launches on the current device: the call's tensors have to lie there."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if _current_device() != device_index:
+        _refuse(where, f"the tensors are on cuda:{device_index}, which is not the current device")
+
+
 def leading(where: str, name: str, t) -> int:
     """The leading size of a tensor, before anything else is known of it."""
     try:
@@ -195,6 +208,7 @@ class LinearAttention:
         if _s._checks:
             qs, ks, vs, os_ = self._common(where, q, k, v, beta, gate, slot_ids, state, o, batch, tokens)
             i = state.get_device()
+            check_current(where, i)
             if not dense(cu_seqlens, torch.int32, (batch + 1,), i):
                 check_dense(where, "cu_seqlens", cu_seqlens, (batch + 1,), torch.int32, state.device)
             if resume is not None and not dense(resume, torch.uint8, (batch,), i):
@@ -230,6 +244,7 @@ class LinearAttention:
         batch = leading(where, "slot_ids", slot_ids)
         if _s._checks:
             qs, ks, vs, os_ = self._common(where, q, k, v, beta, gate, slot_ids, state, o, batch, batch)
+            check_current(where, state.get_device())
         else:
             qs, ks, vs, os_ = self._strides(q, k, v, o)
         p = _s._ptr

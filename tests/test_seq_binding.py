@@ -70,3 +70,27 @@ def test_workspace_and_resume_that_are_no_tensors():
         assert e.value.status == S.STEPQ_ERR_INVALID_ARG
     att.prefill(cu, **a)
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_tensors_of_a_device_that_is_not_current_are_refused(monkeypatch):
+    """The library launches on the current device, so another device's tensors (and its
+    default stream, whose handle is the same 0) must not reach it."""
+    import torch
+    att = LN.LinearAttention(2, 16)
+    a = linear_arguments(torch, "cuda")
+    cu = torch.tensor([0, 1, 2, 3, 4, 5], dtype=torch.int32, device="cuda")
+    ids = torch.arange(4, dtype=torch.int32, device="cuda")
+    pool, new = torch.zeros(4, 16, device="cuda"), torch.empty_like(ids)
+    sel = B.BeamSelect(1, 2, 10)
+    x, s = torch.zeros(2, 10, device="cuda"), torch.zeros(2, device="cuda")
+    calls = (lambda: att.step(**a), lambda: att.prefill(cu, **a), lambda: B.reorder(2, ids, ids % 2, [pool], new),
+             lambda: sel(x, s))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(LN, "_current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(S.StepqError, match="current") as e:
+            call()
+        assert e.value.status == S.STEPQ_ERR_INVALID_ARG
