@@ -41,9 +41,10 @@ def lib() -> ctypes.CDLL:
 
 
 class BeamSelect:
-    """Selection for up to `batch` requests of `beams` beams over `vocab` tokens:
-    keeps the workspace and the buffers of the result, which the next call
-    overwrites."""
+    """Selection for `batch` requests of `beams` beams over `vocab` tokens, no more
+    and no fewer: keeps the workspace and the buffers of the result, which the next
+    call overwrites.  Calls of one object on different streams therefore have to be
+    ordered by the caller, as two calls on one workspace do."""
 
     def __init__(self, batch: int, beams: int, vocab: int, num_out: int | None = None, dtype=None, eos_token: int = 0,
                  device="cuda"):

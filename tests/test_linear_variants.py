@@ -123,3 +123,40 @@ def test_calls_in_one_launch_take_no_workspace(rule):
 def prefill_bytes(att, batch, tokens):
     from quantized_recurrent_state_packed_amd import linear
     return linear.lib().stepq_linear_prefill_bytes(att._desc, batch, tokens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D,heads,rule,tokens", [
+    ("bf16", 128, 2, "delta", 140), ("f16", 128, 2, "delta", 140), ("bf16", 64, 2, "delta", 140), ("f16", 64, 2, "additive", 140),
+    ("bf16", 128, 2, "additive", 600), ("bf16", 32, 2, "delta", 140), ("f32", 128, 2, "delta", 140), ("f32", 64, 2, "additive", 140)])
+def test_token_offsets_past_32_bits(dtype, D, heads, rule, tokens):
+    """Tokens as far apart as is accepted, 2^24 elements: offsets of 2^32 bytes and more
+    within q, k, v and o, and 2^31 bytes within a chunk.  Prompts, then a step of all rows."""
+    import torch
+    r = Run(dtype, heads, 1, D, rule, [tokens], seed=40)
+    wide = torch.empty(tokens, 1 << 24, dtype=r.q.dtype, device="cuda")
+    places = {}
+    for at, (name, x) in zip((0, 1 << 12, 1 << 20, (1 << 24) - (1 << 12)), (("q", r.q), ("k", r.k), ("v", r.v), ("o", r.o))):
+        places[name] = wide[:, at:at + x.shape[1] * D].unflatten(1, x.shape[1:])
+        places[name].copy_(x)
+    assert places["o"].stride(0) == 1 << 24 and (tokens - 1) * wide.stride(0) * wide.element_size() > 2 ** 32
+    r.q, r.k, r.v, r.o = (places[n] for n in "qkvo")
+    ro, rm = recurrence64(r, [1])
+    r.prefill([1])
+    factor = {"f32": 1e-5}.get(dtype, STATE)
+    assert far(r.state[int(r.slots[0])].cpu().numpy(), rm[0].cpu().numpy()) <= factor
+    assert far(r.o.double().cpu().numpy(), ro.cpu().numpy()) <= OUT_TOL[dtype]
+    del ro, rm
+    n = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    state = torch.randn(tokens, heads, D, D, device="cuda")
+    before = state.double()
+    r.att.step(n, r.q, r.k, r.v, r.beta, r.gate, state, r.o)
+    torch.cuda.synchronize()
+    k, q = (x.double().repeat_interleave(heads, 1) for x in (r.k, r.q))
+    m = before * r.gate.double()[..., None, None]
+    u = r.v.double()
+    if r.beta is not None:
+        u = r.beta.double()[..., None] * (u - (m * k[..., None]).sum(-2))
+    m += k[..., None] * u[:, :, None, :]
+    assert far(state.cpu().numpy(), m.cpu().numpy()) <= 1e-5
+    assert far(r.o.double().cpu().numpy(), (m * q[..., None]).sum(-2).cpu().numpy()) <= OUT_TOL[dtype]
