@@ -625,9 +625,11 @@ struct Rates {
 };
 
 // One wave: the chunk's log2 G as a running sum in binary64, so that ratios of
-// retentions far into a fast-forgetting chunk keep binary32 accuracy.  A
-// retention of 0 (or below 2^-200) counts as 2^-200, which leaves nothing in
-// binary32.  Past `count` tokens: retention 1, beta 0.
+// retentions far into a fast-forgetting chunk keep binary32 accuracy.  Its terms are
+// binary32 logarithms, good to a unit in their last place also next to 1 (the
+// binary32 kernel, which has the time, takes them in binary64).  A retention of 0
+// or below 2^-126 counts as 2^-200, which leaves nothing in binary32.  Past `count`
+// tokens: retention 1, beta 0.
 __device__ __forceinline__ void set_rates(Rates& r, float gate, float beta, int count, int lane) {
   double x = 0.0;
   if (lane < count) {
