@@ -15,9 +15,18 @@
  * or copying between host and device (they may be captured into a graph),
  * argument checks run before any launch and have no side effects, no exception
  * crosses the ABI, and work runs on the HIP device that is current, on which every
- * buffer has to lie (not checked here; the Python bindings do).  q, k, v, o, states, regions and workspaces are 16-byte aligned, logits and arrays of
- * 32-bit values (lengths, ids, beta, gate, scores) as their elements.  Two calls that use one workspace must be
- * ordered; its contents need no initialisation and mean nothing afterwards.
+ * buffer has to lie (not checked here; the Python bindings do).  q, k, v, o,
+ * states, regions and workspaces are 16-byte aligned, logits and arrays of 32-bit
+ * values (lengths, ids, beta, gate, scores) as their elements.  Two calls that use
+ * one workspace must be ordered; its contents need no initialisation and mean
+ * nothing afterwards.
+ *
+ * What does not join: stepq_decode_step is the delta rule on dense binary32 q, k
+ * and v of every value head.  After prompts of 16-bit inputs or shared key heads the
+ * caller widens them and repeats key heads for it at every token
+ * (stepq_linear_step takes them as they are, on binary32 states), and the states of
+ * the additive rule can be packed and unpacked, but only the calls here continue
+ * them.
  */
 #ifndef STEPQ_SEQ_H
 #define STEPQ_SEQ_H
@@ -84,7 +93,8 @@ size_t stepq_linear_prefill_bytes(const stepq_linear_desc *desc, int32_t batch, 
  * The slots receive the states after the last token; a pool whose slots are
  * these states is also the packed pool of a layout whose heads are all 32 bits
  * wide, and stepq_pack takes them when slot_ids is 0 .. batch-1.
- * States, sums and retentions are held in binary32; o is rounded once.  A value
+ * States, sums, retentions and the operands of products are held in binary32 (of
+ * 16-bit inputs as three bfloat16 parts); o is rounded once.  A value
  * that is not finite spoils what depends on it and may spoil o of the tokens
  * before it in its chunk of 64, but no other request. */
 stepq_status stepq_linear_prefill(const stepq_linear_desc *desc, int32_t batch, int64_t total_tokens,

@@ -134,10 +134,12 @@ struct Tile {
   }
 };
 
-// Bound by the vector units: 13 or so instruction slots a logit (four of them the
-// exponential's) and some 50 insertions of about 120 cycles a wave.  32 x 8 rows of
-// 131072 bfloat16 logits take 44 us, 1.5 TB/s; copying their bytes takes 13.  With half
-// as many waves 46.5 us, with twice as many 50 (every wave fills a list of its own).
+// 32 x 8 rows of 131072 bfloat16 logits take 44 us, 1.5 TB/s; copying their bytes takes
+// 13.  Bound by instructions, of the vector units first: counters say 21 of them and 15
+// scalar ones a logit of every lane (insertions among them), the vector units busy 63 %
+// of the time that a compute unit works, and 11 of its 16 waves under way on the average,
+// which wait 41 % of their time, for loads and for the chain of their insertions.  With
+// half as many waves 46.5 us, with twice as many 50 (every wave fills a list of its own).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
   using L = Loader<T>;
@@ -204,8 +206,9 @@ __global__ void __launch_bounds__(kThreads) k_select_scan(SelectArgs p) {
 
 // A wave per beam joins the lists of the beam's parts, all of whose entries are
 // loaded at once, and the first wave orders the beams' candidates.  Bound by the
-// latency of its insertions: 17 us for 8 beams of 16 parts and 16 candidates, 5.6 us
-// for 4 beams of 32 parts and 4.
+// latency of its insertions: 17 us for 32 requests of 8 beams of 16 parts and 16
+// candidates (waves wait 61 % of their time, 970 vector instructions each), 5.6 us for
+// one of 4 beams of 32 parts and 4.
 __global__ void __launch_bounds__(1024) k_select_merge(SelectArgs p) {
   __shared__ float sx[kMaxBeams][64];
   __shared__ int32_t si[kMaxBeams][64];

@@ -18,10 +18,10 @@
 // A and B do not depend on the state, and value columns are independent of each
 // other.  So a request's chunks are walked in order by workgroups that own some
 // columns of one head, either with A and B from a kernel that computes them for all
-// chunks at once (few heads: many workgroups a head), or, where there are heads
-// enough to fill the chip, computing them as they go (no 25 KB of them a chunk and
-// head through memory): 8192 tokens of 8 requests and 48 heads, delta rule, bfloat16,
-// 308 us the first way and 248 us the second; 32768 tokens of 16, 1050 and 715 us.
+// chunks at once (few heads: many workgroups a head), or computing them as they go
+// (no 37 KB of them a chunk and head through memory).  512 pairs of 1024 tokens,
+// delta rule, bfloat16, D = 128: 408 us the first way and 273 us the second; where the
+// one takes over from the other stands, with figures, in linear_internal.hpp.
 //
 // Binary32 inputs run on binary32 matrix instructions (k_linear_chunks,
 // k_linear_walk), 16-bit inputs on bfloat16 ones (k_linear16_*).  MI355X copies at
@@ -807,8 +807,8 @@ __global__ void __launch_bounds__(kThreads) k_linear16_chunks(LinearArgs p) {
 
 // The request that comes `nth` by length, longest first, among up to 64 (beyond
 // that, where a chip full of workgroups evens lengths out by itself, in their own
-// order): 32768 tokens of 16 requests of 500 to 3500 took 0.91 ms in their own order,
-// with long ones starting last, and 0.74 ms so.
+// order): 32768 tokens of 16 requests of 500 to 3500 take 1.14 ms in their own order,
+// with long ones starting last, and 0.83 ms so; 8192 of 8, 378 and 306 us.
 __device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lane) {
   if (p.batch == 1 || p.batch > 64) return nth;
   const int n = lane < p.batch ? request_span(p, lane).count : -1;
@@ -829,17 +829,19 @@ __device__ __forceinline__ int nth_longest(const LinearArgs& p, int nth, int lan
 // state it starts from, which only fades.  PASS 1 leaves every segment's own state
 // and retention in the workspace, k_linear_join turns them into the states that
 // segments start from, and PASS 2 computes the outputs.  One 16384-token prompt of
-// 32 heads: 983 us in 256 chunks one after another, 261 us in segments.
+// 32 heads: 1199 us in 256 chunks one after another, 288 us in segments.
 //
 // At D = 128 the delta rule takes 456 matrix instructions of 16 cycles a chunk from
 // each of four waves with 32 columns (fewer, wider waves read q and k from LDS half as
 // often as eight with 16, and those spilled: 381 us against 225 for 512 pairs of 1024
-// tokens); the additive rule fits 128 registers with eight waves (157 against 162 us).
-// Bound by latency: with two workgroups a compute unit the matrix units are busy 36 %
-// and the vector units 47 % of the time, memory 18 % of its rate; the chain of a chunk
-// (staging, blocks and their inverses, K M and Q M, U, O, the state) has five barriers
-// and leaves two waves a SIMD too little to overlap.  32768 tokens of 16 requests and
-// 48 heads take 600 to 640 us, 2.8 times what copying their bytes takes.
+// tokens, both with operands in two parts, where this takes 273 now); the additive rule
+// fits 128 registers with eight waves (157 against 162 us, in two parts as well).
+// Bound by latency: with two workgroups a compute unit the matrix units are busy 44 %
+// and the vector units 46 % of the time, memory 27 % of its rate; the chain of a chunk
+// (staging, blocks and their inverses, K M and Q M, U, O, the state) has three barriers,
+// four where V takes Q's place, and leaves two waves a SIMD too little to overlap.  32768
+// tokens of 16 requests and 48 heads take 780 to 830 us, 3.5 to 3.8 times what copying
+// their bytes takes.
 template <int D, typename T, bool DELTA, int NCT, int NW, bool FUSED, int PASS>
 __global__ void __launch_bounds__(64 * NW, FUSED && __is_same(T, bf16) ? NW / 2 : 1) k_linear16_walk(LinearArgs p) {
   using S = Dims16<D, T>;
