@@ -6,6 +6,9 @@
  *                          prompts
  *   stepq_scan_backward    its gradients
  *   stepq_scan_step        one token of every request
+ *   stepq_norm_forward     the norms before and after a block, with its gate, its residual
+ *                          scale and the residual sum
+ *   stepq_norm_backward    their gradients
  *
  * Conventions are those of stepq_seq.h: the caller owns every device buffer, calls
  * enqueue on the caller's stream and return without synchronising, allocating or copying
@@ -96,6 +99,63 @@ stepq_status stepq_scan_step(const stepq_scan_desc *desc, int32_t batch, const i
                              const void *x, int64_t x_stride, const void *gate_a, int64_t gate_a_stride,
                              const void *gate_x, int64_t gate_x_stride, const float *decay, float *state, void *y,
                              int64_t y_stride, void *stream);
+
+/* The norms around a block.  For every token and head, a row of `width` values o of the block's
+ * result, z of the gate and x of the residual stream:
+ *   n = o rsqrt(mean o^2 + eps) post_weight     (post = 0: n = o)
+ *   t = x + scale n act(z)                      written to out
+ *   y = t rsqrt(mean t^2 + eps) pre_weight      written to normed (pre = 0: there is none)
+ * act is z s(z) or s(z), s the logistic function; what is not given is left out: no gate, act
+ * is 1, no residual, x is 0, no scale or weight, it is 1.  So post alone with a gate is the
+ * gated norm behind a recurrent readout, pre alone with a residual is a residual sum and
+ * the next block's norm.  Everything is worked out in binary32 (y from t before it is rounded)
+ * and rounded once. */
+typedef enum {
+  STEPQ_GATE_SILU = 0,
+  STEPQ_GATE_SIGMOID = 1
+} stepq_gate_activation;
+
+typedef struct {
+  int32_t width;        /* values of a row, 1 .. 16384 */
+  int32_t heads;        /* rows of a token, side by side, >= 1 */
+  int32_t dtype;        /* stepq_dtype of all tensors of tokens */
+  int32_t activation;   /* stepq_gate_activation */
+  int32_t post;         /* 0 or 1 */
+  int32_t pre;          /* 0 or 1 */
+  float eps;            /* finite, > 0 */
+} stepq_norm_desc;
+
+/* Tensors of tokens are [tokens][heads * width], tokens *_stride elements apart; weights and
+ * scale are float [width], shared by the heads.  gate, residual, post_weight, scale and
+ * pre_weight may be NULL; out may be NULL where pre is 1.  out and normed may each be the
+ * buffer of block, gate or residual, at the same stride (not of each other).
+ * tokens * heads is below 2^31.  A value that is not finite spoils its row alone. */
+stepq_status stepq_norm_forward(const stepq_norm_desc *desc, int64_t tokens, const void *block, int64_t block_stride,
+                                const void *gate, int64_t gate_stride, const void *residual,
+                                int64_t residual_stride, const float *post_weight, const float *scale,
+                                const float *pre_weight, void *out, int64_t out_stride, void *normed,
+                                int64_t normed_stride, void *stream);
+
+/* Bytes stepq_norm_backward needs as workspace for up to `tokens` tokens; 0 for an invalid desc
+ * or sizes it refuses. */
+size_t stepq_norm_workspace_bytes(const stepq_norm_desc *desc, int64_t tokens);
+
+/* Gradients.  block, gate, post_weight, scale and pre_weight are those of the forward pass; out
+ * is what it wrote (pre = 0: not read, may be NULL).  d_out and d_normed are the gradients of
+ * out and normed: d_normed is given exactly where pre is 1, and there d_out may be NULL.
+ * Written: d_block; d_gate, where there is a gate; d_residual (NULL where it is not wanted);
+ * and, float [width] each and NULL where not wanted, d_post_weight, d_scale and d_pre_weight
+ * of weights that are given.  d_block, d_gate and d_residual may each be the buffer of
+ * block, gate, out, d_out or d_normed, at the same stride (not of each other).  The same
+ * inputs give the same bits. */
+stepq_status stepq_norm_backward(const stepq_norm_desc *desc, int64_t tokens, const void *block, int64_t block_stride,
+                                 const void *gate, int64_t gate_stride, const void *out, int64_t out_stride,
+                                 const float *post_weight, const float *scale, const float *pre_weight,
+                                 const void *d_out, int64_t d_out_stride, const void *d_normed,
+                                 int64_t d_normed_stride, void *d_block, int64_t d_block_stride, void *d_gate,
+                                 int64_t d_gate_stride, void *d_residual, int64_t d_residual_stride,
+                                 float *d_post_weight, float *d_scale, float *d_pre_weight, void *workspace,
+                                 size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

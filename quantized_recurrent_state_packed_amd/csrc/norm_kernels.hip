@@ -1,0 +1,366 @@
+// gfx950 kernels of the norms around a block, forward and backward.
+//
+// A row is shared by `L` lanes, each of which holds `P` pieces of 16 bytes of every
+// tensor of it in registers from the load to the store: every tensor is read or written
+// once, and a row's two sums (of o^2, then of t^2, which depends on the first) are the only
+// exchange.  The same lane reads and writes an element, so outputs may lie where inputs did.
+//
+// Backward, with r1 and r2 the reciprocal roots, p = n act(z) and v = pre_weight dy:
+//   gt = dt + r2 v - t r2^3 mean(t v)       the gradient of t, and of the residual
+//   dscale = sum gt p,  q = scale gt,  dz = q n act'(z),  m = q act(z)
+//   dpost = sum m o r1,  do = r1 w m - o r1^3 mean(o w m),  dpre = sum dy t r2
+// The weights' gradients are summed over a workgroup's rows in registers, over workgroups
+// in a second launch, in order.
+#include "norm_internal.hpp"
+
+namespace stepq {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);
+
+template <typename T>
+struct alignas(16) Piece {
+  T v[kVec<T>];
+};
+
+// The values base + at .. of a row, zeros behind its end.  IN16: rows lie on 16-byte
+// boundaries and hold whole pieces.
+template <typename T, bool IN16>
+__device__ __forceinline__ Piece<T> load(const T* row, int at, int width) {
+  Piece<T> r;
+  if (IN16) {
+    if (at < width) return *reinterpret_cast<const Piece<T>*>(row + at);
+    for (int i = 0; i < kVec<T>; ++i) r.v[i] = static_cast<T>(0.0f);
+  } else {
+    for (int i = 0; i < kVec<T>; ++i) r.v[i] = at + i < width ? row[at + i] : static_cast<T>(0.0f);
+  }
+  return r;
+}
+template <typename T, bool IN16>
+__device__ __forceinline__ void store(T* row, int at, int width, const float (&x)[kVec<T>]) {
+  if (IN16) {
+    if (at >= width) return;
+    Piece<T> r;
+    for (int i = 0; i < kVec<T>; ++i) r.v[i] = static_cast<T>(x[i]);
+    *reinterpret_cast<Piece<T>*>(row + at) = r;
+  } else {
+    for (int i = 0; i < kVec<T>; ++i)
+      if (at + i < width) row[at + i] = static_cast<T>(x[i]);
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  const int i = __builtin_bit_cast(int, x);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false));
+}
+
+// Sums over the L lanes of a row, the same bits in each of them.
+template <int L, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float (*lds)[N]) {
+  for (int n = 0; n < N; ++n) {
+    x[n] += moved<0xB1>(x[n]);          // quad_perm: neighbours, then pairs
+    x[n] += moved<0x4E>(x[n]);
+    if (L >= 16) {
+      x[n] += moved<0x124>(x[n]);       // row_ror: 4, then 8
+      x[n] += moved<0x128>(x[n]);
+    }
+    if (L >= 64) {
+      x[n] += __shfl_xor(x[n], 16);
+      x[n] += __shfl_xor(x[n], 32);
+    }
+  }
+  if (L > 64) {
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+      for (int n = 0; n < N; ++n) lds[w][n] = x[n];
+    __syncthreads();
+    for (int n = 0; n < N; ++n) {
+      float all = lds[0][n];
+      for (int s = 1; s < L / 64; ++s) all += lds[s][n];
+      x[n] = all;
+    }
+  }
+}
+
+__device__ __forceinline__ float logistic(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
+}
+
+// act(z) and, where it is asked for, its slope.  A gate of -inf shuts.
+__device__ __forceinline__ float activated(float z, bool silu) {
+  const float s = logistic(z);
+  return !silu ? s : s == 0.0f ? 0.0f : z * s;
+}
+__device__ __forceinline__ float activated(float z, bool silu, float& slope) {
+  const float s = logistic(z), rest = 1.0f - s;
+  if (!silu) return slope = s * rest, s;
+  const float bend = rest == 0.0f || s == 0.0f ? 0.0f : z * rest;
+  slope = s * (1.0f + bend);
+  return s == 0.0f ? 0.0f : z * s;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* row_of(const NormRows& r, int row, int heads, int width) {
+  const T* p = static_cast<const T*>(r.p);
+  if (heads == 1) return p + row * r.stride;
+  const uint32_t token = static_cast<uint32_t>(row) / static_cast<uint32_t>(heads);
+  return p + token * r.stride + static_cast<int64_t>(row - token * heads) * width;
+}
+template <typename T>
+__device__ __forceinline__ T* out_row_of(const NormRows& r, int row, int heads, int width) {
+  return const_cast<T*>(row_of<T>(r, row, heads, width));
+}
+
+// A lane's part of a weight, 1 where there is none.
+template <typename T, int P>
+__device__ __forceinline__ void load_weight(float (&w)[P][kVec<T>], const float* from, int lane, int L, int width) {
+  for (int j = 0; j < P; ++j)
+    for (int i = 0; i < kVec<T>; ++i) {
+      const int at = (j * L + lane) * kVec<T> + i;
+      w[j][i] = from != nullptr && at < width ? from[at] : 1.0f;
+    }
+}
+
+template <typename T, bool IN16, int L, int P>
+__global__ void __launch_bounds__(L < 256 ? 256 : L) k_norm(NormArgs p) {
+  constexpr int V = kVec<T>, kAtOnce = L < 256 ? 256 / L : 1;
+  __shared__ float lds[2][L > 64 ? L / 64 : 1][1];
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const float inv = 1.0f / static_cast<float>(p.width);
+  float w1[P][V], sc[P][V], w2[P][V];
+  load_weight<T, P>(w1, p.post_weight, lane, L, p.width);
+  load_weight<T, P>(sc, p.scale, lane, L, p.width);
+  load_weight<T, P>(w2, p.pre_weight, lane, L, p.width);
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kAtOnce; first < p.rows; first += static_cast<int64_t>(gridDim.x) * kAtOnce) {
+    const int64_t mine = first + group;
+    const bool real = mine < p.rows;
+    const int row = static_cast<int>(real ? mine : first);
+    Piece<T> o[P], z[P], x[P];
+    for (int j = 0; j < P; ++j) {
+      const int at = (j * L + lane) * V;
+      o[j] = load<T, IN16>(row_of<T>(p.block, row, p.heads, p.width), at, p.width);
+      if (p.gate.p != nullptr) z[j] = load<T, IN16>(row_of<T>(p.gate, row, p.heads, p.width), at, p.width);
+      if (p.residual.p != nullptr) x[j] = load<T, IN16>(row_of<T>(p.residual, row, p.heads, p.width), at, p.width);
+    }
+    float r1 = 1.0f;
+    if (p.post) {
+      float s[1] = {0.0f};
+      for (int j = 0; j < P; ++j)
+        for (int i = 0; i < V; ++i) s[0] = fmaf(static_cast<float>(o[j].v[i]), static_cast<float>(o[j].v[i]), s[0]);
+      row_sums<L>(s, lds[0]);
+      r1 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, p.eps));
+    }
+    float t[P][V], s[1] = {0.0f};
+    for (int j = 0; j < P; ++j)
+      for (int i = 0; i < V; ++i) {
+        float g = static_cast<float>(o[j].v[i]) * r1 * w1[j][i];
+        if (p.gate.p != nullptr) g *= activated(static_cast<float>(z[j].v[i]), p.silu);
+        t[j][i] = p.residual.p != nullptr ? fmaf(sc[j][i], g, static_cast<float>(x[j].v[i])) : sc[j][i] * g;
+        s[0] = fmaf(t[j][i], t[j][i], s[0]);
+      }
+    if (p.out.p != nullptr && real)
+      for (int j = 0; j < P; ++j)
+        store<T, IN16>(out_row_of<T>(p.out, row, p.heads, p.width), (j * L + lane) * V, p.width, t[j]);
+    if (p.pre) {
+      row_sums<L>(s, lds[1]);
+      const float r2 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, p.eps));
+      for (int j = 0; j < P; ++j) {
+        float y[V];
+        for (int i = 0; i < V; ++i) y[i] = t[j][i] * r2 * w2[j][i];
+        if (real) store<T, IN16>(out_row_of<T>(p.normed, row, p.heads, p.width), (j * L + lane) * V, p.width, y);
+      }
+    }
+    // the next row's sums overwrite this one's, which were read before the other sum's barrier
+    if (L > 64 && !(p.post && p.pre)) __syncthreads();
+  }
+}
+
+template <typename T, bool IN16, int L, int P>
+__global__ void __launch_bounds__(L < 256 ? 256 : L) k_norm_backward(NormArgs p) {
+  constexpr int V = kVec<T>, kAtOnce = L < 256 ? 256 / L : 1;
+  __shared__ float lds1[L > 64 ? L / 64 : 1][3];
+  __shared__ float lds2[L > 64 ? L / 64 : 1][1];
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const float inv = 1.0f / static_cast<float>(p.width);
+  float w1[P][V], sc[P][V], w2[P][V], d1[P][V], ds[P][V], d2[P][V];
+  load_weight<T, P>(w1, p.post_weight, lane, L, p.width);
+  load_weight<T, P>(sc, p.scale, lane, L, p.width);
+  load_weight<T, P>(w2, p.pre_weight, lane, L, p.width);
+  for (int j = 0; j < P; ++j)
+    for (int i = 0; i < V; ++i) d1[j][i] = ds[j][i] = d2[j][i] = 0.0f;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kAtOnce; first < p.rows; first += static_cast<int64_t>(gridDim.x) * kAtOnce) {
+    const int64_t mine = first + group;
+    const bool real = mine < p.rows;
+    const int row = static_cast<int>(real ? mine : first);
+    Piece<T> o[P], z[P], t[P], gt[P], gy[P];
+    for (int j = 0; j < P; ++j) {
+      const int at = (j * L + lane) * V;
+      o[j] = load<T, IN16>(row_of<T>(p.block, row, p.heads, p.width), at, p.width);
+      if (p.gate.p != nullptr) z[j] = load<T, IN16>(row_of<T>(p.gate, row, p.heads, p.width), at, p.width);
+      if (p.d_out.p != nullptr) gt[j] = load<T, IN16>(row_of<T>(p.d_out, row, p.heads, p.width), at, p.width);
+      if (p.pre) {
+        t[j] = load<T, IN16>(row_of<T>(p.out, row, p.heads, p.width), at, p.width);
+        gy[j] = load<T, IN16>(row_of<T>(p.d_normed, row, p.heads, p.width), at, p.width);
+      }
+    }
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < P; ++j)
+      for (int i = 0; i < V; ++i) {
+        const float a = static_cast<float>(o[j].v[i]);
+        s[0] = fmaf(a, a, s[0]);
+        if (p.pre) {
+          const float b = static_cast<float>(t[j].v[i]);
+          s[1] = fmaf(b, b, s[1]);
+          s[2] = fmaf(b, w2[j][i] * static_cast<float>(gy[j].v[i]), s[2]);
+        }
+      }
+    row_sums<L>(s, lds1);
+    const float r1 = p.post ? __builtin_amdgcn_rsqf(fmaf(s[0], inv, p.eps)) : 1.0f;
+    const float r2 = __builtin_amdgcn_rsqf(fmaf(s[1], inv, p.eps)), back = s[2] * inv * r2 * r2;
+    float m[P][V], sum[1] = {0.0f};
+    for (int j = 0; j < P; ++j) {
+      float all[V], dz[V];
+      for (int i = 0; i < V; ++i) {
+        float g = p.d_out.p != nullptr ? static_cast<float>(gt[j].v[i]) : 0.0f;
+        if (p.pre) {
+          const float b = static_cast<float>(t[j].v[i]), dy = static_cast<float>(gy[j].v[i]);
+          g += r2 * (w2[j][i] * dy - b * back);
+          if (real) d2[j][i] = fmaf(dy, b * r2, d2[j][i]);
+        }
+        all[i] = g;
+        const float u = static_cast<float>(o[j].v[i]) * r1, n = u * w1[j][i];
+        float slope = 0.0f, act = 1.0f;
+        if (p.gate.p != nullptr) act = activated(static_cast<float>(z[j].v[i]), p.silu, slope);
+        if (real) ds[j][i] = fmaf(g, n * act, ds[j][i]);
+        const float q = g * sc[j][i];
+        dz[i] = q * n * slope;
+        const float k = q * act;
+        if (real) d1[j][i] = fmaf(k, u, d1[j][i]);
+        m[j][i] = k * w1[j][i];
+        sum[0] = fmaf(static_cast<float>(o[j].v[i]), m[j][i], sum[0]);
+      }
+      const int at = (j * L + lane) * V;
+      if (p.d_residual.p != nullptr && real) store<T, IN16>(out_row_of<T>(p.d_residual, row, p.heads, p.width), at, p.width, all);
+      if (p.gate.p != nullptr && real) store<T, IN16>(out_row_of<T>(p.d_gate, row, p.heads, p.width), at, p.width, dz);
+    }
+    row_sums<L>(sum, lds2);
+    const float mean = p.post ? sum[0] * inv * r1 * r1 : 0.0f;
+    for (int j = 0; j < P; ++j) {
+      float d[V];
+      for (int i = 0; i < V; ++i) d[i] = r1 * (m[j][i] - static_cast<float>(o[j].v[i]) * mean);
+      if (real) store<T, IN16>(out_row_of<T>(p.d_block, row, p.heads, p.width), (j * L + lane) * V, p.width, d);
+    }
+  }
+  if (p.partial == nullptr) return;
+  // the workgroup's rows that were under way together are added in order
+  constexpr int kSlots = kAtOnce > 1 ? 256 * V * P : 1;
+  __shared__ float part[kSlots];
+  for (int k = 0; k < 3; ++k) {
+    float(&d)[P][V] = k == 0 ? d1 : k == 1 ? ds : d2;
+    float* to = p.partial + (static_cast<int64_t>(k) * p.groups + blockIdx.x) * p.width;
+    if (kAtOnce > 1) {
+      __syncthreads();
+      for (int j = 0; j < P; ++j)
+        for (int i = 0; i < V; ++i) part[group * (L * V * P) + (j * L + lane) * V + i] = d[j][i];
+      __syncthreads();
+      for (int at = threadIdx.x; at < L * V * P && at < p.width; at += 256) {
+        float all = part[at];
+        for (int g = 1; g < kAtOnce; ++g) all += part[g * (L * V * P) + at];
+        to[at] = all;
+      }
+    } else {
+      for (int j = 0; j < P; ++j)
+        for (int i = 0; i < V; ++i) {
+          const int at = (j * L + lane) * V + i;
+          if (at < p.width) to[at] = d[j][i];
+        }
+    }
+  }
+}
+
+// The weights' gradients from the workgroups' parts, added in order in binary64.
+__global__ void __launch_bounds__(1024) k_norm_weights(NormArgs p) {
+  __shared__ double sums[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = blockIdx.y;
+  float* to = k == 0 ? p.d_post_weight : k == 1 ? p.d_scale : p.d_pre_weight;
+  if (to == nullptr) return;
+  const int c = blockIdx.x * 64 + lane;
+  double sum = 0.0;
+  if (c < p.width)
+    for (int g = w; g < p.groups; g += 16) sum += p.partial[(static_cast<int64_t>(k) * p.groups + g) * p.width + c];
+  sums[w][lane] = sum;
+  __syncthreads();
+  if (w != 0 || c >= p.width) return;
+  for (int s = 1; s < 16; ++s) sum += sums[s][lane];
+  to[c] = static_cast<float>(sum);
+}
+
+// Whether all rows lie on 16-byte boundaries and hold whole pieces.
+bool in_pieces(const NormArgs& a, int esize) {
+  const NormRows* all[] = {&a.block, &a.gate, &a.residual, &a.out, &a.normed, &a.d_out, &a.d_normed, &a.d_block, &a.d_gate,
+                           &a.d_residual};
+  if (a.width * esize % 16 != 0) return false;
+  for (const NormRows* r : all)
+    if (r->p && (reinterpret_cast<uintptr_t>(r->p) % 16 != 0 || r->stride * esize % 16 != 0)) return false;
+  return true;
+}
+
+template <typename T, bool IN16, bool BACK>
+void launch(const NormArgs& a, int dtype, hipStream_t s) {
+  const NormShape n = norm_shape(a.width, dtype);
+  const int at_once = norm_rows_at_once(n);
+  const int64_t all = (static_cast<int64_t>(a.rows) + at_once - 1) / at_once;
+  const dim3 grid(static_cast<uint32_t>(BACK ? a.groups : all < 2048 ? all : 2048));
+  const auto go = [&](auto lanes, auto pieces) {
+    constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
+    if (BACK) k_norm_backward<T, IN16, L, P><<<grid, L < 256 ? 256 : L, 0, s>>>(a);
+    else k_norm<T, IN16, L, P><<<grid, L < 256 ? 256 : L, 0, s>>>(a);
+  };
+  const auto is = [&](auto lanes, auto pieces) {
+    if (n.lanes != decltype(lanes)::value || n.pieces != decltype(pieces)::value) return false;
+    go(lanes, pieces);
+    return true;
+  };
+#define STEPQ_INT(x) std::integral_constant<int, x>{}
+  is(STEPQ_INT(4), STEPQ_INT(1)) || is(STEPQ_INT(16), STEPQ_INT(1)) || is(STEPQ_INT(64), STEPQ_INT(1)) ||
+      is(STEPQ_INT(64), STEPQ_INT(2)) || is(STEPQ_INT(256), STEPQ_INT(2)) || is(STEPQ_INT(256), STEPQ_INT(4)) ||
+      is(STEPQ_INT(1024), STEPQ_INT(4));
+#undef STEPQ_INT
+}
+
+template <typename T, bool BACK>
+void launch(const NormArgs& a, int dtype, hipStream_t s) {
+  if (in_pieces(a, sizeof(T))) launch<T, true, BACK>(a, dtype, s);
+  else launch<T, false, BACK>(a, dtype, s);
+}
+
+template <bool BACK>
+void launch(const NormArgs& a, int dtype, hipStream_t s) {
+  if (dtype == STEPQ_BF16) launch<__bf16, BACK>(a, dtype, s);
+  else if (dtype == STEPQ_F16) launch<_Float16, BACK>(a, dtype, s);
+  else launch<float, BACK>(a, dtype, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(const NormArgs& a, int dtype, hipStream_t s) {
+  launch<false>(a, dtype, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, int dtype, hipStream_t s) {
+  if (a.rows > 0) {
+    launch<true>(a, dtype, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.d_post_weight == nullptr && a.d_scale == nullptr && a.d_pre_weight == nullptr) return hipSuccess;
+  k_norm_weights<<<dim3(static_cast<uint32_t>((a.width + 63) / 64), 3), 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace stepq
