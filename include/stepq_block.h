@@ -9,6 +9,8 @@
  *   stepq_norm_forward     the norms before and after a block, with its gate, its residual
  *                          scale and the residual sum
  *   stepq_norm_backward    their gradients
+ *   stepq_verify_drafts    which drafted tokens a target model accepts, and the token after
+ *                          them, from given random numbers
  *
  * Conventions are those of stepq_seq.h: the caller owns every device buffer, calls
  * enqueue on the caller's stream and return without synchronising, allocating or copying
@@ -155,6 +157,36 @@ stepq_status stepq_norm_backward(const stepq_norm_desc *desc, int64_t tokens, co
                                  int64_t d_normed_stride, void *d_block, int64_t d_block_stride, void *d_gate,
                                  int64_t d_gate_stride, void *d_residual, int64_t d_residual_stride,
                                  float *d_post_weight, float *d_scale, float *d_pre_weight, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* Bytes stepq_verify_drafts needs as workspace; 0 for sizes it refuses. */
+size_t stepq_verify_workspace_bytes(int32_t batch, int32_t drafts, int32_t vocab);
+
+/* Verification of drafted tokens.  Request b has num_drafts[b] of them (NULL: all `drafts`; clamped to
+ * 0 .. drafts), draft_tokens[b][0 ..]; row b * (drafts + 1) + k of logits is the target's for the
+ * token at place k (one more than there are drafts), row b * drafts + k of draft_logits the draft's.
+ * With p and q the softmax of the two rows over temperature[b] (NULL: 1), drafted token d at
+ * place k is accepted where all before it are and
+ *     uniforms[b][k] q(d) < p(d)
+ * Behind n accepted ones the next token is drawn from max(p - q, 0) where a draft was rejected at
+ * place n (from p should nothing be left of it), from p where all were accepted: it is the first
+ * one up to which the sum exceeds uniforms[b][drafts] times the whole.  So the tokens are distributed as
+ * the target's own, whatever the draft; drafts = 0 draws a token.
+ *   draft_logits NULL: the draft was certain of its tokens, q(d) = 1.
+ *   temperature 0 (or less, or NaN): greedy.  p is the lowest of the tokens with the largest
+ *     logit, a draft is accepted if it is that token, and draft_logits are not read.
+ *   A logit of -inf or NaN bans its token; among logits of +inf the probability is shared.
+ *     Where all of the target's row is banned nothing is accepted and the next token is -1.
+ *   A drafted token outside of the vocabulary ends the request's drafts before it.
+ * Written: accepted int32 [batch], n; tokens int32 [batch][drafts + 1], the accepted drafts, the
+ * next token, and -1 behind it.  logits and draft_logits are of type dtype, their rows *_stride >=
+ * vocab elements apart; draft_tokens int32 [batch][drafts]; uniforms float [batch][drafts + 1] in
+ * [0, 1); temperature float [batch].  Probabilities are worked out and summed in binary64.
+ * drafts: 0 .. 63. */
+stepq_status stepq_verify_drafts(int32_t batch, int32_t drafts, int32_t vocab, const void *logits, int32_t dtype,
+                                 int64_t logits_stride, const void *draft_logits, int64_t draft_logits_stride,
+                                 const int32_t *draft_tokens, const int32_t *num_drafts, const float *temperature,
+                                 const float *uniforms, int32_t *accepted, int32_t *tokens, void *workspace,
                                  size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus

@@ -22,7 +22,7 @@ FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
          "-Wno-unused-command-line-argument", f"-I{INCLUDE}"]
 SOURCES = ["stepq_kernels.hip", "stepq_api.cpp", "linear_kernels.hip", "linear_api.cpp", "beam_kernels.hip",
            "beam_api.cpp", "scan_kernels.hip", "scan_api.cpp", "norm_kernels.hip",
-           "norm_api.cpp"]
+           "norm_api.cpp", "draft_kernels.hip", "draft_api.cpp"]
 
 
 def build(verbose: bool = False) -> Path:
