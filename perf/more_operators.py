@@ -375,8 +375,18 @@ def _own_scan(s):
                 saved=keep["saved"], workspace=keep["ws"])
     if c["op"] == "scan":
         return {"y": s["y"], "state": s["state"]}
+    # The plain form works on a binary32 dy in place and leaves the last states' gradients added to it; a second
+    # pass on the same state has to meet the same dy here.
+    single = c["dtype"] == "f32"
+    if single:
+        if "last" not in keep:
+            some = s["cu"][1:] > s["cu"][:-1]
+            keep["last"], keep["ended"] = s["cu"][1:].long()[some] - 1, s["slots"].long()[some]
+        grad_end = s["dstate"].index_select(0, keep["ended"])
     rec.backward(s["cu"], s["x"], s["ga"], s["gx"], s["decay"], keep["saved"], s["dy"], s["dx"], s["dga"], s["dgx"],
                  s["ddecay"], slot_ids=s["slots"], dstate=s["dstate"], resume=s["resume"], workspace=keep["ws"])
+    if single:
+        s["dy"].index_add_(0, keep["last"], grad_end)
     return _gradients(s)
 
 
