@@ -44,10 +44,12 @@ stepq_status from_hip(hipError_t e) { return e == hipSuccess ? STEPQ_OK : STEPQ_
 
 void place(stepq::ScanArgs& a, const stepq_scan_desc& d, void* workspace, const stepq::ScanWorkspace& w) {
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  if (w.links > w.ends) {
+  if (w.maps > 0) {
     a.ticket = reinterpret_cast<uint32_t*>(base);
+    a.maps = reinterpret_cast<uint64_t*>(base + w.maps);
     a.ends = reinterpret_cast<uint64_t*>(base + w.ends);
-    a.links = reinterpret_cast<uint64_t*>(base + w.links);
+    a.speeds = reinterpret_cast<float*>(base + w.speeds);
+    a.words = static_cast<int64_t>(w.speeds / 16);
   }
   if (w.bytes > w.partial) a.partial = reinterpret_cast<float*>(base + w.partial);
 }

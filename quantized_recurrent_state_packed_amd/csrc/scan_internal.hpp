@@ -38,9 +38,11 @@ struct ScanArgs {
   float* saved;                // nullptr: nothing is saved
   float* ddecay;
   float* partial;              // backward: every piece's part of ddecay
-  uint32_t* ticket;            // see scan_workspace
+  uint32_t* ticket;            // nullptr: no request is longer than a piece; see ScanWorkspace
+  uint64_t* maps;
   uint64_t* ends;
-  uint64_t* links;
+  float* speeds;
+  int64_t words;               // of 16 bytes, to be set before the pieces run
   int64_t total_tokens;
   int32_t batch;
   int32_t num_slots;
@@ -58,17 +60,23 @@ inline int64_t scan_pieces(int64_t total_tokens, int64_t batch) { return total_t
 // Requests of a piece or less have nothing to hand on.
 inline bool scan_linked(int64_t total_tokens) { return total_tokens > kPiece; }
 
+// What a call over requests longer than a piece keeps in its workspace: a ticket (at 0), every
+// piece's map of the state before it to the state behind it, the states behind pieces, each
+// channel's logarithm of the retention at an open gate; and a backward pass every piece's part
+// of ddecay.  Offsets in bytes.
 struct ScanWorkspace {
-  size_t ends, links, partial, bytes;     // offsets; the ticket is at 0
+  size_t maps, ends, speeds, partial, bytes;
 };
 inline ScanWorkspace scan_workspace(const stepq_scan_desc& d, int64_t total_tokens, int64_t batch, bool backward) {
+  const auto whole = [](size_t bytes) { return (bytes + 15) / 16 * 16; };
   const size_t n = static_cast<size_t>(scan_pieces(total_tokens, batch)) * d.width;
-  const size_t words = scan_linked(total_tokens) ? (n * 8 + 15) / 16 * 16 : 0;
+  const bool linked = scan_linked(total_tokens);
   ScanWorkspace w{};
-  w.ends = words ? 16 : 0;
-  w.links = w.ends + words;
-  w.partial = w.links + words;
-  w.bytes = w.partial + (backward ? (n * 4 + 15) / 16 * 16 : 0);
+  w.maps = linked ? 16 : 0;
+  w.ends = w.maps + (linked ? whole(n * 8) : 0);
+  w.speeds = w.ends + (linked ? whole(n * 8) : 0);
+  w.partial = w.speeds + (linked ? whole(static_cast<size_t>(d.width) * 4) : 0);
+  w.bytes = w.partial + (backward ? whole(n * 4) : 0);
   return w;
 }
 

@@ -5,10 +5,12 @@
 //   h_t = a_t h_{t-1} + u_t,  u_t = b_t s(gx_t) x_t,  y_t = h_t
 //
 // A run of tokens is an affine map of the state before it, h -> A h + B, and maps
-// of neighbouring runs compose.  A wave holds kScanTokens tokens of 64 V channels, the
-// kScanRows waves of a workgroup follow each other in time, so each works out its map,
-// the maps meet in LDS, and every wave then walks its tokens from the state that it
-// starts from.
+// of neighbouring runs compose.  A wave holds kScanTokens tokens of 64 V channels in registers,
+// the kScanRows waves of a workgroup follow each other in time and make up a piece of kPiece
+// tokens.  Each wave works out its map, the maps meet in LDS, states are handed on from piece to
+// piece (hand_on), and every wave walks its tokens from the state that it starts from.  So
+// every tensor is read or written once, whatever a request's length, and one long request
+// spreads over the chip like many short ones.
 //
 // Backward, with c_t = a_{t+1} g_{t+1} what comes from the tokens behind (the final
 // state's gradient for the last one), g_t = dy_t + c_t:
@@ -17,6 +19,8 @@
 //   dga_t = P_t (1 - s(ga_t)),   ddecay = sum_t P_t s(decay) / softplus(decay)
 // c is a recurrence of the same kind, backwards: c -> a_t c + a_t dy_t.  log a / b goes to 0
 // with log a, like -sqrt(-log a / 2).
+#include <type_traits>
+
 #include "scan_internal.hpp"
 
 namespace stepq {
@@ -84,13 +88,27 @@ __device__ __forceinline__ int64_t start_of(const ScanArgs& p, int b) {
   return at < 0 ? 0 : at > p.total_tokens ? p.total_tokens : at;
 }
 
-__device__ __forceinline__ Piece request_of(const ScanArgs& p, int b, int64_t piece) {
-  Piece r;
-  r.request = b;
-  r.first = start_of(p, b);
-  const int64_t end = start_of(p, b + 1);
+// The last request that begins at this index or before it, 64 at a time.
+__device__ __forceinline__ Piece find(const ScanArgs& p, int64_t piece) {
+  const int lane = threadIdx.x & 63;
+  Piece r = {-1, 0, 0, 0};
+  int from = 0, n = p.batch;
+  for (bool more = true; more;) {
+    const int step = (n + 63) / 64, at = from + lane * step;
+    const bool before = lane * step < n && start_of(p, at) / kPiece + at <= piece;
+    const int count = __popcll(__ballot(before));
+    if (count == 0) return r;                 // rows before the first request
+    from += (count - 1) * step;
+    n = min(step, n - (count - 1) * step);
+    more = step > 1;
+  }
+  from = __builtin_amdgcn_readfirstlane(from);
+  r.request = from;
+  r.first = start_of(p, from);
+  const int64_t end = start_of(p, from + 1);
   r.count = static_cast<int32_t>(end > r.first ? end - r.first : 0);
-  r.tile = static_cast<int32_t>(piece - (r.first / kPiece + b));
+  r.tile = static_cast<int32_t>(piece - (r.first / kPiece + from));
+  if (r.tile < 0 || (r.tile > 0 && static_cast<int64_t>(r.tile) * kPiece >= r.count)) r.request = -1;
   return r;
 }
 
@@ -100,138 +118,264 @@ __device__ __forceinline__ int slot_of(const ScanArgs& p, int b) {
   return slot >= 0 && slot < p.num_slots ? slot : -2;     // -2: not a slot
 }
 
-// One workgroup walks a request's pieces in order, 64 V channels of it.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) k_scan(ScanArgs p) {
-  __shared__ float maps[2][W][2][64 * V];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.x / p.blocks, c = (blockIdx.x % p.blocks) * 64 * V + lane * V;
-  const bool mine = c < p.width;
-  const int cc = mine ? c : 0;
-  const int64_t piece0 = start_of(p, b) / kPiece + b;
-  const Piece q = request_of(p, b, piece0);
-  const int slot = slot_of(p, b);
-  float H[V], speed[V];
-  for (int v = 0; v < V; ++v) {
-    speed[v] = speed_of(p.decay[cc + v], p.rate);
-    H[v] = slot >= 0 && p.resume != nullptr && p.resume[b] != 0 ? p.state[static_cast<int64_t>(slot) * p.width + cc + v] : 0.0f;
-    if (slot == -2) H[v] = __builtin_nanf("");
-  }
-  const T* x = static_cast<const T*>(p.x) + cc;
-  const T* ga = static_cast<const T*>(p.ga) + cc;
-  const T* gx = static_cast<const T*>(p.gx) + cc;
-  T* y = static_cast<T*>(p.y) + cc;
-  for (int tile = 0; tile * kPiece < q.count; ++tile) {
-    const int64_t t0 = q.first + static_cast<int64_t>(tile) * kPiece + w * R;
-    const int n = max(0, min(R, q.count - tile * kPiece - w * R));
-    float a[R][V], u[R][V], A[V], B[V];
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-    for (int t = 0; t < R; ++t) {
-      if (t < n) {
-        const Vec<T, V> xr = load<T, V>(x + (t0 + t) * p.x_stride), gr = load<T, V>(ga + (t0 + t) * p.ga_stride),
-                        ir = load<T, V>(gx + (t0 + t) * p.gx_stride);
-        for (int v = 0; v < V; ++v) {
-          const float less = one_less_exp(speed[v] * logistic(static_cast<float>(gr.v[v])));
-          a[t][v] = 1.0f - less;
-          u[t][v] = __builtin_amdgcn_sqrtf(less * (1.0f + a[t][v])) * logistic(static_cast<float>(ir.v[v])) *
-                    static_cast<float>(xr.v[v]);
-        }
-      } else {
-        for (int v = 0; v < V; ++v) a[t][v] = 1.0f, u[t][v] = 0.0f;
-      }
-      for (int v = 0; v < V; ++v) A[v] *= a[t][v], B[v] = fmaf(a[t][v], B[v], u[t][v]);
+// Handing states on between workgroups.  A workgroup takes the next piece in order by a ticket, so
+// all that it waits for has been taken by workgroups that run already and that wait for none
+// behind them: every wait ends.  (Every workgroup publishes its words, also for pieces that turn out
+// to hold no tokens, so this does not depend on what cu_seqlens holds.)  A word is 8 bytes, written
+// and read at once and all ones until then, so it needs no flag and no fence.  A piece's map is
+// published as soon as its tokens are read; the states at every kGroup-th piece go on from one to the
+// next, and a piece in between applies the maps of those before it to the last of them.  How a
+// state is put together depends on places alone, never on what came first.
+constexpr uint64_t kNone = ~0ull;
+constexpr int kGroup = W;      // a wave looks at each of the maps before, the last one at the state
+
+__device__ __forceinline__ uint64_t pack(float a, float b) {
+  if (a != a) a = __builtin_nanf("");          // no NaN reads as an empty word
+  return static_cast<uint64_t>(__builtin_bit_cast(uint32_t, a)) << 32 | __builtin_bit_cast(uint32_t, b);
+}
+__device__ __forceinline__ void publish(uint64_t* at, uint64_t word) {
+  __hip_atomic_store(at, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <int V>
+__device__ __forceinline__ void wait_for(const uint64_t* at, bool mine, uint64_t (&word)[V]) {
+  for (int v = 0; v < V; ++v) word[v] = mine ? kNone : 0;
+  for (;;) {
+    bool all = true;
+    for (int v = 0; v < V; ++v) {
+      if (word[v] == kNone) word[v] = __hip_atomic_load(at + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      all = all && word[v] != kNone;
     }
-    for (int v = 0; v < V; ++v) maps[tile & 1][w][0][lane * V + v] = A[v], maps[tile & 1][w][1][lane * V + v] = B[v];
-    __syncthreads();
-    float h[V];
-    for (int s = 0; s < W; ++s)
-      for (int v = 0; v < V; ++v) {
-        if (s == w) h[v] = H[v];
-        H[v] = fmaf(maps[tile & 1][s][0][lane * V + v], H[v], maps[tile & 1][s][1][lane * V + v]);
-      }
-    if (p.saved != nullptr && mine)
-      for (int v = 0; v < V; ++v) p.saved[((piece0 + tile) * W + w) * p.width + c + v] = h[v];
-    for (int t = 0; t < R; ++t) {
-      for (int v = 0; v < V; ++v) h[v] = fmaf(a[t][v], h[v], u[t][v]);
-      if (t < n && mine) store<T, V>(y + (t0 + t) * p.y_stride, h);
-    }
+    if (!__ballot(!all)) return;
+    __builtin_amdgcn_s_sleep(1);
   }
-  if (w == 0 && slot >= 0 && mine)
-    for (int v = 0; v < V; ++v) p.state[static_cast<int64_t>(slot) * p.width + c + v] = H[v];
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) k_scan_backward(ScanArgs p) {
-  __shared__ float maps[2][W][2][64 * V];
-  __shared__ float parts[W][64 * V];
+// The request's state, before the barrier behind which its first piece publishes: whoever overwrites the
+// slot has waited for that.
+template <int V>
+__device__ __forceinline__ void state_of(const ScanArgs& p, int slot, bool from, int c, float (&h)[V]) {
+  for (int v = 0; v < V; ++v) {
+    h[v] = from ? p.state[static_cast<int64_t>(slot) * p.width + c + v] : 0.0f;
+    asm volatile("" : "+v"(h[v]));       // its value, not its load, is here
+  }
+}
+
+// The workspace before the pieces run, and every channel's speed.
+__global__ void __launch_bounds__(256) k_scan_clear(ScanArgs p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4* to = reinterpret_cast<u32x4*>(p.ticket);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = i0; i < p.words; i += step) to[i] = u32x4{~0u, ~0u, ~0u, ~0u};
+  for (int64_t c = i0; c < p.width; c += step) p.speeds[c] = speed_of(p.decay[c], p.rate);
+}
+
+// LDS of a workgroup's waves' maps and of what it reads of the pieces before.
+template <int V>
+struct Shared {
+  float own[W][2][64 * V];
+  float prior[kGroup][2][64 * V];
+  uint32_t ticket;
+};
+
+template <int V>
+__device__ __forceinline__ void write(float (&to)[2][64 * V], int lane, const float (&a)[V], const float (&b)[V]) {
+  for (int v = 0; v < V; ++v) to[0][lane * V + v] = a[v], to[1][lane * V + v] = b[v];
+}
+template <int V>
+__device__ __forceinline__ void apply(const float (&map)[2][64 * V], int lane, float (&h)[V]) {
+  for (int v = 0; v < V; ++v) h[v] = fmaf(map[0][lane * V + v], h[v], map[1][lane * V + v]);
+}
+
+// From the waves' maps, in order of time w = 0 .. W - 1, the state that each wave starts from, and the one
+// behind the last.  `index`: of this piece; `ahead`: +1 where pieces follow each other by rising index, -1 where
+// by falling; `place`: this piece's among its request's, from the end that the states come
+// from; h: the request's state there, used by its first piece.
+template <int V, bool LINKED>
+__device__ __forceinline__ void hand_on(const ScanArgs& p, Shared<V>& s, int w, int lane, int64_t index, int ahead, int place,
+                                        int c, const float (&A)[V], const float (&B)[V], float (&h)[V], float (&end)[V]) {
+  const bool mine = c < p.width;
+  write<V>(s.own[w], lane, A, B);
+  __syncthreads();
+  const int behind = LINKED ? place % kGroup : 0;       // pieces before this one in its group
+  if (LINKED) {
+    if (w == W - 1) {
+      float a[V], b[V];
+      for (int v = 0; v < V; ++v) a[v] = 1.0f, b[v] = 0.0f;
+      for (int k = 0; k < W; ++k)
+        for (int v = 0; v < V; ++v) {
+          const float m = s.own[k][0][lane * V + v];
+          a[v] *= m, b[v] = fmaf(m, b[v], s.own[k][1][lane * V + v]);
+        }
+      if (place == 0)          // the request's first piece knows its state: its map is a constant
+        for (int v = 0; v < V; ++v) b[v] = fmaf(a[v], h[v], b[v]), a[v] = 0.0f;
+      if (mine)
+        for (int v = 0; v < V; ++v) publish(p.maps + index * p.width + c + v, pack(a[v], b[v]));
+    }
+    uint64_t word[V];
+    float a[V], b[V];
+    if (w < behind || (w == W - 1 && place > behind)) {
+      const int64_t from = index - static_cast<int64_t>(ahead) * (w < behind ? behind - w : behind + 1);
+      wait_for<V>((w < behind ? p.maps : p.ends) + from * p.width + (mine ? c : 0), mine, word);
+      for (int v = 0; v < V; ++v) {
+        a[v] = __builtin_bit_cast(float, static_cast<uint32_t>(word[v] >> 32));
+        b[v] = __builtin_bit_cast(float, static_cast<uint32_t>(word[v]));
+      }
+      write<V>(s.prior[w], lane, a, b);
+    }
+    __syncthreads();
+    if (place > behind)
+      for (int v = 0; v < V; ++v) h[v] = s.prior[W - 1][0][lane * V + v];
+    for (int k = 0; k < behind; ++k) apply<V>(s.prior[k], lane, h);
+  }
+  for (int k = 0; k < w; ++k) apply<V>(s.own[k], lane, h);
+  for (int v = 0; v < V; ++v) end[v] = h[v];
+  if (w == W - 1) {
+    apply<V>(s.own[W - 1], lane, end);
+    if (LINKED && mine)
+      for (int v = 0; v < V; ++v) publish(p.ends + index * p.width + c + v, pack(end[v], 0.0f));
+  }
+}
+
+// The piece and channels of this workgroup; direction -1 takes pieces from the last to the first.
+template <int V, bool LINKED>
+__device__ __forceinline__ int64_t next_piece(const ScanArgs& p, Shared<V>& s, int direction, int& block) {
+  uint32_t id = blockIdx.x;
+  if (LINKED) {
+    // the ticket starts at 2^32 - 1, as the clearing leaves it
+    if (threadIdx.x == 0) s.ticket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+    __syncthreads();
+    id = __builtin_amdgcn_readfirstlane(s.ticket);
+  }
+  block = static_cast<int>(id % static_cast<uint32_t>(p.blocks));
+  const int64_t piece = id / static_cast<uint32_t>(p.blocks);
+  return direction > 0 ? piece : p.pieces - 1 - piece;
+}
+
+// A piece of no request hands on nothing, but nobody may wait for it.
+template <int V, bool LINKED>
+__device__ __forceinline__ void publish_nothing(const ScanArgs& p, int64_t index, int w, int c) {
+  if (!LINKED || w != 0 || c >= p.width) return;
+  for (int v = 0; v < V; ++v) {
+    publish(p.maps + index * p.width + c + v, pack(1.0f, 0.0f));
+    publish(p.ends + index * p.width + c + v, pack(0.0f, 0.0f));
+  }
+}
+
+template <int V, bool LINKED>
+__device__ __forceinline__ void load_speeds(const ScanArgs& p, int c, float (&speed)[V]) {
+  for (int v = 0; v < V; ++v) speed[v] = LINKED ? p.speeds[c + v] : speed_of(p.decay[c + v], p.rate);
+}
+
+// One workgroup takes a piece of a request, 64 V channels of it.
+template <typename T, int V, bool LINKED>
+__global__ void __launch_bounds__(kThreads) k_scan(ScanArgs p) {
+  __shared__ Shared<V> s;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.x / p.blocks, c = (blockIdx.x % p.blocks) * 64 * V + lane * V;
+  int block;
+  const int64_t index = next_piece<V, LINKED>(p, s, 1, block);
+  const Piece q = find(p, index);
+  const int c = (block * 64 + lane) * V;
+  if (q.request < 0) return publish_nothing<V, LINKED>(p, index, w, c);
   const bool mine = c < p.width;
   const int cc = mine ? c : 0;
-  const int64_t piece0 = start_of(p, b) / kPiece + b;
-  const Piece q = request_of(p, b, piece0);
-  const int slot = slot_of(p, b);
-  const int tiles = (q.count + kPiece - 1) / kPiece;
-  // pieces of no tokens add nothing
-  const int64_t until = b + 1 < p.batch ? start_of(p, b + 1) / kPiece + b + 1 : p.pieces;
-  if (w == 0 && mine) {
-    for (int64_t j = b == 0 ? 0 : piece0 + tiles; j < until; ++j)
-      if (j < piece0 || j >= piece0 + tiles)
-        for (int v = 0; v < V; ++v) p.partial[j * p.width + c + v] = 0.0f;
-  }
-  float G[V], speed[V];
-  for (int v = 0; v < V; ++v) {
-    speed[v] = speed_of(p.decay[cc + v], p.rate);
-    G[v] = slot >= 0 ? p.state[static_cast<int64_t>(slot) * p.width + cc + v] : 0.0f;
-  }
-  const T* x = static_cast<const T*>(p.x) + cc;
-  const T* ga = static_cast<const T*>(p.ga) + cc;
-  const T* gx = static_cast<const T*>(p.gx) + cc;
-  const T* dy = static_cast<const T*>(p.dy) + cc;
-  T* dx = static_cast<T*>(p.y) + cc;
-  T* dga = static_cast<T*>(p.dga) + cc;
-  T* dgx = static_cast<T*>(p.dgx) + cc;
-  for (int tile = tiles - 1; tile >= 0; --tile) {
-    const int64_t t0 = q.first + static_cast<int64_t>(tile) * kPiece + w * R;
-    const int n = max(0, min(R, q.count - tile * kPiece - w * R));
-    float less[R][V], ra[R][V], A[V], B[V];
-    Vec<T, V> gr[R];
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-    for (int t = R - 1; t >= 0; --t) {
-      for (int v = 0; v < V; ++v) less[t][v] = 0.0f, ra[t][v] = 0.0f, gr[t].v[v] = static_cast<T>(0.0f);
-      if (t < n) {
-        const Vec<T, V> ar = load<T, V>(ga + (t0 + t) * p.ga_stride);
-        gr[t] = load<T, V>(dy + (t0 + t) * p.dy_stride);
-        for (int v = 0; v < V; ++v) {
-          ra[t][v] = logistic(static_cast<float>(ar.v[v]));
-          less[t][v] = one_less_exp(speed[v] * ra[t][v]);
-        }
+  const int slot = slot_of(p, q.request);
+  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kPiece + w * R;
+  const int n = max(0, min(R, q.count - q.tile * kPiece - w * R));
+  float a[R][V], u[R][V], A[V], B[V], h[V], end[V];
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+  for (int t = 0; t < R; ++t)
+    for (int v = 0; v < V; ++v) a[t][v] = 1.0f, u[t][v] = 0.0f;
+  if (n > 0) {
+    float speed[V];
+    load_speeds<V, LINKED>(p, cc, speed);
+    Vec<T, V> xr[R], gr[R], ir[R];
+    for (int t = 0; t < R; ++t) {                 // rows behind the last one are read as it
+      const int64_t row = t0 + min(t, n - 1);
+      xr[t] = load<T, V>(static_cast<const T*>(p.x) + row * p.x_stride + cc);
+      gr[t] = load<T, V>(static_cast<const T*>(p.ga) + row * p.ga_stride + cc);
+      ir[t] = load<T, V>(static_cast<const T*>(p.gx) + row * p.gx_stride + cc);
+    }
+    for (int t = 0; t < R; ++t)
+      for (int v = 0; v < V; ++v) {
+        const float less = one_less_exp(speed[v] * logistic(static_cast<float>(gr[t].v[v])));
+        const float keep = 1.0f - less;
+        const float in = __builtin_amdgcn_sqrtf(less * (1.0f + keep)) * logistic(static_cast<float>(ir[t].v[v])) *
+                         static_cast<float>(xr[t].v[v]);
+        a[t][v] = t < n ? keep : 1.0f;
+        u[t][v] = t < n ? in : 0.0f;
+        A[v] *= a[t][v], B[v] = fmaf(a[t][v], B[v], u[t][v]);
       }
+  }
+  state_of<V>(p, slot, q.tile == 0 && slot >= 0 && p.resume != nullptr && p.resume[q.request] != 0, cc, h);
+  if (slot == -2)
+    for (int v = 0; v < V; ++v) h[v] = __builtin_nanf("");
+  hand_on<V, LINKED>(p, s, w, lane, index, 1, q.tile, c, A, B, h, end);
+  if (!mine) return;
+  if (p.saved != nullptr)
+    for (int v = 0; v < V; ++v) p.saved[(index * W + w) * p.width + c + v] = h[v];
+  for (int t = 0; t < R; ++t) {
+    for (int v = 0; v < V; ++v) h[v] = fmaf(a[t][v], h[v], u[t][v]);
+    if (t < n) store<T, V>(static_cast<T*>(p.y) + (t0 + t) * p.y_stride + c, h);
+  }
+  if (w == W - 1 && slot >= 0 && static_cast<int64_t>(q.tile + 1) * kPiece >= q.count)
+    for (int v = 0; v < V; ++v) p.state[static_cast<int64_t>(slot) * p.width + c + v] = h[v];
+}
+
+template <typename T, int V, bool LINKED>
+__global__ void __launch_bounds__(kThreads) k_scan_backward(ScanArgs p) {
+  __shared__ Shared<V> s;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int block;
+  const int64_t index = next_piece<V, LINKED>(p, s, -1, block);
+  const Piece q = find(p, index);
+  const int c = (block * 64 + lane) * V;
+  const bool mine = c < p.width;
+  if (q.request < 0) {
+    if (w == 0 && mine)
+      for (int v = 0; v < V; ++v) p.partial[index * p.width + c + v] = 0.0f;
+    return publish_nothing<V, LINKED>(p, index, w, c);
+  }
+  const int cc = mine ? c : 0;
+  const int slot = slot_of(p, q.request);
+  // wave 0 holds the last tokens: it is the first that the gradients reach
+  const int back = W - 1 - w;
+  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kPiece + back * R;
+  const int n = max(0, min(R, q.count - q.tile * kPiece - back * R));
+  const int last = q.count > 0 ? (q.count - 1) / kPiece : 0;
+  float less[R][V], ra[R][V], A[V], B[V], g[V], end[V], speed[V];
+  Vec<T, V> gr[R], xr[R], ir[R];
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+  if (n > 0) {
+    load_speeds<V, LINKED>(p, cc, speed);
+    Vec<T, V> ar[R];
+    for (int t = 0; t < R; ++t) {
+      const int64_t row = t0 + min(t, n - 1);
+      ar[t] = load<T, V>(static_cast<const T*>(p.ga) + row * p.ga_stride + cc);
+      gr[t] = load<T, V>(static_cast<const T*>(p.dy) + row * p.dy_stride + cc);
+      xr[t] = load<T, V>(static_cast<const T*>(p.x) + row * p.x_stride + cc);
+      ir[t] = load<T, V>(static_cast<const T*>(p.gx) + row * p.gx_stride + cc);
+    }
+    for (int t = R - 1; t >= 0; --t)
+      for (int v = 0; v < V; ++v) {
+        ra[t][v] = logistic(static_cast<float>(ar[t].v[v]));
+        less[t][v] = one_less_exp(speed[v] * ra[t][v]);
+        const float keep = t < n ? 1.0f - less[t][v] : 1.0f;
+        A[v] *= keep, B[v] = keep * (B[v] + (t < n ? static_cast<float>(gr[t].v[v]) : 0.0f));
+      }
+  }
+  state_of<V>(p, slot, slot >= 0 && q.tile == last, cc, g);
+  hand_on<V, LINKED>(p, s, w, lane, index, -1, last - q.tile, c, A, B, g, end);
+  float sum[V];
+  for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+  if (n > 0) {
+    float before[R][V], h[V];
+    for (int v = 0; v < V; ++v) h[v] = p.saved[(index * W + back) * p.width + cc + v];
+    for (int t = 0; t < R; ++t)
       for (int v = 0; v < V; ++v) {
         const float a = 1.0f - less[t][v];
-        A[v] *= a, B[v] = a * (B[v] + static_cast<float>(gr[t].v[v]));
-      }
-    }
-    for (int v = 0; v < V; ++v) maps[tile & 1][w][0][lane * V + v] = A[v], maps[tile & 1][w][1][lane * V + v] = B[v];
-    __syncthreads();
-    float g[V], h[V], sum[V];
-    for (int s = W - 1; s >= 0; --s)
-      for (int v = 0; v < V; ++v) {
-        if (s == w) g[v] = G[v];
-        G[v] = fmaf(maps[tile & 1][s][0][lane * V + v], G[v], maps[tile & 1][s][1][lane * V + v]);
-      }
-    for (int v = 0; v < V; ++v) sum[v] = 0.0f, h[v] = p.saved[((piece0 + tile) * W + w) * p.width + cc + v];
-    float before[R][V];
-    Vec<T, V> xr[R], ir[R];
-    for (int t = 0; t < R; ++t)
-      if (t < n) {
-        xr[t] = load<T, V>(x + (t0 + t) * p.x_stride), ir[t] = load<T, V>(gx + (t0 + t) * p.gx_stride);
-        for (int v = 0; v < V; ++v) {
-          const float a = 1.0f - less[t][v];
-          before[t][v] = h[v];
-          h[v] = fmaf(a, h[v], __builtin_amdgcn_sqrtf(less[t][v] * (1.0f + a)) * logistic(static_cast<float>(ir[t].v[v])) *
-                                   static_cast<float>(xr[t].v[v]));
-        }
+        before[t][v] = h[v];
+        h[v] = fmaf(a, h[v], __builtin_amdgcn_sqrtf(less[t][v] * (1.0f + a)) * logistic(static_cast<float>(ir[t].v[v])) *
+                                 static_cast<float>(xr[t].v[v]));
       }
     for (int t = R - 1; t >= 0; --t)
       if (t < n) {
@@ -251,24 +395,25 @@ __global__ void __launch_bounds__(kThreads) k_scan_backward(ScanArgs p) {
           if (slot == -2) ox[v] = oi[v] = oa[v] = __builtin_nanf(""), sum[v] = 0.0f;
         }
         if (mine) {
-          store<T, V>(dx + (t0 + t) * p.y_stride, ox);
-          store<T, V>(dga + (t0 + t) * p.dga_stride, oa);
-          store<T, V>(dgx + (t0 + t) * p.dgx_stride, oi);
+          store<T, V>(static_cast<T*>(p.y) + (t0 + t) * p.y_stride + c, ox);
+          store<T, V>(static_cast<T*>(p.dga) + (t0 + t) * p.dga_stride + c, oa);
+          store<T, V>(static_cast<T*>(p.dgx) + (t0 + t) * p.dgx_stride + c, oi);
         }
       }
-    for (int v = 0; v < V; ++v) parts[w][lane * V + v] = sum[v];
-    __syncthreads();
-    if (w == 0 && mine)
-      for (int v = 0; v < V; ++v) {
-        float all = 0.0f;
-        for (int s = 0; s < W; ++s) all += parts[s][lane * V + v];
-        p.partial[(piece0 + tile) * p.width + c + v] = all;
-      }
-    __syncthreads();
   }
-  if (w == 0 && slot >= 0 && mine)
+  if (w == W - 1 && slot >= 0 && q.tile == 0 && mine)
     for (int v = 0; v < V; ++v)
-      p.state[static_cast<int64_t>(slot) * p.width + c + v] = p.resume != nullptr && p.resume[b] != 0 ? G[v] : 0.0f;
+      p.state[static_cast<int64_t>(slot) * p.width + c + v] = p.resume != nullptr && p.resume[q.request] != 0 ? end[v] : 0.0f;
+  // a sum over the piece, the waves in order
+  __syncthreads();
+  write<V>(s.own[w], lane, sum, sum);
+  __syncthreads();
+  if (w != 0 || !mine) return;
+  for (int v = 0; v < V; ++v) {
+    float all = 0.0f;
+    for (int k = 0; k < W; ++k) all += s.own[k][0][lane * V + v];
+    p.partial[index * p.width + c + v] = all;
+  }
 }
 
 // ddecay from the pieces' parts, added in order in binary64: a wave takes 64 channels and
@@ -325,25 +470,38 @@ bool in_pairs(const ScanArgs& a, int esize) {
          pair(a.y, a.y_stride) && pair(a.dy, a.dy_stride) && pair(a.dga, a.dga_stride) && pair(a.dgx, a.dgx_stride);
 }
 
-template <typename T>
-hipError_t forward(ScanArgs a, hipStream_t s) {
-  const bool two = in_pairs(a, sizeof(T));
+// Every piece's workgroups, behind the clearing of the words that they hand on.
+template <typename T, bool BACK>
+hipError_t over_pieces(ScanArgs a, hipStream_t s) {
+  const bool two = in_pairs(a, sizeof(T)), linked = a.ticket != nullptr;
   a.blocks = two ? (a.width + 127) / 128 : (a.width + 63) / 64;
-  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.batch) * a.blocks));
-  if (two) k_scan<T, 2><<<grid, kThreads, 0, s>>>(a);
-  else k_scan<T, 1><<<grid, kThreads, 0, s>>>(a);
+  if (linked) {
+    const int64_t all = (a.words + 255) / 256;
+    k_scan_clear<<<dim3(static_cast<uint32_t>(all < 1024 ? all : 1024)), 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.pieces) * a.blocks));
+  const auto go = [&](auto v, auto l) {
+    constexpr int V = decltype(v)::value;
+    constexpr bool LINKED = decltype(l)::value;
+    if (BACK) k_scan_backward<T, V, LINKED><<<grid, kThreads, 0, s>>>(a);
+    else k_scan<T, V, LINKED><<<grid, kThreads, 0, s>>>(a);
+  };
+  const std::integral_constant<int, 1> one{};
+  const std::integral_constant<int, 2> pair{};
+  if (two) linked ? go(pair, std::true_type{}) : go(pair, std::false_type{});
+  else linked ? go(one, std::true_type{}) : go(one, std::false_type{});
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t backward(ScanArgs a, hipStream_t s) {
+hipError_t forward(const ScanArgs& a, hipStream_t s) { return over_pieces<T, false>(a, s); }
+
+template <typename T>
+hipError_t backward(const ScanArgs& a, hipStream_t s) {
   if (a.pieces > 0) {
-    const bool two = in_pairs(a, sizeof(T));
-    a.blocks = two ? (a.width + 127) / 128 : (a.width + 63) / 64;
-    const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.batch) * a.blocks));
-    if (two) k_scan_backward<T, 2><<<grid, kThreads, 0, s>>>(a);
-    else k_scan_backward<T, 1><<<grid, kThreads, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = over_pieces<T, true>(a, s);
     if (e != hipSuccess) return e;
   }
   k_scan_decay<<<dim3(static_cast<uint32_t>((a.width + 63) / 64)), 1024, 0, s>>>(a);
