@@ -26,12 +26,12 @@ stepq_status check_sizes(const stepq_scan_desc* d, int32_t batch, int64_t total_
   if (batch < 0 || total_tokens < 0) return STEPQ_ERR_INVALID_ARG;
   if (total_tokens > 0x7fffffffLL) return STEPQ_ERR_UNSUPPORTED;
   const int64_t blocks = (d->width + 63) / 64;
-  return stepq::scan_pieces(total_tokens, batch) > kMostGroups / blocks ? STEPQ_ERR_UNSUPPORTED : STEPQ_OK;
+  return stepq::scan_pieces(total_tokens, batch, stepq::kBackPiece) > kMostGroups / blocks ? STEPQ_ERR_UNSUPPORTED : STEPQ_OK;
 }
 
 // A tensor of tokens: [tokens][width], tokens `stride` apart.
 bool rows_ok(const void* p, int64_t stride, const stepq_scan_desc& d) {
-  return p && aligned(p, elem_bytes(d.dtype)) && stride >= d.width && stride <= (int64_t{1} << 40);
+  return p && aligned(p, elem_bytes(d.dtype)) && stride >= d.width && stride <= (int64_t{1} << 24);
 }
 
 stepq_status check_slots(const int32_t* slot_ids, const float* state, int32_t num_slots) {
@@ -60,12 +60,14 @@ extern "C" {
 
 size_t stepq_scan_workspace_bytes(const stepq_scan_desc* d, int32_t batch, int64_t total_tokens) {
   if (check_sizes(d, batch, total_tokens) != STEPQ_OK) return 0;
-  return stepq::scan_workspace(*d, total_tokens, batch, true).bytes;
+  const size_t forward = stepq::scan_workspace(*d, total_tokens, batch, false).bytes;
+  const size_t backward = stepq::scan_workspace(*d, total_tokens, batch, true).bytes;
+  return forward > backward ? forward : backward;
 }
 
 size_t stepq_scan_saved_bytes(const stepq_scan_desc* d, int32_t batch, int64_t total_tokens) {
   if (check_sizes(d, batch, total_tokens) != STEPQ_OK) return 0;
-  return static_cast<size_t>(stepq::scan_pieces(total_tokens, batch)) * stepq::kScanRows * d->width * sizeof(float);
+  return stepq::scan_saved(*d, total_tokens, batch);
 }
 
 stepq_status stepq_scan_forward(const stepq_scan_desc* d, int32_t batch, int64_t total_tokens, const int32_t* cu_seqlens,
@@ -92,7 +94,7 @@ stepq_status stepq_scan_forward(const stepq_scan_desc* d, int32_t batch, int64_t
   a.decay = decay; a.cu_seqlens = cu_seqlens; a.slot_ids = slot_ids; a.resume = resume; a.state = state;
   a.saved = static_cast<float*>(saved);
   a.total_tokens = total_tokens; a.batch = batch; a.num_slots = num_slots; a.width = d->width; a.rate = d->rate;
-  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch));
+  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch, stepq::kScanPiece));
   place(a, *d, workspace, w);
   return from_hip(stepq::launch_scan_forward(a, d->dtype, static_cast<hipStream_t>(stream)));
 }
@@ -128,7 +130,7 @@ stepq_status stepq_scan_backward(const stepq_scan_desc* d, int32_t batch, int64_
   a.saved = const_cast<float*>(static_cast<const float*>(saved));
   a.ddecay = ddecay;
   a.total_tokens = total_tokens; a.batch = batch; a.num_slots = num_slots; a.width = d->width; a.rate = d->rate;
-  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch));
+  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch, stepq::kBackPiece));
   if (batch == 0) a.pieces = 0;
   else place(a, *d, workspace, w);
   return from_hip(stepq::launch_scan_backward(a, d->dtype, static_cast<hipStream_t>(stream)));

@@ -11,9 +11,16 @@
 
 namespace stepq {
 
-constexpr int kScanTokens = 8;                            // tokens a wave holds
-constexpr int kScanRows = 8;                              // waves of a workgroup, one behind the other in time
-constexpr int kPiece = kScanTokens * kScanRows;           // tokens of a workgroup
+// Tokens that a wave holds, and waves of a workgroup, one behind the other in time.  us of a prompt of
+// 32768 tokens x 4096 bfloat16 channels, of 8 prompts of 8192 x 6144:
+//   16 tokens of 4 waves 300, 116;  16 of 8 253, 107;  16 of 16 324, 138;  32 of 4 238, 105;  32 of 8 271, 117
+// The backward pass holds twice the tensors: us of forward and backward of 12288 tokens x 4096 with 8 tokens of
+// 4 waves 345, of 6 422, of 8 300, of 16 446; 16 tokens of 4 waves 390.
+constexpr int kScanTokens = 32, kScanWaves = 4;
+constexpr int kBackTokens = 8, kBackWaves = 8;
+constexpr int kScanPiece = kScanTokens * kScanWaves;      // tokens of a workgroup
+constexpr int kBackPiece = kBackTokens * kBackWaves;
+static_assert(kScanTokens % kBackTokens == 0);            // a forward pass saves a state every kBackTokens tokens
 
 struct ScanArgs {
   const void* x;
@@ -52,13 +59,10 @@ struct ScanArgs {
   float rate;
 };
 
-// Pieces of all requests together: request b's start at index cu_seqlens[b] / kPiece + b, so
-// that no table of them is needed.  From b to b + 1 the index grows by at least the
-// ceil((cu[b + 1] - cu[b]) / kPiece) pieces of request b, and by 1 for an empty one.
-inline int64_t scan_pieces(int64_t total_tokens, int64_t batch) { return total_tokens / kPiece + batch; }
-
-// Requests of a piece or less have nothing to hand on.
-inline bool scan_linked(int64_t total_tokens) { return total_tokens > kPiece; }
+// Pieces of `piece` tokens of all requests together: request b's start at index
+// cu_seqlens[b] / piece + b, so that no table of them is needed.  From b to b + 1 the index grows by
+// at least the ceil((cu[b + 1] - cu[b]) / piece) pieces of request b, and by 1 for an empty one.
+inline int64_t scan_pieces(int64_t total_tokens, int64_t batch, int piece) { return total_tokens / piece + batch; }
 
 // What a call over requests longer than a piece keeps in its workspace: a ticket (at 0), every
 // piece's map of the state before it to the state behind it, the states behind pieces, each
@@ -69,8 +73,9 @@ struct ScanWorkspace {
 };
 inline ScanWorkspace scan_workspace(const stepq_scan_desc& d, int64_t total_tokens, int64_t batch, bool backward) {
   const auto whole = [](size_t bytes) { return (bytes + 15) / 16 * 16; };
-  const size_t n = static_cast<size_t>(scan_pieces(total_tokens, batch)) * d.width;
-  const bool linked = scan_linked(total_tokens);
+  const int piece = backward ? kBackPiece : kScanPiece;
+  const size_t n = static_cast<size_t>(scan_pieces(total_tokens, batch, piece)) * d.width;
+  const bool linked = total_tokens > piece;      // requests of a piece or less have nothing to hand on
   ScanWorkspace w{};
   w.maps = linked ? 16 : 0;
   w.ends = w.maps + (linked ? whole(n * 8) : 0);
@@ -78,6 +83,11 @@ inline ScanWorkspace scan_workspace(const stepq_scan_desc& d, int64_t total_toke
   w.partial = w.speeds + (linked ? whole(static_cast<size_t>(d.width) * 4) : 0);
   w.bytes = w.partial + (backward ? whole(n * 4) : 0);
   return w;
+}
+
+// Saved: the states before every kBackTokens tokens, by the same index rule.
+inline size_t scan_saved(const stepq_scan_desc& d, int64_t total_tokens, int64_t batch) {
+  return static_cast<size_t>(scan_pieces(total_tokens, batch, kBackTokens)) * d.width * sizeof(float);
 }
 
 hipError_t launch_scan_forward(const ScanArgs& a, int dtype, hipStream_t s);

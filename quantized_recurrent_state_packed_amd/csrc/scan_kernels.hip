@@ -5,9 +5,8 @@
 //   h_t = a_t h_{t-1} + u_t,  u_t = b_t s(gx_t) x_t,  y_t = h_t
 //
 // A run of tokens is an affine map of the state before it, h -> A h + B, and maps
-// of neighbouring runs compose.  A wave holds kScanTokens tokens of 64 V channels in registers,
-// the kScanRows waves of a workgroup follow each other in time and make up a piece of kPiece
-// tokens.  Each wave works out its map, the maps meet in LDS, states are handed on from piece to
+// of neighbouring runs compose.  A wave holds some tokens of 64 V channels in registers,
+// the waves of a workgroup follow each other in time and make up a piece.  Each wave works out its map, the maps meet in LDS, states are handed on from piece to
 // piece (hand_on), and every wave walks its tokens from the state that it starts from.  So
 // every tensor is read or written once, whatever a request's length, and one long request
 // spreads over the chip like many short ones.
@@ -26,53 +25,82 @@
 namespace stepq {
 namespace {
 
-constexpr int R = kScanTokens;
-constexpr int W = kScanRows;
-constexpr int kThreads = 64 * W;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2 = 0.6931471805599453f;
 
-// V neighbouring channels of a token.
+// V neighbouring channels of a token, as they lie in memory until they are used: 16-bit pairs stay in
+// one register.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<2> { typedef uint16_t type; };
+template <>
+struct Word<4> { typedef uint32_t type; };
+template <>
+struct Word<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
+
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T v[V];
+struct Vec {
+  typedef typename Word<sizeof(T) * V>::type Raw;
+  Raw raw;
+  __device__ __forceinline__ float operator[](int v) const {
+    if constexpr (sizeof(T) == 4) {
+      if constexpr (V == 1) return __builtin_bit_cast(float, raw);
+      else return __builtin_bit_cast(float, static_cast<uint32_t>(raw[v]));
+    } else if constexpr (std::is_same<T, __bf16>::value) {
+      if constexpr (V == 1) return __builtin_bit_cast(float, static_cast<uint32_t>(raw) << 16);
+      else return __builtin_bit_cast(float, v ? raw & 0xffff0000u : raw << 16);
+    } else {
+      return static_cast<float>(__builtin_bit_cast(T, static_cast<uint16_t>(v ? static_cast<uint32_t>(raw) >> 16 : raw)));
+    }
+  }
 };
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const T* p) {
-  return *reinterpret_cast<const Vec<T, V>*>(p);
+  return {*reinterpret_cast<const typename Vec<T, V>::Raw*>(p)};
+}
+template <typename T, int V>
+__device__ __forceinline__ typename Vec<T, V>::Raw rounded(const float (&x)[V]) {
+  typedef T Some __attribute__((ext_vector_type(V)));
+  Some r;
+  for (int i = 0; i < V; ++i) r[i] = static_cast<T>(x[i]);
+  return __builtin_bit_cast(typename Vec<T, V>::Raw, r);
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float (&x)[V]) {
-  Vec<T, V> r;
-  for (int i = 0; i < V; ++i) r.v[i] = static_cast<T>(x[i]);
-  *reinterpret_cast<Vec<T, V>*>(p) = r;
+  *reinterpret_cast<typename Vec<T, V>::Raw*>(p) = rounded<T, V>(x);
+}
+
+// Keeps the compiler from holding on to what it worked out of these values before.
+template <typename T, int V>
+__device__ __forceinline__ void again(Vec<T, V>& x) {
+  if constexpr (sizeof(x) >= 4) asm volatile("" : "+v"(x.raw));
 }
 
 __device__ __forceinline__ float logistic(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
 
-// 1 - exp(z) for z <= 0, good to a few 2^-24 of itself: the series up to z^7 for |z| below
-// log(2) / 2 (the next term is 1.5e-8 of the sum there), beyond it the difference, which
-// the rounding of exp leaves 1.4e-7 of itself at worst.
-__device__ __forceinline__ float one_less_exp(float z) {
-  float s = 1.0f / 5040.0f;
-  s = fmaf(s, z, 1.0f / 720.0f);
-  s = fmaf(s, z, 1.0f / 120.0f);
-  s = fmaf(s, z, 1.0f / 24.0f);
-  s = fmaf(s, z, 1.0f / 6.0f);
-  s = fmaf(s, z, 0.5f);
-  s = fmaf(s, z, 1.0f);
-  const float far = 1.0f - __builtin_amdgcn_exp2f(z * kLog2e);
-  return z > -0.34657359f ? -z * s : far;
+// 1 - 2^z for z <= 0.  Up to |z| = 1/4 the series up to z^5 (the next term is 4e-8 of the sum
+// there); beyond it the difference, off by half a step of 2^z, which is 2e-7 of it at worst.  The
+// retention, 1 less this, has half a step's error of its own either way.
+__device__ __forceinline__ float one_less_exp2(float z) {
+  float s = 1.3333558e-3f;                     // log(2)^k / k!
+  s = fmaf(s, z, 9.6181291e-3f);
+  s = fmaf(s, z, 5.5504109e-2f);
+  s = fmaf(s, z, 2.4022651e-1f);
+  s = fmaf(s, z, 6.9314718e-1f);
+  const float far = 1.0f - __builtin_amdgcn_exp2f(z);
+  return z > -0.25f ? -z * s : far;
 }
 
-// -rate softplus(decay), the logarithm of the retention at an open gate; log1p by the
+// -rate softplus(decay) log2(e), the binary logarithm of the retention at an open gate; log1p by the
 // quotient that takes the rounding of 1 + e back out.
 __device__ __forceinline__ float speed_of(float decay, float rate) {
   const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(decay));
   const float w = 1.0f + e;
   const float l = w == 1.0f ? e : logf(w) * (e / (w - 1.0f));
-  return -rate * (fmaxf(decay, 0.0f) + l);
+  return -rate * kLog2e * (fmaxf(decay, 0.0f) + l);
 }
 
 // The request whose pieces hold index `piece`, and which of them it is.
@@ -89,32 +117,55 @@ __device__ __forceinline__ int64_t start_of(const ScanArgs& p, int b) {
 }
 
 // The last request that begins at this index or before it, 64 at a time.
+template <int PIECE>
 __device__ __forceinline__ Piece find(const ScanArgs& p, int64_t piece) {
   const int lane = threadIdx.x & 63;
   Piece r = {-1, 0, 0, 0};
   int from = 0, n = p.batch;
   for (bool more = true; more;) {
     const int step = (n + 63) / 64, at = from + lane * step;
-    const bool before = lane * step < n && start_of(p, at) / kPiece + at <= piece;
+    const bool before = lane * step < n && start_of(p, at) / PIECE + at <= piece;
     const int count = __popcll(__ballot(before));
     if (count == 0) return r;                 // rows before the first request
     from += (count - 1) * step;
     n = min(step, n - (count - 1) * step);
     more = step > 1;
   }
+  // the same in all lanes, and the compiler is to know: addresses of rows stay in scalar registers
   from = __builtin_amdgcn_readfirstlane(from);
   r.request = from;
-  r.first = start_of(p, from);
-  const int64_t end = start_of(p, from + 1);
-  r.count = static_cast<int32_t>(end > r.first ? end - r.first : 0);
-  r.tile = static_cast<int32_t>(piece - (r.first / kPiece + from));
-  if (r.tile < 0 || (r.tile > 0 && static_cast<int64_t>(r.tile) * kPiece >= r.count)) r.request = -1;
+  const int32_t first = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(start_of(p, from)));
+  const int32_t end = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(start_of(p, from + 1)));
+  r.first = first;
+  r.count = end > first ? end - first : 0;
+  r.tile = static_cast<int32_t>(piece - (r.first / PIECE + from));
+  if (r.tile < 0 || (r.tile > 0 && static_cast<int64_t>(r.tile) * PIECE >= r.count)) r.request = -1;
   return r;
 }
 
+// Some tokens' rows: the first one's start in scalar registers, a lane's offset from there in 32 bits
+// (strides are at most 2^24 elements).
+template <typename T, int V>
+struct Rows {
+  typedef __attribute__((address_space(1))) typename Vec<T, V>::Raw Global;
+  typedef __attribute__((address_space(1))) char Byte;
+  uint64_t first;
+  uint32_t stride, column;      // bytes
+  __device__ __forceinline__ Rows(const void* p, int64_t stride, int64_t row, uint32_t column)
+      : first(reinterpret_cast<uint64_t>(static_cast<const T*>(p) + row * stride)), stride(static_cast<uint32_t>(stride * sizeof(T))),
+        column(static_cast<uint32_t>(column * sizeof(T))) {
+    asm("" : "+s"(first));
+  }
+  __device__ __forceinline__ Global* at(int t) const {
+    return reinterpret_cast<Global*>(reinterpret_cast<Byte*>(first) + (static_cast<uint32_t>(t) * stride + column));
+  }
+  __device__ __forceinline__ Vec<T, V> load(int t) const { return {*at(t)}; }
+  __device__ __forceinline__ void store(int t, const float (&x)[V]) const { *at(t) = rounded<T, V>(x); }
+};
+
 __device__ __forceinline__ int slot_of(const ScanArgs& p, int b) {
   if (p.slot_ids == nullptr) return -1;
-  const int slot = p.slot_ids[b];
+  const int slot = __builtin_amdgcn_readfirstlane(p.slot_ids[b]);
   return slot >= 0 && slot < p.num_slots ? slot : -2;     // -2: not a slot
 }
 
@@ -122,31 +173,44 @@ __device__ __forceinline__ int slot_of(const ScanArgs& p, int b) {
 // all that it waits for has been taken by workgroups that run already and that wait for none
 // behind them: every wait ends.  (Every workgroup publishes its words, also for pieces that turn out
 // to hold no tokens, so this does not depend on what cu_seqlens holds.)  A word is 8 bytes, written
-// and read at once and all ones until then, so it needs no flag and no fence.  A piece's map is
-// published as soon as its tokens are read; the states at every kGroup-th piece go on from one to the
-// next, and a piece in between applies the maps of those before it to the last of them.  How a
+// and read at once and all ones until then, so it needs no flag and no fence.
+// A piece's map is published in `maps` as soon as its tokens are read.  W pieces make a group (W waves of
+// a workgroup, one looking at each map), W groups a run: a group's last piece publishes the group's
+// map in `ends` when it has the maps of the others, a run's last piece the state behind it, as a
+// constant map.  A piece applies the state before its run, the maps of the groups before its own and
+// those of the pieces before it.  So states go from run to run, W W pieces at a time (64 of them; with groups alone,
+// 8 pieces at a time, the way from one to the next, some 3 us under load, held up the whole pass).  How a
 // state is put together depends on places alone, never on what came first.
 constexpr uint64_t kNone = ~0ull;
-constexpr int kGroup = W;      // a wave looks at each of the maps before, the last one at the state
 
 __device__ __forceinline__ uint64_t pack(float a, float b) {
   if (a != a) a = __builtin_nanf("");          // no NaN reads as an empty word
   return static_cast<uint64_t>(__builtin_bit_cast(uint32_t, a)) << 32 | __builtin_bit_cast(uint32_t, b);
 }
-__device__ __forceinline__ void publish(uint64_t* at, uint64_t word) {
-  __hip_atomic_store(at, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+template <int V>
+__device__ __forceinline__ void publish(uint64_t* words, int64_t index, int width, int c, const float (&a)[V],
+                                        const float (&b)[V]) {
+  if (c >= width) return;
+  for (int v = 0; v < V; ++v)
+    __hip_atomic_store(words + index * width + c + v, pack(a[v], b[v]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 template <int V>
-__device__ __forceinline__ void wait_for(const uint64_t* at, bool mine, uint64_t (&word)[V]) {
-  for (int v = 0; v < V; ++v) word[v] = mine ? kNone : 0;
+__device__ __forceinline__ void wait_for(const uint64_t* words, int64_t index, int width, int c, float (&a)[V], float (&b)[V]) {
+  const uint64_t* at = words + index * width + (c < width ? c : 0);
+  uint64_t word[V];
+  for (int v = 0; v < V; ++v) word[v] = c < width ? kNone : 0;
   for (;;) {
     bool all = true;
     for (int v = 0; v < V; ++v) {
       if (word[v] == kNone) word[v] = __hip_atomic_load(at + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       all = all && word[v] != kNone;
     }
-    if (!__ballot(!all)) return;
+    if (!__ballot(!all)) break;
     __builtin_amdgcn_s_sleep(1);
+  }
+  for (int v = 0; v < V; ++v) {
+    a[v] = __builtin_bit_cast(float, static_cast<uint32_t>(word[v] >> 32));
+    b[v] = __builtin_bit_cast(float, static_cast<uint32_t>(word[v]));
   }
 }
 
@@ -169,11 +233,12 @@ __global__ void __launch_bounds__(256) k_scan_clear(ScanArgs p) {
   for (int64_t c = i0; c < p.width; c += step) p.speeds[c] = speed_of(p.decay[c], p.rate);
 }
 
-// LDS of a workgroup's waves' maps and of what it reads of the pieces before.
-template <int V>
+// LDS of a workgroup's waves' maps, and of the maps before it: of pieces, of groups, and of runs.
+template <int V, int W>
 struct Shared {
   float own[W][2][64 * V];
-  float prior[kGroup][2][64 * V];
+  float pieces[W - 1][2][64 * V];
+  float groups[W][2][64 * V];        // the last one: the state before the run
   uint32_t ticket;
 };
 
@@ -186,59 +251,72 @@ __device__ __forceinline__ void apply(const float (&map)[2][64 * V], int lane, f
   for (int v = 0; v < V; ++v) h[v] = fmaf(map[0][lane * V + v], h[v], map[1][lane * V + v]);
 }
 
+// (a, b) becomes the map of what it was of and then of this one.
+template <int V>
+__device__ __forceinline__ void compose(const float (&map)[2][64 * V], int lane, float (&a)[V], float (&b)[V]) {
+  for (int v = 0; v < V; ++v) {
+    const float m = map[0][lane * V + v];
+    a[v] *= m, b[v] = fmaf(m, b[v], map[1][lane * V + v]);
+  }
+}
+
 // From the waves' maps, in order of time w = 0 .. W - 1, the state that each wave starts from, and the one
 // behind the last.  `index`: of this piece; `ahead`: +1 where pieces follow each other by rising index, -1 where
 // by falling; `place`: this piece's among its request's, from the end that the states come
 // from; h: the request's state there, used by its first piece.
-template <int V, bool LINKED>
-__device__ __forceinline__ void hand_on(const ScanArgs& p, Shared<V>& s, int w, int lane, int64_t index, int ahead, int place,
+template <int V, int W, bool LINKED>
+__device__ __forceinline__ void hand_on(const ScanArgs& p, Shared<V, W>& s, int w, int lane, int64_t index, int ahead, int place,
                                         int c, const float (&A)[V], const float (&B)[V], float (&h)[V], float (&end)[V]) {
-  const bool mine = c < p.width;
   write<V>(s.own[w], lane, A, B);
   __syncthreads();
-  const int behind = LINKED ? place % kGroup : 0;       // pieces before this one in its group
+  // pieces of its group, groups of its run before this one; where the run begins
+  const int behind = LINKED ? place % W : 0, groups = LINKED ? place / W % W : 0, run = LINKED ? place % (W * W) : 0;
   if (LINKED) {
+    float a[V], b[V];
     if (w == W - 1) {
-      float a[V], b[V];
       for (int v = 0; v < V; ++v) a[v] = 1.0f, b[v] = 0.0f;
-      for (int k = 0; k < W; ++k)
-        for (int v = 0; v < V; ++v) {
-          const float m = s.own[k][0][lane * V + v];
-          a[v] *= m, b[v] = fmaf(m, b[v], s.own[k][1][lane * V + v]);
-        }
+      for (int k = 0; k < W; ++k) compose<V>(s.own[k], lane, a, b);
       if (place == 0)          // the request's first piece knows its state: its map is a constant
         for (int v = 0; v < V; ++v) b[v] = fmaf(a[v], h[v], b[v]), a[v] = 0.0f;
-      if (mine)
-        for (int v = 0; v < V; ++v) publish(p.maps + index * p.width + c + v, pack(a[v], b[v]));
-    }
-    uint64_t word[V];
-    float a[V], b[V];
-    if (w < behind || (w == W - 1 && place > behind)) {
-      const int64_t from = index - static_cast<int64_t>(ahead) * (w < behind ? behind - w : behind + 1);
-      wait_for<V>((w < behind ? p.maps : p.ends) + from * p.width + (mine ? c : 0), mine, word);
-      for (int v = 0; v < V; ++v) {
-        a[v] = __builtin_bit_cast(float, static_cast<uint32_t>(word[v] >> 32));
-        b[v] = __builtin_bit_cast(float, static_cast<uint32_t>(word[v]));
-      }
-      write<V>(s.prior[w], lane, a, b);
+      publish<V>(p.maps, index, p.width, c, a, b);
+      if (behind != W - 1) publish<V>(p.ends, index, p.width, c, a, b);       // nobody asks for it
+    } else if (w < behind) {
+      wait_for<V>(p.maps, index - static_cast<int64_t>(ahead) * (behind - w), p.width, c, a, b);
+      write<V>(s.pieces[w], lane, a, b);
     }
     __syncthreads();
-    if (place > behind)
-      for (int v = 0; v < V; ++v) h[v] = s.prior[W - 1][0][lane * V + v];
-    for (int k = 0; k < behind; ++k) apply<V>(s.prior[k], lane, h);
+    if (w == W - 1 && behind == W - 1 && run != W * W - 1) {
+      float ga[V], gb[V];
+      for (int v = 0; v < V; ++v) ga[v] = 1.0f, gb[v] = 0.0f;
+      for (int k = 0; k < W - 1; ++k) compose<V>(s.pieces[k], lane, ga, gb);
+      for (int v = 0; v < V; ++v) gb[v] = fmaf(a[v], gb[v], b[v]), ga[v] *= a[v];
+      publish<V>(p.ends, index, p.width, c, ga, gb);
+    }
+    if (w < groups || (w == W - 1 && place > run)) {
+      const int back = w < groups ? behind + 1 + W * (groups - 1 - w) : run + 1;
+      wait_for<V>(p.ends, index - static_cast<int64_t>(ahead) * back, p.width, c, a, b);
+      write<V>(s.groups[w], lane, a, b);
+    }
+    __syncthreads();
+    if (place > run) apply<V>(s.groups[W - 1], lane, h);
+    for (int k = 0; k < groups; ++k) apply<V>(s.groups[k], lane, h);
+    for (int k = 0; k < behind; ++k) apply<V>(s.pieces[k], lane, h);
   }
   for (int k = 0; k < w; ++k) apply<V>(s.own[k], lane, h);
   for (int v = 0; v < V; ++v) end[v] = h[v];
   if (w == W - 1) {
     apply<V>(s.own[W - 1], lane, end);
-    if (LINKED && mine)
-      for (int v = 0; v < V; ++v) publish(p.ends + index * p.width + c + v, pack(end[v], 0.0f));
+    if (LINKED && run == W * W - 1) {
+      float none[V];
+      for (int v = 0; v < V; ++v) none[v] = 0.0f;
+      publish<V>(p.ends, index, p.width, c, none, end);
+    }
   }
 }
 
 // The piece and channels of this workgroup; direction -1 takes pieces from the last to the first.
-template <int V, bool LINKED>
-__device__ __forceinline__ int64_t next_piece(const ScanArgs& p, Shared<V>& s, int direction, int& block) {
+template <int V, int W, bool LINKED>
+__device__ __forceinline__ int64_t next_piece(const ScanArgs& p, Shared<V, W>& s, int direction, int& block) {
   uint32_t id = blockIdx.x;
   if (LINKED) {
     // the ticket starts at 2^32 - 1, as the clearing leaves it
@@ -254,11 +332,11 @@ __device__ __forceinline__ int64_t next_piece(const ScanArgs& p, Shared<V>& s, i
 // A piece of no request hands on nothing, but nobody may wait for it.
 template <int V, bool LINKED>
 __device__ __forceinline__ void publish_nothing(const ScanArgs& p, int64_t index, int w, int c) {
-  if (!LINKED || w != 0 || c >= p.width) return;
-  for (int v = 0; v < V; ++v) {
-    publish(p.maps + index * p.width + c + v, pack(1.0f, 0.0f));
-    publish(p.ends + index * p.width + c + v, pack(0.0f, 0.0f));
-  }
+  if (!LINKED || w != 0) return;
+  float a[V], b[V];
+  for (int v = 0; v < V; ++v) a[v] = 1.0f, b[v] = 0.0f;
+  publish<V>(p.maps, index, p.width, c, a, b);
+  publish<V>(p.ends, index, p.width, c, a, b);
 }
 
 template <int V, bool LINKED>
@@ -268,66 +346,78 @@ __device__ __forceinline__ void load_speeds(const ScanArgs& p, int c, float (&sp
 
 // One workgroup takes a piece of a request, 64 V channels of it.
 template <typename T, int V, bool LINKED>
-__global__ void __launch_bounds__(kThreads) k_scan(ScanArgs p) {
-  __shared__ Shared<V> s;
+__global__ void __launch_bounds__(64 * kScanWaves) k_scan(ScanArgs p) {
+  constexpr int R = kScanTokens, W = kScanWaves;
+  __shared__ Shared<V, W> s;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int block;
-  const int64_t index = next_piece<V, LINKED>(p, s, 1, block);
-  const Piece q = find(p, index);
+  const int64_t index = next_piece<V, W, LINKED>(p, s, 1, block);
+  const Piece q = find<kScanPiece>(p, index);
   const int c = (block * 64 + lane) * V;
   if (q.request < 0) return publish_nothing<V, LINKED>(p, index, w, c);
   const bool mine = c < p.width;
-  const int cc = mine ? c : 0;
+  const uint32_t cc = mine ? c : 0;
   const int slot = slot_of(p, q.request);
-  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kPiece + w * R;
-  const int n = max(0, min(R, q.count - q.tile * kPiece - w * R));
+  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kScanPiece + w * R;
+  const int n = max(0, min(R, q.count - q.tile * kScanPiece - w * R));
   float a[R][V], u[R][V], A[V], B[V], h[V], end[V];
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-  for (int t = 0; t < R; ++t)
-    for (int v = 0; v < V; ++v) a[t][v] = 1.0f, u[t][v] = 0.0f;
-  if (n > 0) {
+  const auto read = [&](auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
     float speed[V];
     load_speeds<V, LINKED>(p, cc, speed);
     Vec<T, V> xr[R], gr[R], ir[R];
+    const Rows<T, V> x(p.x, p.x_stride, t0, cc), ga(p.ga, p.ga_stride, t0, cc), gx(p.gx, p.gx_stride, t0, cc);
     for (int t = 0; t < R; ++t) {                 // rows behind the last one are read as it
-      const int64_t row = t0 + min(t, n - 1);
-      xr[t] = load<T, V>(static_cast<const T*>(p.x) + row * p.x_stride + cc);
-      gr[t] = load<T, V>(static_cast<const T*>(p.ga) + row * p.ga_stride + cc);
-      ir[t] = load<T, V>(static_cast<const T*>(p.gx) + row * p.gx_stride + cc);
+      const int row = WHOLE ? t : min(t, n - 1);
+      xr[t] = x.load(row);
+      gr[t] = ga.load(row);
+      ir[t] = gx.load(row);
     }
     for (int t = 0; t < R; ++t)
       for (int v = 0; v < V; ++v) {
-        const float less = one_less_exp(speed[v] * logistic(static_cast<float>(gr[t].v[v])));
+        const float less = one_less_exp2(speed[v] * logistic(gr[t][v]));
         const float keep = 1.0f - less;
-        const float in = __builtin_amdgcn_sqrtf(less * (1.0f + keep)) * logistic(static_cast<float>(ir[t].v[v])) *
-                         static_cast<float>(xr[t].v[v]);
-        a[t][v] = t < n ? keep : 1.0f;
-        u[t][v] = t < n ? in : 0.0f;
+        const float in = __builtin_amdgcn_sqrtf(less * (1.0f + keep)) * logistic(ir[t][v]) *
+                         xr[t][v];
+        a[t][v] = WHOLE || t < n ? keep : 1.0f;
+        u[t][v] = WHOLE || t < n ? in : 0.0f;
         A[v] *= a[t][v], B[v] = fmaf(a[t][v], B[v], u[t][v]);
       }
+  };
+  if (n == R) {
+    read(std::true_type{});
+  } else {
+    for (int t = 0; t < R; ++t)
+      for (int v = 0; v < V; ++v) a[t][v] = 1.0f, u[t][v] = 0.0f;
+    if (n > 0) read(std::false_type{});
   }
   state_of<V>(p, slot, q.tile == 0 && slot >= 0 && p.resume != nullptr && p.resume[q.request] != 0, cc, h);
   if (slot == -2)
     for (int v = 0; v < V; ++v) h[v] = __builtin_nanf("");
-  hand_on<V, LINKED>(p, s, w, lane, index, 1, q.tile, c, A, B, h, end);
+  hand_on<V, W, LINKED>(p, s, w, lane, index, 1, q.tile, c, A, B, h, end);
   if (!mine) return;
-  if (p.saved != nullptr)
-    for (int v = 0; v < V; ++v) p.saved[(index * W + w) * p.width + c + v] = h[v];
+  // as find() does for pieces: the states before every kBackTokens tokens
+  const Rows<T, V> y(p.y, p.y_stride, t0, cc);
+  float* saved = p.saved == nullptr ? nullptr : p.saved + (q.first / kBackTokens + q.request + (q.tile * W + w) * (R / kBackTokens)) * p.width + cc;
   for (int t = 0; t < R; ++t) {
+    if (t % kBackTokens == 0 && t < n && saved != nullptr)
+      for (int v = 0; v < V; ++v) saved[t / kBackTokens * static_cast<int64_t>(p.width) + v] = h[v];
     for (int v = 0; v < V; ++v) h[v] = fmaf(a[t][v], h[v], u[t][v]);
-    if (t < n) store<T, V>(static_cast<T*>(p.y) + (t0 + t) * p.y_stride + c, h);
+    if (t < n) y.store(t, h);
   }
-  if (w == W - 1 && slot >= 0 && static_cast<int64_t>(q.tile + 1) * kPiece >= q.count)
+  if (w == W - 1 && slot >= 0 && static_cast<int64_t>(q.tile + 1) * kScanPiece >= q.count)
     for (int v = 0; v < V; ++v) p.state[static_cast<int64_t>(slot) * p.width + c + v] = h[v];
 }
 
 template <typename T, int V, bool LINKED>
-__global__ void __launch_bounds__(kThreads) k_scan_backward(ScanArgs p) {
-  __shared__ Shared<V> s;
+__global__ void __launch_bounds__(64 * kBackWaves, 4) k_scan_backward(ScanArgs p) {
+  constexpr int R = kBackTokens, W = kBackWaves;
+  __shared__ Shared<V, W> s;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int block;
-  const int64_t index = next_piece<V, LINKED>(p, s, -1, block);
-  const Piece q = find(p, index);
+  const int64_t index = next_piece<V, W, LINKED>(p, s, -1, block);
+  const Piece q = find<kBackPiece>(p, index);
   const int c = (block * 64 + lane) * V;
   const bool mine = c < p.width;
   if (q.request < 0) {
@@ -335,72 +425,90 @@ __global__ void __launch_bounds__(kThreads) k_scan_backward(ScanArgs p) {
       for (int v = 0; v < V; ++v) p.partial[index * p.width + c + v] = 0.0f;
     return publish_nothing<V, LINKED>(p, index, w, c);
   }
-  const int cc = mine ? c : 0;
+  const uint32_t cc = mine ? c : 0;
   const int slot = slot_of(p, q.request);
   // wave 0 holds the last tokens: it is the first that the gradients reach
   const int back = W - 1 - w;
-  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kPiece + back * R;
-  const int n = max(0, min(R, q.count - q.tile * kPiece - back * R));
-  const int last = q.count > 0 ? (q.count - 1) / kPiece : 0;
-  float less[R][V], ra[R][V], A[V], B[V], g[V], end[V], speed[V];
-  Vec<T, V> gr[R], xr[R], ir[R];
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-  if (n > 0) {
+  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kBackPiece + back * R;
+  const int n = max(0, min(R, q.count - q.tile * kBackPiece - back * R));
+  const int last = q.count > 0 ? (q.count - 1) / kBackPiece : 0;
+  float less[R][V], A[V], B[V], g[V], end[V], speed[V], sum[V];
+  Vec<T, V> ar[R], gr[R], xr[R], ir[R];
+  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, sum[v] = 0.0f;
+  const auto read = [&](auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
     load_speeds<V, LINKED>(p, cc, speed);
-    Vec<T, V> ar[R];
-    for (int t = 0; t < R; ++t) {
-      const int64_t row = t0 + min(t, n - 1);
-      ar[t] = load<T, V>(static_cast<const T*>(p.ga) + row * p.ga_stride + cc);
-      gr[t] = load<T, V>(static_cast<const T*>(p.dy) + row * p.dy_stride + cc);
-      xr[t] = load<T, V>(static_cast<const T*>(p.x) + row * p.x_stride + cc);
-      ir[t] = load<T, V>(static_cast<const T*>(p.gx) + row * p.gx_stride + cc);
+    if (slot == -2)                                 // makes every gradient NaN
+      for (int v = 0; v < V; ++v) speed[v] = __builtin_nanf("");
+    const Rows<T, V> x(p.x, p.x_stride, t0, cc), ga(p.ga, p.ga_stride, t0, cc), gx(p.gx, p.gx_stride, t0, cc);
+    const Rows<T, V> dy(p.dy, p.dy_stride, t0, cc);
+    for (int t = 0; t < R; ++t) {                   // rows behind the last one are read as it
+      const int row = WHOLE ? t : min(t, n - 1);
+      ar[t] = ga.load(row);
+      gr[t] = dy.load(row);
+      xr[t] = x.load(row);
+      ir[t] = gx.load(row);
     }
     for (int t = R - 1; t >= 0; --t)
       for (int v = 0; v < V; ++v) {
-        ra[t][v] = logistic(static_cast<float>(ar[t].v[v]));
-        less[t][v] = one_less_exp(speed[v] * ra[t][v]);
-        const float keep = t < n ? 1.0f - less[t][v] : 1.0f;
-        A[v] *= keep, B[v] = keep * (B[v] + (t < n ? static_cast<float>(gr[t].v[v]) : 0.0f));
+        less[t][v] = one_less_exp2(speed[v] * logistic(ar[t][v]));
+        if (WHOLE || t < n) {
+          const float keep = 1.0f - less[t][v];
+          A[v] *= keep, B[v] = keep * (B[v] + gr[t][v]);
+        }
       }
-  }
+  };
+  if (n == R) read(std::true_type{});
+  else if (n > 0) read(std::false_type{});
   state_of<V>(p, slot, slot >= 0 && q.tile == last, cc, g);
-  hand_on<V, LINKED>(p, s, w, lane, index, -1, last - q.tile, c, A, B, g, end);
-  float sum[V];
-  for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-  if (n > 0) {
-    float before[R][V], h[V];
-    for (int v = 0; v < V; ++v) h[v] = p.saved[(index * W + back) * p.width + cc + v];
-    for (int t = 0; t < R; ++t)
+  hand_on<V, W, LINKED>(p, s, w, lane, index, -1, last - q.tile, c, A, B, g, end);
+  // The gates are worked out again from what was read rather than kept: registers are what limits how many
+  // workgroups a compute unit has under way.
+  const auto gradients = [&](auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    const Rows<T, V> dx(p.y, p.y_stride, t0, cc), dga(p.dga, p.dga_stride, t0, cc), dgx(p.dgx, p.dgx_stride, t0, cc);
+    float before[R][V], h[V], slow[V];
+    for (int v = 0; v < V; ++v) {
+      h[v] = p.saved[(q.first / R + q.request + q.tile * W + back) * p.width + cc + v];
+      slow[v] = speed[v] * kLog2;
+    }
+    for (int t = 0; t < R; ++t) {
+      again(ar[t]), again(ir[t]), again(xr[t]), again(gr[t]);
       for (int v = 0; v < V; ++v) {
         const float a = 1.0f - less[t][v];
         before[t][v] = h[v];
-        h[v] = fmaf(a, h[v], __builtin_amdgcn_sqrtf(less[t][v] * (1.0f + a)) * logistic(static_cast<float>(ir[t].v[v])) *
-                                 static_cast<float>(xr[t].v[v]));
+        h[v] = fmaf(a, h[v], __builtin_amdgcn_sqrtf(less[t][v] * (1.0f + a)) * logistic(ir[t][v]) *
+                                 xr[t][v]);
       }
-    for (int t = R - 1; t >= 0; --t)
-      if (t < n) {
-        float ox[V], oa[V], oi[V];
-        for (int v = 0; v < V; ++v) {
-          const float a = 1.0f - less[t][v], b2 = less[t][v] * (1.0f + a), ri = logistic(static_cast<float>(ir[t].v[v]));
-          const float la = speed[v] * ra[t][v], root = __builtin_amdgcn_sqrtf(b2);
-          const float slope = b2 > 0.0f ? la * __builtin_amdgcn_rcpf(root) : 0.0f;      // log a / b
-          const float gain = ri * static_cast<float>(xr[t].v[v]);
-          const float now = g[v] + static_cast<float>(gr[t].v[v]);
-          const float P = now * a * (before[t][v] * la - a * gain * slope);
-          ox[v] = now * root * ri;
-          oi[v] = now * root * gain * (1.0f - ri);
-          oa[v] = P * (1.0f - ra[t][v]);
-          sum[v] += P;
-          g[v] = a * now;
-          if (slot == -2) ox[v] = oi[v] = oa[v] = __builtin_nanf(""), sum[v] = 0.0f;
-        }
-        if (mine) {
-          store<T, V>(static_cast<T*>(p.y) + (t0 + t) * p.y_stride + c, ox);
-          store<T, V>(static_cast<T*>(p.dga) + (t0 + t) * p.dga_stride + c, oa);
-          store<T, V>(static_cast<T*>(p.dgx) + (t0 + t) * p.dgx_stride + c, oi);
-        }
+      again(ir[t]), again(xr[t]);
+    }
+    for (int t = R - 1; t >= 0; --t) {
+      if (!WHOLE && t >= n) continue;
+      float ox[V], oa[V], oi[V];
+      for (int v = 0; v < V; ++v) {
+        const float a = 1.0f - less[t][v], b2 = less[t][v] * (1.0f + a);
+        const float inv = b2 > 0.0f ? __builtin_amdgcn_rsqf(b2) : 0.0f;       // a state that is kept whole has no slope
+        const float ra = logistic(ar[t][v]), ri = logistic(ir[t][v]);
+        const float gain = ri * xr[t][v];
+        const float now = g[v] + gr[t][v], in = now * (b2 * inv);
+        g[v] = a * now;
+        const float P = g[v] * (slow[v] * ra) * fmaf(-a, gain * inv, before[t][v]);
+        ox[v] = in * ri;
+        oi[v] = in * gain * (1.0f - ri);
+        oa[v] = P * (1.0f - ra);
+        sum[v] += P;
       }
-  }
+      if (mine) {
+        dx.store(t, ox);
+        dga.store(t, oa);
+        dgx.store(t, oi);
+      }
+    }
+  };
+  if (n == R) gradients(std::true_type{});
+  else if (n > 0) gradients(std::false_type{});
+  if (slot == -2)
+    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
   if (w == W - 1 && slot >= 0 && q.tile == 0 && mine)
     for (int v = 0; v < V; ++v)
       p.state[static_cast<int64_t>(slot) * p.width + c + v] = p.resume != nullptr && p.resume[q.request] != 0 ? end[v] : 0.0f;
@@ -452,10 +560,10 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanArgs p) {
                   ir = load<T, V>(static_cast<const T*>(p.gx) + b * p.gx_stride + c);
   float* at = p.state + static_cast<int64_t>(slot) * p.width + c;
   for (int v = 0; v < V; ++v) {
-    const float less = one_less_exp(speed_of(p.decay[c + v], p.rate) * logistic(static_cast<float>(gr.v[v])));
+    const float less = one_less_exp2(speed_of(p.decay[c + v], p.rate) * logistic(gr[v]));
     const float a = 1.0f - less;
-    h[v] = fmaf(a, at[v], __builtin_amdgcn_sqrtf(less * (1.0f + a)) * logistic(static_cast<float>(ir.v[v])) *
-                              static_cast<float>(xr.v[v]));
+    h[v] = fmaf(a, at[v], __builtin_amdgcn_sqrtf(less * (1.0f + a)) * logistic(ir[v]) *
+                              xr[v]);
     at[v] = h[v];
   }
   store<T, V>(static_cast<T*>(p.y) + b * p.y_stride + c, h);
@@ -483,6 +591,7 @@ hipError_t over_pieces(ScanArgs a, hipStream_t s) {
   }
   const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.pieces) * a.blocks));
   const auto go = [&](auto v, auto l) {
+    constexpr int kThreads = 64 * (BACK ? kBackWaves : kScanWaves);
     constexpr int V = decltype(v)::value;
     constexpr bool LINKED = decltype(l)::value;
     if (BACK) k_scan_backward<T, V, LINKED><<<grid, kThreads, 0, s>>>(a);

@@ -19,7 +19,7 @@ from quantized_recurrent_state_packed_amd import stepq as S
 HEADER = Path(__file__).resolve().parents[1] / "include" / "stepq_block.h"
 GOOD = 4096          # an address that is never dereferenced
 RATE = 8.0
-PIECE = 64           # tokens of a workgroup
+PIECE = 128          # tokens of a workgroup of the forward pass, twice those of the backward pass
 
 
 @pytest.fixture(scope="module")
@@ -55,7 +55,7 @@ BAD = [
     (dict(rate=-1.0), 1), (dict(rate=float("nan")), 1), (dict(rate=float("inf")), 1), (dict(batch=-1), 1), (dict(tokens=-1), 1),
     (dict(cu=None), 1), (dict(cu=GOOD + 2), 1), (dict(x=None), 1), (dict(x=GOOD + 1), 1), (dict(xs=99), 1), (dict(gas=99), 1),
     (dict(gxs=-100), 1), (dict(ga=None), 1), (dict(gx=None), 1), (dict(decay=None), 1), (dict(decay=GOOD + 2), 1),
-    (dict(dtype=0, x=GOOD + 2), 1), (dict(xs=2 ** 41), 1), (dict(slots=None), 1), (dict(slots=GOOD + 1), 1), (dict(state=None), 1),
+    (dict(dtype=0, x=GOOD + 2), 1), (dict(xs=2 ** 24 + 1), 1), (dict(slots=None), 1), (dict(slots=GOOD + 1), 1), (dict(state=None), 1),
     (dict(state=GOOD + 2), 1), (dict(num_slots=0), 1), (dict(width=2 ** 20 + 1), 2),
     (dict(tokens=2 ** 31), 2), (dict(batch=2 ** 23), 2),
 ]
@@ -63,7 +63,7 @@ BAD = [
 
 @pytest.mark.parametrize("bad,status", BAD + [
     (dict(y=None), 1), (dict(y=GOOD + 1), 1), (dict(ys=99), 1), (dict(saved=GOOD + 8, saved_bytes=1 << 30), 1),
-    (dict(saved=GOOD, saved_bytes=3 * 8 * 100 * 4 - 1), 1),
+    (dict(saved=GOOD, saved_bytes=10 * 400 - 1), 1),
 ])
 def test_forward_arguments_that_are_refused(lib, bad, status):
     assert forward_status(lib, **bad) == status
@@ -78,7 +78,7 @@ def backward_status(lib, d=None, batch=2, tokens=70, cu=GOOD, x=GOOD, xs=100, ga
 
 
 @pytest.mark.parametrize("bad,status", BAD + [
-    (dict(saved=None), 1), (dict(saved=GOOD + 4), 1), (dict(saved_bytes=3 * 8 * 100 * 4 - 1), 1), (dict(dy=None), 1),
+    (dict(saved=None), 1), (dict(saved=GOOD + 4), 1), (dict(saved_bytes=10 * 400 - 1), 1), (dict(dy=None), 1),
     (dict(dys=99), 1), (dict(dx=None), 1), (dict(dga=GOOD + 1), 1), (dict(dgxs=50), 1), (dict(ddecay=None), 1),
     (dict(ddecay=GOOD + 2), 1), (dict(ws=None), 1), (dict(ws=GOOD + 8), 1), (dict(nbytes=0), 1),
 ])
@@ -103,7 +103,7 @@ def test_empty_batches_and_sizes(lib):
     size, saved = lib.stepq_scan_workspace_bytes, lib.stepq_scan_saved_bytes
     for f in (size, saved):
         assert f(None, 1, 1) == 0 and f(desc(width=0), 1, 1) == 0 and f(desc(), -1, 1) == 0 and f(desc(), 1, 2 ** 31) == 0
-    assert saved(desc(), 2, 70) == 3 * 8 * 100 * 4
+    assert saved(desc(), 2, 70) == (70 // 8 + 2) * 400
     sizes = [size(desc(), b, t) for t in (0, 1, 64, 65, 1000, 100000) for b in (0, 1, 3, 50)]
     assert sizes[:4] == [max(0, 16 * -(-b * 400 // 16)) for b in (0, 1, 3, 50)]
     for t in range(5):      # more requests or tokens never need less
@@ -291,8 +291,8 @@ class Case:
             assert np.all(np.abs(self.host(self.ddecay) - total) <= room + 2.0 ** -23 * np.abs(total))
 
 
-LENGTHS = {"one": [1], "short": [37], "piece": [PIECE], "piece+1": [PIECE + 1], "ragged": [3, 0, 1, 130, 64, 65, 7, 0],
-           "long": [1500], "many": [1, 2, 0, 9, 8, 7] * 23, "two long": [700, 513]}
+LENGTHS = {"one": [1], "short": [37], "piece": [PIECE], "piece+1": [PIECE + 1], "half": [PIECE // 2],
+           "half+1": [PIECE // 2 + 1], "ragged": [3, 0, 1, 130, 64, 65, 7, 0], "long": [1500], "many": [1, 2, 0, 9, 8, 7] * 23, "two long": [700, 513]}
 
 
 @pytest.mark.gpu
@@ -301,6 +301,14 @@ LENGTHS = {"one": [1], "short": [37], "piece": [PIECE], "piece+1": [PIECE + 1], 
 @pytest.mark.parametrize("width", [1, 64, 130, 203])
 def test_prompts_and_their_gradients(lengths, width, dtype):
     Case(LENGTHS[lengths], width, dtype, seed=width).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[64 * PIECE + 1], [10, 70 * PIECE, 5], [20000, 0, 9000]])
+def test_prompts_of_several_runs(lengths, dtype):
+    """Requests longer than the 64 pieces over which states are handed on in one go."""
+    Case(lengths, 6, dtype).check()
 
 
 @pytest.mark.gpu
@@ -498,28 +506,35 @@ def test_same_bits_again_on_another_stream_and_in_a_graph():
 def test_rows_past_32_bits():
     """Tokens so far apart that the last ones lie 2^32 bytes and more behind the first."""
     import torch
-    rows, width, stride = 70, 64, (1 << 31) // 64 + 64
+    rows, width, stride = 140, 64, 1 << 24
     flat = torch.zeros((rows - 1) * stride + width, dtype=torch.bfloat16, device="cuda")
     assert flat.numel() * 2 > 1 << 32
     rec = RC.GatedRecurrence(width, torch.bfloat16, RATE)
     g = torch.Generator(device="cuda").manual_seed(1)
-    x, ga, gx = (torch.randn(rows, width, generator=g, device="cuda").bfloat16() for _ in range(3))
+    x, ga, gx, dy = (torch.randn(rows, width, generator=g, device="cuda").bfloat16() for _ in range(4))
     far = flat.as_strided((rows, width), (stride, 1))
     far.copy_(x)
     cu = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
     decay, y, z = torch.full((width,), -3.0, device="cuda"), torch.empty_like(x), torch.empty_like(x)
-    rec.prefill(cu, x, ga, gx, decay, None, None, y)
+    saved, dd = rec.saved(1, rows), torch.empty(width, device="cuda")
+    rec.prefill(cu, x, ga, gx, decay, None, None, y, saved=saved)
     rec.prefill(cu, far, ga, gx, decay, None, None, z)
+    dx, da, dg, da2, dg2 = (torch.empty_like(x) for _ in range(5))
+    rec.backward(cu, x, ga, gx, decay, saved, dy, dx, da, dg, dd)
+    far.copy_(dy)
+    rec.backward(cu, x, ga, gx, decay, saved, far, torch.empty_like(x), da2, dg2, dd)
+    torch.cuda.synchronize()
+    assert torch.equal(y, z) and torch.equal(da, da2) and torch.equal(dg, dg2)
     rec.prefill(cu, x, ga, gx, decay, None, None, far)
     torch.cuda.synchronize()
-    assert torch.equal(y, z) and torch.equal(far, y)
+    assert torch.equal(far, y)
 
 
 @pytest.mark.gpu
 def test_refusals_that_need_a_device(monkeypatch):
     import torch
     from quantized_recurrent_state_packed_amd import linear as LN
-    c = Case([5, 80], 8, "f32")
+    c = Case([5, 2 * PIECE], 8, "f32")
     ws, saved = c.buffers()
     calls = (lambda: c.forward(saved, workspace=ws), lambda: c.backward(saved, workspace=ws),
              lambda: c.rec.step(c.ids, c.x[:2], c.ga[:2], c.gx[:2], c.decay, c.state, c.y[:2]))
