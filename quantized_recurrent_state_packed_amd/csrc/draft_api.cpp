@@ -51,16 +51,16 @@ stepq_status stepq_verify_drafts(int32_t batch, int32_t drafts, int32_t vocab, c
   a.draft_tokens = draft_tokens; a.num_drafts = num_drafts; a.temperature = temperature; a.uniforms = uniforms;
   a.accepted = accepted; a.tokens = tokens;
   a.parts = reinterpret_cast<stepq::VerifyPart*>(base);
+  a.plans = reinterpret_cast<stepq::VerifyPlan*>(base + w.plans);
   a.sums = reinterpret_cast<double*>(base + w.sums);
-  a.arrived = reinterpret_cast<uint32_t*>(base + w.arrived);
   a.batch = batch; a.drafts = drafts; a.vocab = vocab;
   a.num_parts = stepq::verify_parts(static_cast<int64_t>(batch) * (2 * drafts + 1), vocab);
   a.tiles = stepq::verify_tiles(vocab);
   a.part_tiles = (a.tiles + a.num_parts - 1) / a.num_parts;
-  // a request's tiles go to workgroups of 4 waves, 2048 waves in all or one tile each
-  int64_t groups = (512 + batch - 1) / batch;
+  // a request's tiles go to workgroups of 4 waves, 1024 of them in all or a tile a wave
+  int64_t groups = (1024 + batch - 1) / batch;
   if (groups > (a.tiles + 3) / 4) groups = (a.tiles + 3) / 4;
-  a.pick_groups = static_cast<int32_t>(groups);
+  a.groups = static_cast<int32_t>(groups);
   return from_hip(stepq::launch_verify(a, dtype, static_cast<hipStream_t>(stream)));
 }
 

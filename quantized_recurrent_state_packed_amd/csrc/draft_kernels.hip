@@ -1,9 +1,8 @@
 // gfx950 kernels of the verification of drafted tokens.
 //
-// k_verify_scan reads every row once and leaves the sums of its softmax, k_verify_pick decides
-// how many drafts a request keeps, sums what the next token is drawn from over tiles of the one
-// row that matters, and its last workgroup finds the token in the tile where the sum crosses the
-// random number.
+// k_verify_scan reads every row once and leaves the sums of its softmax, k_verify_sums decides how many
+// drafts a request keeps and sums what the next token is drawn from over tiles of the one row
+// that matters, k_verify_choose finds the token in the tile where the sum crosses the random number.
 //
 // A drawn token is a whole number that a difference in the last places of a sum can change:
 // with sums good to d, one in 1 / (2 d tokens) draws near a border goes the other way, 3 % at
@@ -48,23 +47,21 @@ struct Tile {
   __device__ __forceinline__ float value(int e) const { return static_cast<float>(raw[e / V].v[e % V]); }
 };
 
-// 2^t good to 2e-15 of itself: the series of 2^f up to f^11, |f| <= 1/2.  Below 2^-1100, and for a
-// NaN, 0.
+// 2^t good to 3e-14 of itself: the polynomial that equals 2^f at the ten Chebyshev points of |f| <= 1/2.
+// Below 2^-1100, and for a NaN, 0.
 __device__ __forceinline__ double power(double t) {
   t = fmax(t, -1100.0);
   const double n = rint(t), f = t - n;
-  double s = 4.4455382718708114976e-10;                        // log(2)^k / k!
-  s = fma(s, f, 7.0549116208011233299e-09);
-  s = fma(s, f, 1.0178086009239699728e-07);
-  s = fma(s, f, 1.3215486790144309488e-06);
-  s = fma(s, f, 1.5252733804059840280e-05);
-  s = fma(s, f, 1.5403530393381609954e-04);
-  s = fma(s, f, 1.3333558146428443423e-03);
-  s = fma(s, f, 9.6181291076284771619e-03);
-  s = fma(s, f, 5.5504108664821579953e-02);
-  s = fma(s, f, 2.4022650695910071233e-01);
-  s = fma(s, f, 6.9314718055994530942e-01);
-  s = fma(s, f, 1.0);
+  double s = 1.0219919843734715e-07;
+  s = fma(s, f, 1.3259776859619875e-06);
+  s = fma(s, f, 1.525259924712863e-05);
+  s = fma(s, f, 1.5403433057773475e-04);
+  s = fma(s, f, 1.33335583295702e-03);
+  s = fma(s, f, 9.618129195121405e-03);
+  s = fma(s, f, 5.550410866380432e-02);
+  s = fma(s, f, 2.4022650695633263e-01);
+  s = fma(s, f, 6.931471805599624e-01);
+  s = fma(s, f, 1.0000000000000144);
   return __builtin_amdgcn_ldexp(s, static_cast<int>(n));
 }
 
@@ -104,7 +101,6 @@ __global__ void __launch_bounds__(kThreads) k_verify_scan(VerifyArgs p) {
   if (unit >= static_cast<int64_t>(p.batch) * rows * p.num_parts) return;
   const int part = static_cast<int>(unit % p.num_parts), r = static_cast<int>(unit / p.num_parts % rows);
   const int b = static_cast<int>(unit / p.num_parts / rows);
-  if (part == 0 && r == 0 && lane == 0) p.arrived[b] = 0;
   const Request q = request_of(p, b);
   const bool drafted = r > p.drafts;
   const int place = drafted ? r - p.drafts - 1 : r;
@@ -163,199 +159,218 @@ __global__ void __launch_bounds__(kThreads) k_verify_scan(VerifyArgs p) {
   if (lane == 0) p.parts[unit] = {sum, m, at};
 }
 
-// A row's softmax: probabilities are weight(x, m, c) * scale.
-struct Row {
-  float m;
-  int32_t at;
-  double scale;      // 0: everything is banned
-};
-
-// The parts of a row, one a lane, joined; the same in every lane.
-__device__ __forceinline__ Row join(const VerifyArgs& p, int64_t row, const Request& q, int lane) {
-  VerifyPart v = {0.0, -kInf, -1};
-  if (lane < p.num_parts) v = p.parts[row * p.num_parts + lane];
-  Row r;
-  r.m = v.m, r.at = v.at;
-  for (int s = 1; s < 64; s <<= 1) {
-    const float om = __shfl_xor(r.m, s);
-    const int32_t oa = __shfl_xor(r.at, s);
-    if (om > r.m || (om == r.m && static_cast<uint32_t>(oa) < static_cast<uint32_t>(r.at))) r.m = om, r.at = oa;
-  }
-  double sum = v.m == -kInf ? 0.0 : v.sum * (q.greedy ? 1.0 : weight(v.m, r.m, q.c));
-  for (int s = 1; s < 64; s <<= 1) sum += across(sum, s);
-  r.scale = sum > 0.0 ? 1.0 / sum : 0.0;
-  return r;
-}
-
-// What the next token is drawn from.
-struct Source {
-  Row p, q;
-  bool minus;         // p - q
-  int32_t sharp;      // q is 1 at this token and nowhere else; -1: it is not
-};
-
-template <typename T>
-__device__ __forceinline__ void shares(const Source& s, const T* x, const T* z, const Request& q, int tile, int vocab, int lane,
-                                       double (&rest)[kPer], double (&whole)[kPer]) {
-  Tile<T> a, d;
-  a.load(x, tile * kVerifyTile, vocab, lane);
-  const bool two = s.minus && s.sharp < 0;
-  if (two) d.load(z, tile * kVerifyTile, vocab, lane);
-  for (int e = 0; e < kPer; ++e) {
-    whole[e] = s.p.scale > 0.0 ? weight(a.value(e), s.p.m, q.c) * s.p.scale : 0.0;
-    rest[e] = whole[e];
-    if (two && s.q.scale > 0.0) rest[e] = fmax(whole[e] - weight(d.value(e), s.q.m, q.c) * s.q.scale, 0.0);
-    if (s.minus && s.sharp == tile * kVerifyTile + Tile<T>::place(e, lane)) rest[e] = 0.0;
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_verify_pick(VerifyArgs p) {
-  __shared__ Row joined[2 * kMostDrafts + 1];
-  __shared__ double scan[kThreads];
-  __shared__ int found[4];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.x / p.pick_groups, g = blockIdx.x % p.pick_groups;
-  const Request q = request_of(p, b);
-  const int64_t row0 = static_cast<int64_t>(b) * (2 * p.drafts + 1);
-  const bool sharp = q.greedy || p.draft_logits == nullptr;
-  for (int r = w; r <= 2 * p.drafts; r += kWaves) {
-    const int place = r > p.drafts ? r - p.drafts - 1 : r;
-    if (r > p.drafts ? place >= q.count || sharp : place > q.count) continue;
-    const Row j = join(p, row0 + r, q, lane);
-    if (lane == 0) joined[r] = j;
+// Joins the parts of a request's rows into LDS: `span` lanes (a power of two that holds num_parts) take a row.
+__device__ __forceinline__ void join_rows(const VerifyArgs& p, int b, const Request& q, bool sharp, VerifyRow* joined) {
+  const int span = p.num_parts <= 1 ? 1 : 1 << (32 - __builtin_clz(p.num_parts - 1));
+  const int rows = 2 * p.drafts + 1, part = threadIdx.x & (span - 1);
+  const int64_t row0 = static_cast<int64_t>(b) * rows;
+  for (int first = 0; first < rows; first += kThreads / span) {
+    const int r = first + static_cast<int>(threadIdx.x) / span, place = r > p.drafts ? r - p.drafts - 1 : r;
+    const bool read = r < rows && (r > p.drafts ? place < q.count && !sharp : place <= q.count);
+    VerifyPart v = {0.0, -kInf, -1};
+    if (read && part < p.num_parts) v = p.parts[(row0 + r) * p.num_parts + part];
+    float m = v.m;
+    int32_t at = v.at;
+    for (int s = 1; s < span; s <<= 1) {
+      const float om = __shfl_xor(m, s);
+      const int32_t oa = __shfl_xor(at, s);
+      if (om > m || (om == m && static_cast<uint32_t>(oa) < static_cast<uint32_t>(at))) m = om, at = oa;
+    }
+    double sum = v.m == -kInf || q.greedy ? 0.0 : v.sum * weight(v.m, m, q.c);
+    for (int s = 1; s < span; s <<= 1) sum += across(sum, s);
+    if (read && part == 0) joined[r] = {sum > 0.0 ? 1.0 / sum : 0.0, m, at};
   }
   __syncthreads();
-  const T* target = static_cast<const T*>(p.logits) + static_cast<int64_t>(b) * (p.drafts + 1) * p.logits_stride;
-  const T* draft = static_cast<const T*>(p.draft_logits) + static_cast<int64_t>(b) * p.drafts * p.draft_stride;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* target_row(const VerifyArgs& p, int b, int place) {
+  return static_cast<const T*>(p.logits) + (static_cast<int64_t>(b) * (p.drafts + 1) + place) * p.logits_stride;
+}
+template <typename T>
+__device__ __forceinline__ const T* draft_row(const VerifyArgs& p, int b, int place) {
+  return static_cast<const T*>(p.draft_logits) + (static_cast<int64_t>(b) * p.drafts + place) * p.draft_stride;
+}
+
+// A tile of what the next token is drawn from, p - q, and of p alone.
+template <typename T>
+__device__ __forceinline__ void shares(const VerifyArgs& p, int b, const VerifyPlan& s, double c, int tile, int lane,
+                                       double (&rest)[kPer], double (&whole)[kPer]) {
+  const bool two = s.minus && s.sharp < 0 && s.q.scale > 0.0;
+  Tile<T> a, d;
+  a.load(target_row<T>(p, b, s.n), tile * kVerifyTile, p.vocab, lane);
+  if (two) d.load(draft_row<T>(p, b, s.n), tile * kVerifyTile, p.vocab, lane);
+  for (int e = 0; e < kPer; ++e) {
+    whole[e] = s.p.scale > 0.0 ? weight(a.value(e), s.p.m, c) * s.p.scale : 0.0;
+    rest[e] = whole[e];
+  }
+  if (two)
+    for (int e = 0; e < kPer; ++e) rest[e] = fmax(whole[e] - weight(d.value(e), s.q.m, c) * s.q.scale, 0.0);
+  if (s.minus && s.sharp >= 0)
+    for (int e = 0; e < kPer; ++e)
+      if (s.sharp == tile * kVerifyTile + Tile<T>::place(e, lane)) rest[e] = 0.0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs p) {
+  __shared__ VerifyRow joined[2 * kMostDrafts + 1];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int b = blockIdx.x / p.groups, g = blockIdx.x % p.groups;
+  const Request q = request_of(p, b);
+  const bool sharp = q.greedy || p.draft_logits == nullptr;
   // lane k looks at draft k
-  bool good = false, known = false;
   int32_t token = -1;
+  float xt = 0.0f, zt = 0.0f, u = 0.0f;
+  bool known = false;
   if (lane < q.count) {
     token = p.draft_tokens[b * static_cast<int64_t>(p.drafts) + lane];
     known = token >= 0 && token < p.vocab;
-    if (known) {
-      const Row t = joined[lane];
-      if (q.greedy) {
-        good = t.at == token;
-      } else {
-        const double pd = t.scale > 0.0 ? weight(static_cast<float>(target[lane * p.logits_stride + token]), t.m, q.c) * t.scale : 0.0;
-        double qd = 1.0;
-        if (!sharp) {
-          const Row d = joined[p.drafts + 1 + lane];
-          qd = d.scale > 0.0 ? weight(static_cast<float>(draft[lane * p.draft_stride + token]), d.m, q.c) * d.scale : 0.0;
-        }
-        good = static_cast<double>(p.uniforms[static_cast<int64_t>(b) * (p.drafts + 1) + lane]) * qd < pd;
+    u = p.uniforms[static_cast<int64_t>(b) * (p.drafts + 1) + lane];
+    if (known && !q.greedy) {
+      xt = static_cast<float>(target_row<T>(p, b, lane)[token]);
+      if (!sharp) zt = static_cast<float>(draft_row<T>(p, b, lane)[token]);
+    }
+  }
+  join_rows(p, b, q, sharp, joined);
+  bool good = false;
+  if (known) {
+    const VerifyRow t = joined[lane];
+    if (q.greedy) {
+      good = t.at == token;
+    } else {
+      const double pd = t.scale > 0.0 ? weight(xt, t.m, q.c) * t.scale : 0.0;
+      double qd = 1.0;
+      if (!sharp) {
+        const VerifyRow d = joined[p.drafts + 1 + lane];
+        qd = d.scale > 0.0 ? weight(zt, d.m, q.c) * d.scale : 0.0;
       }
+      good = static_cast<double>(u) * qd < pd;
     }
   }
   const int n = __builtin_ctzll(~__ballot(good));          // at most 63 lanes are good
-  const bool rejected = n < q.count && (__ballot(known) >> n & 1);
-  int32_t* out = p.tokens + static_cast<int64_t>(b) * (p.drafts + 1);
+  VerifyPlan s;
+  s.n = n;
+  s.p = joined[n];
+  s.minus = n < q.count && (__ballot(known) >> n & 1);     // a draft was rejected
+  s.sharp = s.minus && sharp ? __shfl(token, n) : -1;
+  s.q = s.minus && !sharp ? joined[p.drafts + 1 + n] : VerifyRow{0.0, 0.0f, -1};
+  s.pad = 0;
   if (g == 0 && w == 0) {
+    int32_t* out = p.tokens + static_cast<int64_t>(b) * (p.drafts + 1);
     if (lane < n) out[lane] = token;
     if (lane > n && lane <= p.drafts) out[lane] = -1;
-    if (lane == 0) p.accepted[b] = n;
-    if (q.greedy && lane == 0) out[n] = joined[n].at;
+    if (lane == 0) {
+      p.accepted[b] = n;
+      p.plans[b] = s;
+      if (q.greedy) out[n] = s.p.at;
+    }
   }
   if (q.greedy) return;
-  Source s;
-  s.p = joined[n];
-  s.minus = rejected;
-  s.sharp = sharp && rejected ? __shfl(token, n) : -1;
-  if (s.minus && !sharp) s.q = joined[p.drafts + 1 + n];
-  const T *x = target + n * p.logits_stride, *z = s.minus && !sharp ? draft + n * p.draft_stride : nullptr;
   double* sums = p.sums + static_cast<int64_t>(b) * p.tiles * 2;
   double rest[kPer], whole[kPer];
-  for (int tile = g * kWaves + w; tile < p.tiles; tile += p.pick_groups * kWaves) {
-    shares(s, x, z, q, tile, p.vocab, lane, rest, whole);
+  for (int tile = g * kWaves + w; tile < p.tiles; tile += p.groups * kWaves) {
+    shares<T>(p, b, s, q.c, tile, lane, rest, whole);
     double a = 0.0, c = 0.0;
     for (int e = 0; e < kPer; ++e) a += rest[e], c += whole[e];
-    for (int k = 1; k < 64; k <<= 1) a += across(a, k), c += across(c, k);
-    if (lane == 0) sums[2 * tile] = a, sums[2 * tile + 1] = c;
+    // even lanes go on with one sum, odd lanes with the other
+    double mine = lane & 1 ? c : a;
+    mine += across(lane & 1 ? a : c, 1);
+    for (int k = 2; k < 64; k <<= 1) mine += across(mine, k);
+    if (lane < 2) sums[2 * tile + lane] = mine;
   }
-  // the request's last workgroup goes on; nothing waits for it
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) found[0] = atomicAdd(p.arrived + b, 1u) == static_cast<uint32_t>(p.pick_groups) - 1;
-  __syncthreads();
-  if (!found[0]) return;
-  __threadfence();
-  // every thread takes a run of tiles; which sum counts depends on whether anything is left of p - q
-  const int run = (p.tiles + kThreads - 1) / kThreads, from = min(static_cast<int>(threadIdx.x) * run, p.tiles);
-  const int to = min(from + run, p.tiles);
-  int which = 0;
-  double total = 0.0;
-  for (; which < 2; ++which) {
-    double mine = 0.0;
-    for (int tile = from; tile < to; ++tile) mine += sums[2 * tile + which];
-    __syncthreads();
-    scan[threadIdx.x] = mine;
-    __syncthreads();
-    total = 0.0;
-    for (int k = 0; k < kThreads; ++k) {
-      if (k == static_cast<int>(threadIdx.x)) mine = total;      // what lies before
-      total += scan[k];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_verify_choose(VerifyArgs p) {
+  __shared__ double waves[2][kWaves];
+  __shared__ double start;
+  __shared__ int found[2];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.x;
+  const Request q = request_of(p, b);
+  if (q.greedy) return;
+  const VerifyPlan s = p.plans[b];
+  const float u = p.uniforms[static_cast<int64_t>(b) * (p.drafts + 1) + p.drafts];
+  int32_t* out = p.tokens + static_cast<int64_t>(b) * (p.drafts + 1) + s.n;
+  const double* sums = p.sums + static_cast<int64_t>(b) * p.tiles * 2;
+  if (threadIdx.x == 0) found[0] = p.tiles, found[1] = -1;
+  // every thread takes a run of tiles
+  const int run = (p.tiles + kThreads - 1) / kThreads;
+  const int from = min(static_cast<int>(threadIdx.x) * run, p.tiles), to = min(from + run, p.tiles);
+  double mine[2] = {0.0, 0.0}, upto[2];
+  for (int tile = from; tile < to; ++tile)
+    for (int k = 0; k < 2; ++k) mine[k] += sums[2 * tile + k];
+  for (int k = 0; k < 2; ++k) {
+    upto[k] = mine[k];
+    for (int d = 1; d < 64; d <<= 1) {
+      const double o = __longlong_as_double(__shfl_up(__double_as_longlong(upto[k]), d));
+      if (lane >= d) upto[k] += o;
     }
-    __syncthreads();
-    scan[threadIdx.x] = mine;
-    if (total > 0.0) break;
+    if (lane == 63) waves[k][w] = upto[k];
   }
-  if (!(total > 0.0)) {
-    if (threadIdx.x == 0) out[n] = -1;
+  __syncthreads();
+  double total[2], before[2];
+  for (int k = 0; k < 2; ++k) {
+    total[k] = 0.0;
+    for (int v = 0; v < kWaves; ++v) {
+      if (v == w) before[k] = total[k] + (upto[k] - mine[k]);
+      total[k] += waves[k][v];
+    }
+  }
+  const int which = total[0] > 0.0 ? 0 : 1;         // nothing is left of p - q: p
+  if (!(total[which] > 0.0)) {
+    if (threadIdx.x == 0) *out = -1;
     return;
   }
-  const double goal = static_cast<double>(p.uniforms[static_cast<int64_t>(b) * (p.drafts + 1) + p.drafts]) * total;
+  const double goal = static_cast<double>(u) * total[which];
   // the first tile whose sum crosses the goal, or the last that has any
-  if (threadIdx.x == 0) found[1] = p.tiles, found[2] = -1;
-  __syncthreads();
-  double before = scan[threadIdx.x];
+  double at = before[which];
   for (int tile = from; tile < to; ++tile) {
     const double add = sums[2 * tile + which];
     if (add > 0.0) {
-      atomicMax(&found[2], tile);
-      if (before + add > goal) {
-        atomicMin(&found[1], tile);
+      atomicMax(&found[1], tile);
+      if (at + add > goal) {
+        atomicMin(&found[0], tile);
         break;
       }
     }
-    before += add;
+    at += add;
   }
   __syncthreads();
-  const int tile = found[1] < p.tiles ? found[1] : found[2];
+  const int tile = found[0] < p.tiles ? found[0] : found[1];
   if (tile >= from && tile < to) {
-    double at = scan[threadIdx.x];
+    at = before[which];
     for (int k = from; k < tile; ++k) at += sums[2 * k + which];
-    scan[0] = at;             // one thread owns the tile, and the others are past their reads
+    start = at;
   }
   __syncthreads();
   if (w != 0) return;
-  double left = scan[0];
-  shares(s, x, z, q, tile, p.vocab, lane, rest, whole);
+  double left = start;
+  double rest[kPer], whole[kPer];
+  shares<T>(p, b, s, q.c, tile, lane, rest, whole);
   int32_t best = 0x7fffffff, last = -1;
   constexpr int V = kVec<T>;
   for (int e = 0; e < kPer; e += V) {
-    double mine = 0.0;
-    for (int i = 0; i < V; ++i) mine += which == 0 ? rest[e + i] : whole[e + i];
-    double upto = mine;                                       // of the lanes up to this one
+    double own = 0.0;
+    for (int i = 0; i < V; ++i) own += which == 0 ? rest[e + i] : whole[e + i];
+    double all = own;                                         // of the lanes up to this one
     for (int k = 1; k < 64; k <<= 1) {
-      const double o = __longlong_as_double(__shfl_up(__double_as_longlong(upto), k));
-      if (lane >= k) upto += o;
+      const double o = __longlong_as_double(__shfl_up(__double_as_longlong(all), k));
+      if (lane >= k) all += o;
     }
-    double at = left + (upto - mine);
+    double x = left + (all - own);
     for (int i = 0; i < V; ++i) {
       const double v = which == 0 ? rest[e + i] : whole[e + i];
-      at += v;
-      const int32_t token_at = tile * kVerifyTile + Tile<T>::place(e + i, lane);
+      x += v;
+      const int32_t token = tile * kVerifyTile + Tile<T>::place(e + i, lane);
       if (v > 0.0) {
-        last = max(last, token_at);
-        if (at > goal) best = min(best, token_at);
+        last = max(last, token);
+        if (x > goal) best = min(best, token);
       }
     }
-    left += __longlong_as_double(__shfl(__double_as_longlong(upto), 63));
+    left += __longlong_as_double(__shfl(__double_as_longlong(all), 63));
   }
   for (int k = 1; k < 64; k <<= 1) best = min(best, __shfl_xor(best, k)), last = max(last, __shfl_xor(last, k));
-  if (lane == 0) out[n] = best != 0x7fffffff ? best : last;
+  if (lane == 0) *out = best != 0x7fffffff ? best : last;
 }
 
 template <typename T>
@@ -363,7 +378,9 @@ void launch(const VerifyArgs& a, hipStream_t s) {
   const int64_t units = static_cast<int64_t>(a.batch) * (2 * a.drafts + 1) * a.num_parts;
   k_verify_scan<T><<<dim3(static_cast<uint32_t>((units + kWaves - 1) / kWaves)), kThreads, 0, s>>>(a);
   if (hipPeekAtLastError() != hipSuccess) return;
-  k_verify_pick<T><<<dim3(static_cast<uint32_t>(a.batch) * a.pick_groups), kThreads, 0, s>>>(a);
+  k_verify_sums<T><<<dim3(static_cast<uint32_t>(a.batch) * a.groups), kThreads, 0, s>>>(a);
+  if (hipPeekAtLastError() != hipSuccess) return;
+  k_verify_choose<T><<<dim3(static_cast<uint32_t>(a.batch)), kThreads, 0, s>>>(a);
 }
 
 }  // namespace

@@ -118,7 +118,7 @@ def status(lib, batch=2, drafts=3, vocab=100, logits=GOOD, dtype=1, stride=100, 
     (dict(logits=GOOD + 1), 1), (dict(stride=99), 1), (dict(stride=2 ** 39), 1), (dict(zs=99), 1), (dict(zs=2 ** 39), 1),
     (dict(z=GOOD + 1), 1), (dict(d=None), 1), (dict(d=GOOD + 2), 1), (dict(count=GOOD + 1), 1), (dict(temp=GOOD + 2), 1),
     (dict(u=None), 1), (dict(u=GOOD + 1), 1), (dict(accepted=None), 1), (dict(tokens=None), 1), (dict(tokens=GOOD + 2), 1),
-    (dict(ws=None), 1), (dict(ws=GOOD + 8), 1), (dict(nbytes=0), 1), (dict(nbytes=14 * 16 + 2 * 16 + 15), 1),
+    (dict(ws=None), 1), (dict(ws=GOOD + 8), 1), (dict(nbytes=0), 1), (dict(nbytes=14 * 16 + 2 * 48 + 2 * 16 - 1), 1),
     (dict(drafts=64), 2), (dict(vocab=2 ** 31 - 1024), 2), (dict(batch=2 ** 20), 2),
 ])
 def test_arguments_that_are_refused(lib, bad, want):
@@ -129,8 +129,8 @@ def test_empty_batches_and_workspace_sizes(lib):
     assert status(lib, batch=0, logits=None, ws=None) == S.STEPQ_OK
     size = lib.stepq_verify_workspace_bytes
     assert size(0, 4, 100) == 0 and size(1, 64, 100) == 0 and size(1, 4, 0) == 0 and size(2 ** 22, 4, 100) == 0
-    assert size(2, 3, 100) == 14 * 16 + 2 * 16 + 16
-    assert size(1, 0, 1025) == 2 * 16 + 2 * 16 + 16
+    assert size(2, 3, 100) == 14 * 16 + 2 * 48 + 2 * 16
+    assert size(1, 0, 1025) == 2 * 16 + 48 + 2 * 16
 
 
 def test_binding_refuses_bad_tensors_before_the_library(lib):
