@@ -49,24 +49,26 @@ struct Tile {
 
 // 2^t good to 3e-14 of itself: the polynomial that equals 2^f at the ten Chebyshev points of |f| <= 1/2.
 // Below 2^-1100, and for a NaN, 0.
-__device__ __forceinline__ double power(double t) {
-  t = fmax(t, -1100.0);
-  const double n = rint(t), f = t - n;
-  double s = 1.0219919843734715e-07;
-  s = fma(s, f, 1.3259776859619875e-06);
-  s = fma(s, f, 1.525259924712863e-05);
-  s = fma(s, f, 1.5403433057773475e-04);
-  s = fma(s, f, 1.33335583295702e-03);
-  s = fma(s, f, 9.618129195121405e-03);
-  s = fma(s, f, 5.550410866380432e-02);
-  s = fma(s, f, 2.4022650695633263e-01);
-  s = fma(s, f, 6.931471805599624e-01);
-  s = fma(s, f, 1.0000000000000144);
-  return __builtin_amdgcn_ldexp(s, static_cast<int>(n));
-}
+struct Power {
+  double c[10] = {1.0000000000000144,    6.931471805599624e-01,  2.4022650695633263e-01, 5.550410866380432e-02,
+                  9.618129195121405e-03, 1.33335583295702e-03,   1.5403433057773475e-04, 1.525259924712863e-05,
+                  1.3259776859619875e-06, 1.0219919843734715e-07};
+  // In scalar registers, which a multiplication takes as its addend; as constants the compiler would copy
+  // five of them for every power.
+  __device__ __forceinline__ Power() {
+    for (int k = 0; k < 10; ++k) asm("" : "+s"(c[k]));
+  }
+  __device__ __forceinline__ double operator()(double t) const {
+    t = fmax(t, -1100.0);
+    const double n = rint(t), f = t - n;
+    double s = fma(c[9], f, c[8]);
+    for (int k = 7; k >= 0; --k) s = fma(s, f, c[k]);
+    return __builtin_amdgcn_ldexp(s, static_cast<int>(n));
+  }
+};
 
 // exp((x - m) / temperature) with c = log2(e) / temperature; an infinity shares with infinities alone.
-__device__ __forceinline__ double weight(float x, float m, double c) {
+__device__ __forceinline__ double weight(const Power& power, float x, float m, double c) {
   if (m == kInf) return x == kInf ? 1.0 : 0.0;
   return power((static_cast<double>(x) - static_cast<double>(m)) * c);
 }
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_scan(VerifyArgs p) {
   const int part = static_cast<int>(unit % p.num_parts), r = static_cast<int>(unit / p.num_parts % rows);
   const int b = static_cast<int>(unit / p.num_parts / rows);
   const Request q = request_of(p, b);
+  const Power power;
   const bool drafted = r > p.drafts;
   const int place = drafted ? r - p.drafts - 1 : r;
   if (drafted ? place >= q.count || q.greedy || p.draft_logits == nullptr : place > q.count) return;
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_scan(VerifyArgs p) {
         }
       }
       if (__ballot(m == kInf)) {
-        for (int e = 0; e < kPer; ++e) sum += m > -kInf ? weight(now.value(e), m, q.c) : 0.0;
+        for (int e = 0; e < kPer; ++e) sum += m > -kInf ? weight(power, now.value(e), m, q.c) : 0.0;
       } else {
         const double from = m > -kInf ? m : 0.0;        // a lane without a logit that counts adds zeros
         double add = 0.0;
@@ -160,7 +163,8 @@ __global__ void __launch_bounds__(kThreads) k_verify_scan(VerifyArgs p) {
 }
 
 // Joins the parts of a request's rows into LDS: `span` lanes (a power of two that holds num_parts) take a row.
-__device__ __forceinline__ void join_rows(const VerifyArgs& p, int b, const Request& q, bool sharp, VerifyRow* joined) {
+__device__ __forceinline__ void join_rows(const VerifyArgs& p, const Power& power, int b, const Request& q, bool sharp,
+                                          VerifyRow* joined) {
   const int span = p.num_parts <= 1 ? 1 : 1 << (32 - __builtin_clz(p.num_parts - 1));
   const int rows = 2 * p.drafts + 1, part = threadIdx.x & (span - 1);
   const int64_t row0 = static_cast<int64_t>(b) * rows;
@@ -176,7 +180,7 @@ __device__ __forceinline__ void join_rows(const VerifyArgs& p, int b, const Requ
       const int32_t oa = __shfl_xor(at, s);
       if (om > m || (om == m && static_cast<uint32_t>(oa) < static_cast<uint32_t>(at))) m = om, at = oa;
     }
-    double sum = v.m == -kInf || q.greedy ? 0.0 : v.sum * weight(v.m, m, q.c);
+    double sum = v.m == -kInf || q.greedy ? 0.0 : v.sum * weight(power, v.m, m, q.c);
     for (int s = 1; s < span; s <<= 1) sum += across(sum, s);
     if (read && part == 0) joined[r] = {sum > 0.0 ? 1.0 / sum : 0.0, m, at};
   }
@@ -194,18 +198,18 @@ __device__ __forceinline__ const T* draft_row(const VerifyArgs& p, int b, int pl
 
 // A tile of what the next token is drawn from, p - q, and of p alone.
 template <typename T>
-__device__ __forceinline__ void shares(const VerifyArgs& p, int b, const VerifyPlan& s, double c, int tile, int lane,
+__device__ __forceinline__ void shares(const VerifyArgs& p, const Power& power, int b, const VerifyPlan& s, double c, int tile, int lane,
                                        double (&rest)[kPer], double (&whole)[kPer]) {
   const bool two = s.minus && s.sharp < 0 && s.q.scale > 0.0;
   Tile<T> a, d;
   a.load(target_row<T>(p, b, s.n), tile * kVerifyTile, p.vocab, lane);
   if (two) d.load(draft_row<T>(p, b, s.n), tile * kVerifyTile, p.vocab, lane);
   for (int e = 0; e < kPer; ++e) {
-    whole[e] = s.p.scale > 0.0 ? weight(a.value(e), s.p.m, c) * s.p.scale : 0.0;
+    whole[e] = s.p.scale > 0.0 ? weight(power, a.value(e), s.p.m, c) * s.p.scale : 0.0;
     rest[e] = whole[e];
   }
   if (two)
-    for (int e = 0; e < kPer; ++e) rest[e] = fmax(whole[e] - weight(d.value(e), s.q.m, c) * s.q.scale, 0.0);
+    for (int e = 0; e < kPer; ++e) rest[e] = fmax(whole[e] - weight(power, d.value(e), s.q.m, c) * s.q.scale, 0.0);
   if (s.minus && s.sharp >= 0)
     for (int e = 0; e < kPer; ++e)
       if (s.sharp == tile * kVerifyTile + Tile<T>::place(e, lane)) rest[e] = 0.0;
@@ -217,6 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs p) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x / p.groups, g = blockIdx.x % p.groups;
   const Request q = request_of(p, b);
+  const Power power;
   const bool sharp = q.greedy || p.draft_logits == nullptr;
   // lane k looks at draft k
   int32_t token = -1;
@@ -231,18 +236,18 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs p) {
       if (!sharp) zt = static_cast<float>(draft_row<T>(p, b, lane)[token]);
     }
   }
-  join_rows(p, b, q, sharp, joined);
+  join_rows(p, power, b, q, sharp, joined);
   bool good = false;
   if (known) {
     const VerifyRow t = joined[lane];
     if (q.greedy) {
       good = t.at == token;
     } else {
-      const double pd = t.scale > 0.0 ? weight(xt, t.m, q.c) * t.scale : 0.0;
+      const double pd = t.scale > 0.0 ? weight(power, xt, t.m, q.c) * t.scale : 0.0;
       double qd = 1.0;
       if (!sharp) {
         const VerifyRow d = joined[p.drafts + 1 + lane];
-        qd = d.scale > 0.0 ? weight(zt, d.m, q.c) * d.scale : 0.0;
+        qd = d.scale > 0.0 ? weight(power, zt, d.m, q.c) * d.scale : 0.0;
       }
       good = static_cast<double>(u) * qd < pd;
     }
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_sums(VerifyArgs p) {
   double* sums = p.sums + static_cast<int64_t>(b) * p.tiles * 2;
   double rest[kPer], whole[kPer];
   for (int tile = g * kWaves + w; tile < p.tiles; tile += p.groups * kWaves) {
-    shares<T>(p, b, s, q.c, tile, lane, rest, whole);
+    shares<T>(p, power, b, s, q.c, tile, lane, rest, whole);
     double a = 0.0, c = 0.0;
     for (int e = 0; e < kPer; ++e) a += rest[e], c += whole[e];
     // even lanes go on with one sum, odd lanes with the other
@@ -287,6 +292,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_choose(VerifyArgs p) {
   __shared__ int found[2];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.x;
   const Request q = request_of(p, b);
+  const Power power;
   if (q.greedy) return;
   const VerifyPlan s = p.plans[b];
   const float u = p.uniforms[static_cast<int64_t>(b) * (p.drafts + 1) + p.drafts];
@@ -346,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_choose(VerifyArgs p) {
   if (w != 0) return;
   double left = start;
   double rest[kPer], whole[kPer];
-  shares<T>(p, b, s, q.c, tile, lane, rest, whole);
+  shares<T>(p, power, b, s, q.c, tile, lane, rest, whole);
   int32_t best = 0x7fffffff, last = -1;
   constexpr int V = kVec<T>;
   for (int e = 0; e < kPer; e += V) {
