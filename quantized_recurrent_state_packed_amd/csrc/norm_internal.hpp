@@ -12,7 +12,6 @@
 namespace stepq {
 
 constexpr int kMostWidth = 16384;
-constexpr int kNormGroups = 512;      // workgroups of a backward pass, each with its part of the weights' gradients
 
 // A tensor of tokens; nullptr: none.
 struct NormRows {
@@ -51,19 +50,25 @@ inline NormShape norm_shape(int width, int dtype) {
   if (n <= 4) return {4, 1};
   if (n <= 16) return {16, 1};
   if (n <= 64) return {64, 1};
-  if (n <= 128) return {64, 2};
-  if (n <= 512) return {256, 2};
-  if (n <= 1024) return {256, 4};
-  return {1024, 4};
+  if (n <= 128) return {128, 1};
+  if (n <= 256) return {256, 1};
+  if (n <= 512) return {512, 1};
+  if (n <= 1024) return {1024, 1};
+  return {1024, n <= 2048 ? 2 : 4};
 }
 
 // Rows that a workgroup has under way at a time.
-inline int norm_rows_at_once(const NormShape& s) { return s.lanes < 256 ? 256 / s.lanes : 1; }
+constexpr int kNormThreads = 256;
+inline int norm_rows_at_once(const NormShape& s) { return s.lanes < kNormThreads ? kNormThreads / s.lanes : 1; }
 
+// Workgroups of a backward pass, each with its part of the weights' gradients: as many as the chip holds at
+// once with 150 to 160 registers a lane.  8192 tokens of 4096 with 256 workgroups of 512 lanes 127 us, with 512 146
+// (half as many registers, to hold two of them a compute unit: 307, by what goes to memory and back).
 inline int32_t norm_groups(const stepq_norm_desc& d, int64_t rows) {
-  const int at_once = norm_rows_at_once(norm_shape(d.width, d.dtype));
-  const int64_t all = (rows + at_once - 1) / at_once;
-  return static_cast<int32_t>(all < kNormGroups ? all : kNormGroups);
+  const NormShape s = norm_shape(d.width, d.dtype);
+  const int at_once = norm_rows_at_once(s);
+  const int64_t all = (rows + at_once - 1) / at_once, most = s.lanes > kNormThreads ? 256 : 768;
+  return static_cast<int32_t>(all < most ? all : most);
 }
 
 hipError_t launch_norm_forward(const NormArgs& a, int dtype, hipStream_t s);

@@ -11,41 +11,64 @@
 //   dpost = sum m o r1,  do = r1 w m - o r1^3 mean(o w m),  dpre = sum dy t r2
 // The weights' gradients are summed over a workgroup's rows in registers, over workgroups
 // in a second launch, in order.
+#include <type_traits>
+
 #include "norm_internal.hpp"
 
 namespace stepq {
 namespace {
 
+// Workgroups of a forward pass: each takes several rows, so that weights are read once for them.  us of 8192
+// tokens of 4096, of 8192 x 48 rows of 128: 1024 workgroups 73, 58; 2048 79, 65; one a row 217, 133.
+constexpr int kGrid = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <typename T>
 constexpr int kVec = 16 / sizeof(T);
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// As it lies in memory until it is used: 16-bit pairs stay in one register.
 template <typename T>
-struct alignas(16) Piece {
-  T v[kVec<T>];
+struct Piece {
+  u32x4 raw;
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __builtin_bit_cast(float, static_cast<uint32_t>(raw[i]));
+    } else {
+      const uint32_t w = raw[i / 2];
+      if constexpr (std::is_same<T, __bf16>::value) return __builtin_bit_cast(float, i % 2 ? w & 0xffff0000u : w << 16);
+      else return static_cast<float>(__builtin_bit_cast(T, static_cast<uint16_t>(i % 2 ? w >> 16 : w)));
+    }
+  }
 };
+template <typename T>
+__device__ __forceinline__ u32x4 rounded(const float (&x)[kVec<T>]) {
+  typedef T Some __attribute__((ext_vector_type(kVec<T>)));
+  Some r;
+  for (int i = 0; i < kVec<T>; ++i) r[i] = static_cast<T>(x[i]);
+  return __builtin_bit_cast(u32x4, r);
+}
 
 // The values base + at .. of a row, zeros behind its end.  IN16: rows lie on 16-byte
 // boundaries and hold whole pieces.
 template <typename T, bool IN16>
 __device__ __forceinline__ Piece<T> load(const T* row, int at, int width) {
-  Piece<T> r;
-  if (IN16) {
-    if (at < width) return *reinterpret_cast<const Piece<T>*>(row + at);
-    for (int i = 0; i < kVec<T>; ++i) r.v[i] = static_cast<T>(0.0f);
+  if constexpr (IN16) {
+    Piece<T> r = {u32x4{0, 0, 0, 0}};
+    if (at < width) r.raw = *reinterpret_cast<const u32x4*>(row + at);
+    return r;
   } else {
-    for (int i = 0; i < kVec<T>; ++i) r.v[i] = at + i < width ? row[at + i] : static_cast<T>(0.0f);
+    typedef T Some __attribute__((ext_vector_type(kVec<T>)));
+    Some r;
+    for (int i = 0; i < kVec<T>; ++i) r[i] = at + i < width ? row[at + i] : static_cast<T>(0.0f);
+    return {__builtin_bit_cast(u32x4, r)};
   }
-  return r;
 }
 template <typename T, bool IN16>
 __device__ __forceinline__ void store(T* row, int at, int width, const float (&x)[kVec<T>]) {
-  if (IN16) {
-    if (at >= width) return;
-    Piece<T> r;
-    for (int i = 0; i < kVec<T>; ++i) r.v[i] = static_cast<T>(x[i]);
-    *reinterpret_cast<Piece<T>*>(row + at) = r;
+  if constexpr (IN16) {
+    if (at < width) *reinterpret_cast<u32x4*>(row + at) = rounded<T>(x);
   } else {
     for (int i = 0; i < kVec<T>; ++i)
       if (at + i < width) row[at + i] = static_cast<T>(x[i]);
@@ -74,13 +97,13 @@ __device__ __forceinline__ void row_sums(float (&x)[N], float (*lds)[N]) {
     }
   }
   if (L > 64) {
-    const int w = threadIdx.x >> 6;
+    const int w = threadIdx.x >> 6, first = threadIdx.x / L * (L / 64);
     if ((threadIdx.x & 63) == 0)
       for (int n = 0; n < N; ++n) lds[w][n] = x[n];
     __syncthreads();
     for (int n = 0; n < N; ++n) {
-      float all = lds[0][n];
-      for (int s = 1; s < L / 64; ++s) all += lds[s][n];
+      float all = lds[first][n];
+      for (int s = 1; s < L / 64; ++s) all += lds[first + s][n];
       x[n] = all;
     }
   }
@@ -125,43 +148,56 @@ __device__ __forceinline__ void load_weight(float (&w)[P][kVec<T>], const float*
     }
 }
 
+constexpr int threads_of(int L) { return L < kNormThreads ? kNormThreads : L; }
+constexpr int at_once(int L) { return threads_of(L) / L; }
+
+// The pieces of a row that a lane holds.
 template <typename T, bool IN16, int L, int P>
-__global__ void __launch_bounds__(L < 256 ? 256 : L) k_norm(NormArgs p) {
-  constexpr int V = kVec<T>, kAtOnce = L < 256 ? 256 / L : 1;
-  __shared__ float lds[2][L > 64 ? L / 64 : 1][1];
+__device__ __forceinline__ void load_row(const NormRows& r, int row, const NormArgs& p, int lane, Piece<T> (&x)[P]) {
+  if (r.p == nullptr) return;
+  const T* at = row_of<T>(r, row, p.heads, p.width);
+  for (int j = 0; j < P; ++j) x[j] = load<T, IN16>(at, (j * L + lane) * kVec<T>, p.width);
+}
+
+template <typename T, bool IN16, int L, int P>
+__global__ void __launch_bounds__(threads_of(L)) k_norm(NormArgs p) {
+  constexpr int V = kVec<T>, kAtOnce = at_once(L);
+  __shared__ float lds[2][threads_of(L) / 64][1];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const float inv = 1.0f / static_cast<float>(p.width);
   float w1[P][V], sc[P][V], w2[P][V];
   load_weight<T, P>(w1, p.post_weight, lane, L, p.width);
   load_weight<T, P>(sc, p.scale, lane, L, p.width);
   load_weight<T, P>(w2, p.pre_weight, lane, L, p.width);
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kAtOnce; first < p.rows; first += static_cast<int64_t>(gridDim.x) * kAtOnce) {
-    const int64_t mine = first + group;
-    const bool real = mine < p.rows;
-    const int row = static_cast<int>(real ? mine : first);
-    Piece<T> o[P], z[P], x[P];
-    for (int j = 0; j < P; ++j) {
-      const int at = (j * L + lane) * V;
-      o[j] = load<T, IN16>(row_of<T>(p.block, row, p.heads, p.width), at, p.width);
-      if (p.gate.p != nullptr) z[j] = load<T, IN16>(row_of<T>(p.gate, row, p.heads, p.width), at, p.width);
-      if (p.residual.p != nullptr) x[j] = load<T, IN16>(row_of<T>(p.residual, row, p.heads, p.width), at, p.width);
-    }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kAtOnce, first0 = static_cast<int64_t>(blockIdx.x) * kAtOnce;
+  Piece<T> o[P], z[P], x[P];
+  const auto read = [&](int64_t first) {        // groups behind the last row read it
+    const int row = static_cast<int>(first + group < p.rows ? first + group : p.rows - 1);
+    load_row<T, IN16, L, P>(p.block, row, p, lane, o);
+    load_row<T, IN16, L, P>(p.gate, row, p, lane, z);
+    load_row<T, IN16, L, P>(p.residual, row, p, lane, x);
+  };
+  if (first0 < p.rows) read(first0);
+  for (int64_t first = first0; first < p.rows; first += step) {
+    const bool real = first + group < p.rows;
+    const int row = static_cast<int>(real ? first + group : p.rows - 1);
     float r1 = 1.0f;
     if (p.post) {
       float s[1] = {0.0f};
       for (int j = 0; j < P; ++j)
-        for (int i = 0; i < V; ++i) s[0] = fmaf(static_cast<float>(o[j].v[i]), static_cast<float>(o[j].v[i]), s[0]);
+        for (int i = 0; i < V; ++i) s[0] = fmaf(o[j][i], o[j][i], s[0]);
       row_sums<L>(s, lds[0]);
       r1 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, p.eps));
     }
     float t[P][V], s[1] = {0.0f};
     for (int j = 0; j < P; ++j)
       for (int i = 0; i < V; ++i) {
-        float g = static_cast<float>(o[j].v[i]) * r1 * w1[j][i];
-        if (p.gate.p != nullptr) g *= activated(static_cast<float>(z[j].v[i]), p.silu);
-        t[j][i] = p.residual.p != nullptr ? fmaf(sc[j][i], g, static_cast<float>(x[j].v[i])) : sc[j][i] * g;
+        float g = o[j][i] * r1 * w1[j][i];
+        if (p.gate.p != nullptr) g *= activated(z[j][i], p.silu);
+        t[j][i] = p.residual.p != nullptr ? fmaf(sc[j][i], g, x[j][i]) : sc[j][i] * g;
         s[0] = fmaf(t[j][i], t[j][i], s[0]);
       }
+    if (first + step < p.rows) read(first + step);      // in flight while this row ends
     if (p.out.p != nullptr && real)
       for (int j = 0; j < P; ++j)
         store<T, IN16>(out_row_of<T>(p.out, row, p.heads, p.width), (j * L + lane) * V, p.width, t[j]);
@@ -180,10 +216,10 @@ __global__ void __launch_bounds__(L < 256 ? 256 : L) k_norm(NormArgs p) {
 }
 
 template <typename T, bool IN16, int L, int P>
-__global__ void __launch_bounds__(L < 256 ? 256 : L) k_norm_backward(NormArgs p) {
-  constexpr int V = kVec<T>, kAtOnce = L < 256 ? 256 / L : 1;
-  __shared__ float lds1[L > 64 ? L / 64 : 1][3];
-  __shared__ float lds2[L > 64 ? L / 64 : 1][1];
+__global__ void __launch_bounds__(threads_of(L)) k_norm_backward(NormArgs p) {
+  constexpr int V = kVec<T>, kAtOnce = at_once(L), kThreads = threads_of(L);
+  __shared__ float lds1[kThreads / 64][3];
+  __shared__ float lds2[kThreads / 64][1];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const float inv = 1.0f / static_cast<float>(p.width);
   float w1[P][V], sc[P][V], w2[P][V], d1[P][V], ds[P][V], d2[P][V];
@@ -192,72 +228,74 @@ __global__ void __launch_bounds__(L < 256 ? 256 : L) k_norm_backward(NormArgs p)
   load_weight<T, P>(w2, p.pre_weight, lane, L, p.width);
   for (int j = 0; j < P; ++j)
     for (int i = 0; i < V; ++i) d1[j][i] = ds[j][i] = d2[j][i] = 0.0f;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kAtOnce; first < p.rows; first += static_cast<int64_t>(gridDim.x) * kAtOnce) {
-    const int64_t mine = first + group;
-    const bool real = mine < p.rows;
-    const int row = static_cast<int>(real ? mine : first);
-    Piece<T> o[P], z[P], t[P], gt[P], gy[P];
-    for (int j = 0; j < P; ++j) {
-      const int at = (j * L + lane) * V;
-      o[j] = load<T, IN16>(row_of<T>(p.block, row, p.heads, p.width), at, p.width);
-      if (p.gate.p != nullptr) z[j] = load<T, IN16>(row_of<T>(p.gate, row, p.heads, p.width), at, p.width);
-      if (p.d_out.p != nullptr) gt[j] = load<T, IN16>(row_of<T>(p.d_out, row, p.heads, p.width), at, p.width);
-      if (p.pre) {
-        t[j] = load<T, IN16>(row_of<T>(p.out, row, p.heads, p.width), at, p.width);
-        gy[j] = load<T, IN16>(row_of<T>(p.d_normed, row, p.heads, p.width), at, p.width);
-      }
-    }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kAtOnce, first0 = static_cast<int64_t>(blockIdx.x) * kAtOnce;
+  Piece<T> o[P], z[P], t[P], gt[P], gy[P];
+  const auto read = [&](int64_t first) {        // groups behind the last row read it
+    const int row = static_cast<int>(first + group < p.rows ? first + group : p.rows - 1);
+    load_row<T, IN16, L, P>(p.block, row, p, lane, o);
+    load_row<T, IN16, L, P>(p.gate, row, p, lane, z);
+    load_row<T, IN16, L, P>(p.d_out, row, p, lane, gt);
+    load_row<T, IN16, L, P>(p.out, row, p, lane, t);
+    load_row<T, IN16, L, P>(p.d_normed, row, p, lane, gy);
+  };
+  if (first0 < p.rows) read(first0);
+  for (int64_t first = first0; first < p.rows; first += step) {
+    const bool real = first + group < p.rows;
+    const int row = static_cast<int>(real ? first + group : p.rows - 1);
     float s[3] = {0.0f, 0.0f, 0.0f};
     for (int j = 0; j < P; ++j)
       for (int i = 0; i < V; ++i) {
-        const float a = static_cast<float>(o[j].v[i]);
+        const float a = o[j][i];
         s[0] = fmaf(a, a, s[0]);
         if (p.pre) {
-          const float b = static_cast<float>(t[j].v[i]);
+          const float b = t[j][i];
           s[1] = fmaf(b, b, s[1]);
-          s[2] = fmaf(b, w2[j][i] * static_cast<float>(gy[j].v[i]), s[2]);
+          s[2] = fmaf(b, w2[j][i] * gy[j][i], s[2]);
         }
       }
     row_sums<L>(s, lds1);
     const float r1 = p.post ? __builtin_amdgcn_rsqf(fmaf(s[0], inv, p.eps)) : 1.0f;
     const float r2 = __builtin_amdgcn_rsqf(fmaf(s[1], inv, p.eps)), back = s[2] * inv * r2 * r2;
     float m[P][V], sum[1] = {0.0f};
+    Piece<T> keep[P];
     for (int j = 0; j < P; ++j) {
       float all[V], dz[V];
       for (int i = 0; i < V; ++i) {
-        float g = p.d_out.p != nullptr ? static_cast<float>(gt[j].v[i]) : 0.0f;
+        float g = p.d_out.p != nullptr ? gt[j][i] : 0.0f;
         if (p.pre) {
-          const float b = static_cast<float>(t[j].v[i]), dy = static_cast<float>(gy[j].v[i]);
+          const float b = t[j][i], dy = gy[j][i];
           g += r2 * (w2[j][i] * dy - b * back);
-          if (real) d2[j][i] = fmaf(dy, b * r2, d2[j][i]);
+          d2[j][i] = fmaf(real ? dy : 0.0f, b * r2, d2[j][i]);
         }
         all[i] = g;
-        const float u = static_cast<float>(o[j].v[i]) * r1, n = u * w1[j][i];
+        const float u = o[j][i] * r1, n = u * w1[j][i];
         float slope = 0.0f, act = 1.0f;
-        if (p.gate.p != nullptr) act = activated(static_cast<float>(z[j].v[i]), p.silu, slope);
-        if (real) ds[j][i] = fmaf(g, n * act, ds[j][i]);
+        if (p.gate.p != nullptr) act = activated(z[j][i], p.silu, slope);
+        ds[j][i] = fmaf(real ? g : 0.0f, n * act, ds[j][i]);
         const float q = g * sc[j][i];
         dz[i] = q * n * slope;
         const float k = q * act;
-        if (real) d1[j][i] = fmaf(k, u, d1[j][i]);
+        d1[j][i] = fmaf(real ? k : 0.0f, u, d1[j][i]);
         m[j][i] = k * w1[j][i];
-        sum[0] = fmaf(static_cast<float>(o[j].v[i]), m[j][i], sum[0]);
+        sum[0] = fmaf(o[j][i], m[j][i], sum[0]);
       }
       const int at = (j * L + lane) * V;
       if (p.d_residual.p != nullptr && real) store<T, IN16>(out_row_of<T>(p.d_residual, row, p.heads, p.width), at, p.width, all);
       if (p.gate.p != nullptr && real) store<T, IN16>(out_row_of<T>(p.d_gate, row, p.heads, p.width), at, p.width, dz);
+      keep[j] = o[j];
     }
+    if (first + step < p.rows) read(first + step);      // in flight while this row ends
     row_sums<L>(sum, lds2);
     const float mean = p.post ? sum[0] * inv * r1 * r1 : 0.0f;
     for (int j = 0; j < P; ++j) {
       float d[V];
-      for (int i = 0; i < V; ++i) d[i] = r1 * (m[j][i] - static_cast<float>(o[j].v[i]) * mean);
+      for (int i = 0; i < V; ++i) d[i] = r1 * (m[j][i] - keep[j][i] * mean);
       if (real) store<T, IN16>(out_row_of<T>(p.d_block, row, p.heads, p.width), (j * L + lane) * V, p.width, d);
     }
   }
   if (p.partial == nullptr) return;
   // the workgroup's rows that were under way together are added in order
-  constexpr int kSlots = kAtOnce > 1 ? 256 * V * P : 1;
+  constexpr int kSlots = kAtOnce > 1 ? kThreads * V * P : 1;
   __shared__ float part[kSlots];
   for (int k = 0; k < 3; ++k) {
     float(&d)[P][V] = k == 0 ? d1 : k == 1 ? ds : d2;
@@ -267,7 +305,7 @@ __global__ void __launch_bounds__(L < 256 ? 256 : L) k_norm_backward(NormArgs p)
       for (int j = 0; j < P; ++j)
         for (int i = 0; i < V; ++i) part[group * (L * V * P) + (j * L + lane) * V + i] = d[j][i];
       __syncthreads();
-      for (int at = threadIdx.x; at < L * V * P && at < p.width; at += 256) {
+      for (int at = threadIdx.x; at < L * V * P && at < p.width; at += kThreads) {
         float all = part[at];
         for (int g = 1; g < kAtOnce; ++g) all += part[g * (L * V * P) + at];
         to[at] = all;
@@ -312,24 +350,24 @@ bool in_pieces(const NormArgs& a, int esize) {
 template <typename T, bool IN16, bool BACK>
 void launch(const NormArgs& a, int dtype, hipStream_t s) {
   const NormShape n = norm_shape(a.width, dtype);
-  const int at_once = norm_rows_at_once(n);
-  const int64_t all = (static_cast<int64_t>(a.rows) + at_once - 1) / at_once;
-  const dim3 grid(static_cast<uint32_t>(BACK ? a.groups : all < 2048 ? all : 2048));
+  const int64_t all = (static_cast<int64_t>(a.rows) + norm_rows_at_once(n) - 1) / norm_rows_at_once(n);
+  const dim3 grid(static_cast<uint32_t>(BACK ? a.groups : all < kGrid ? all : kGrid));
   const auto go = [&](auto lanes, auto pieces) {
     constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
-    if (BACK) k_norm_backward<T, IN16, L, P><<<grid, L < 256 ? 256 : L, 0, s>>>(a);
-    else k_norm<T, IN16, L, P><<<grid, L < 256 ? 256 : L, 0, s>>>(a);
+    if (n.lanes != L || n.pieces != P) return;
+    if (BACK) k_norm_backward<T, IN16, L, P><<<grid, threads_of(L), 0, s>>>(a);
+    else k_norm<T, IN16, L, P><<<grid, threads_of(L), 0, s>>>(a);
   };
-  const auto is = [&](auto lanes, auto pieces) {
-    if (n.lanes != decltype(lanes)::value || n.pieces != decltype(pieces)::value) return false;
-    go(lanes, pieces);
-    return true;
-  };
-#define STEPQ_INT(x) std::integral_constant<int, x>{}
-  is(STEPQ_INT(4), STEPQ_INT(1)) || is(STEPQ_INT(16), STEPQ_INT(1)) || is(STEPQ_INT(64), STEPQ_INT(1)) ||
-      is(STEPQ_INT(64), STEPQ_INT(2)) || is(STEPQ_INT(256), STEPQ_INT(2)) || is(STEPQ_INT(256), STEPQ_INT(4)) ||
-      is(STEPQ_INT(1024), STEPQ_INT(4));
-#undef STEPQ_INT
+  const std::integral_constant<int, 1> one{};
+  go(std::integral_constant<int, 4>{}, one);
+  go(std::integral_constant<int, 16>{}, one);
+  go(std::integral_constant<int, 64>{}, one);
+  go(std::integral_constant<int, 128>{}, one);
+  go(std::integral_constant<int, 256>{}, one);
+  go(std::integral_constant<int, 512>{}, one);
+  go(std::integral_constant<int, 1024>{}, one);
+  go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  if constexpr (sizeof(T) == 4) go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
 template <typename T, bool BACK>
