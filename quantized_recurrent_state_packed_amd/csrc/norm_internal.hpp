@@ -45,7 +45,7 @@ struct NormArgs {
 struct NormShape {
   int lanes, pieces;
 };
-inline NormShape norm_shape(int width, int dtype) {
+inline NormShape norm_shape(int width, int dtype, bool backward) {
   const int n = dtype == STEPQ_F32 ? (width + 3) / 4 : (width + 7) / 8;      // pieces of a row
   if (n <= 4) return {4, 1};
   if (n <= 16) return {16, 1};
@@ -53,6 +53,10 @@ inline NormShape norm_shape(int width, int dtype) {
   if (n <= 128) return {128, 1};
   if (n <= 256) return {256, 1};
   if (n <= 512) return {512, 1};
+  // a backward pass needs more registers than the 128 that each of 1024 lanes has: 4096 tokens of 8192 bfloat16
+  // values, 266 us with 1024 lanes, 155 with 512; binary32 271, 213
+  if (backward && dtype != STEPQ_F32 && n <= 1024) return {512, 2};
+  if (backward && dtype == STEPQ_F32 && n > 1024 && n <= 2048) return {512, 4};
   if (n <= 1024) return {1024, 1};
   return {1024, n <= 2048 ? 2 : 4};
 }
@@ -65,7 +69,7 @@ inline int norm_rows_at_once(const NormShape& s) { return s.lanes < kNormThreads
 // once with 150 to 160 registers a lane.  8192 tokens of 4096 with 256 workgroups of 512 lanes 127 us, with 512 146
 // (half as many registers, to hold two of them a compute unit: 307, by what goes to memory and back).
 inline int32_t norm_groups(const stepq_norm_desc& d, int64_t rows) {
-  const NormShape s = norm_shape(d.width, d.dtype);
+  const NormShape s = norm_shape(d.width, d.dtype, true);
   const int at_once = norm_rows_at_once(s);
   const int64_t all = (rows + at_once - 1) / at_once, most = s.lanes > kNormThreads ? 256 : 768;
   return static_cast<int32_t>(all < most ? all : most);

@@ -50,8 +50,15 @@ __device__ __forceinline__ u32x4 rounded(const float (&x)[kVec<T>]) {
   return __builtin_bit_cast(u32x4, r);
 }
 
-// The values base + at .. of a row, zeros behind its end.  IN16: rows lie on 16-byte
-// boundaries and hold whole pieces.
+// 16 bytes on the boundary of an element: the memory system takes them whole, a cache line more at worst.
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Anywhere {
+  u32x4 raw;
+};
+
+// The values at .. of a row, zeros behind its end.  IN16: rows lie on 16-byte boundaries and hold whole
+// pieces.  us of 8192 bfloat16 tokens of 1001, forward and backward, with single elements 52, 97, with 16 bytes
+// anywhere 22, 64.
 template <typename T, bool IN16>
 __device__ __forceinline__ Piece<T> load(const T* row, int at, int width) {
   if constexpr (IN16) {
@@ -59,6 +66,7 @@ __device__ __forceinline__ Piece<T> load(const T* row, int at, int width) {
     if (at < width) r.raw = *reinterpret_cast<const u32x4*>(row + at);
     return r;
   } else {
+    if (at + kVec<T> <= width) return {reinterpret_cast<const Anywhere<T>*>(row + at)->raw};
     typedef T Some __attribute__((ext_vector_type(kVec<T>)));
     Some r;
     for (int i = 0; i < kVec<T>; ++i) r[i] = at + i < width ? row[at + i] : static_cast<T>(0.0f);
@@ -69,6 +77,8 @@ template <typename T, bool IN16>
 __device__ __forceinline__ void store(T* row, int at, int width, const float (&x)[kVec<T>]) {
   if constexpr (IN16) {
     if (at < width) *reinterpret_cast<u32x4*>(row + at) = rounded<T>(x);
+  } else if (at + kVec<T> <= width) {
+    reinterpret_cast<Anywhere<T>*>(row + at)->raw = rounded<T>(x);
   } else {
     for (int i = 0; i < kVec<T>; ++i)
       if (at + i < width) row[at + i] = static_cast<T>(x[i]);
@@ -138,14 +148,20 @@ __device__ __forceinline__ T* out_row_of(const NormRows& r, int row, int heads, 
   return const_cast<T*>(row_of<T>(r, row, heads, width));
 }
 
-// A lane's part of a weight, 1 where there is none.
+// A lane's part of a weight, 1 where there is none and behind the row's end.
 template <typename T, int P>
 __device__ __forceinline__ void load_weight(float (&w)[P][kVec<T>], const float* from, int lane, int L, int width) {
-  for (int j = 0; j < P; ++j)
-    for (int i = 0; i < kVec<T>; ++i) {
-      const int at = (j * L + lane) * kVec<T> + i;
-      w[j][i] = from != nullptr && at < width ? from[at] : 1.0f;
+  for (int j = 0; j < P; ++j) {
+    const int at = (j * L + lane) * kVec<T>;
+    if (from != nullptr && at + kVec<T> <= width) {
+      for (int i = 0; i < kVec<T>; i += 4) {
+        const u32x4 r = reinterpret_cast<const Anywhere<float>*>(from + at + i)->raw;
+        for (int k = 0; k < 4; ++k) w[j][i + k] = __builtin_bit_cast(float, static_cast<uint32_t>(r[k]));
+      }
+    } else {
+      for (int i = 0; i < kVec<T>; ++i) w[j][i] = from != nullptr && at + i < width ? from[at + i] : 1.0f;
     }
+  }
 }
 
 constexpr int threads_of(int L) { return L < kNormThreads ? kNormThreads : L; }
@@ -223,9 +239,15 @@ __global__ void __launch_bounds__(threads_of(L)) k_norm_backward(NormArgs p) {
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const float inv = 1.0f / static_cast<float>(p.width);
   float w1[P][V], sc[P][V], w2[P][V], d1[P][V], ds[P][V], d2[P][V];
-  load_weight<T, P>(w1, p.post_weight, lane, L, p.width);
-  load_weight<T, P>(sc, p.scale, lane, L, p.width);
-  load_weight<T, P>(w2, p.pre_weight, lane, L, p.width);
+  const auto weights = [&]() {
+    load_weight<T, P>(w1, p.post_weight, lane, L, p.width);
+    load_weight<T, P>(sc, p.scale, lane, L, p.width);
+    load_weight<T, P>(w2, p.pre_weight, lane, L, p.width);
+  };
+  // lanes with several pieces have no room to keep the weights too, every row reads them again: 4096 tokens
+  // of 8192 bfloat16 values 155 us against 294
+  constexpr bool kAgain = P > 1;
+  if (!kAgain) weights();
   for (int j = 0; j < P; ++j)
     for (int i = 0; i < V; ++i) d1[j][i] = ds[j][i] = d2[j][i] = 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kAtOnce, first0 = static_cast<int64_t>(blockIdx.x) * kAtOnce;
@@ -242,6 +264,7 @@ __global__ void __launch_bounds__(threads_of(L)) k_norm_backward(NormArgs p) {
   for (int64_t first = first0; first < p.rows; first += step) {
     const bool real = first + group < p.rows;
     const int row = static_cast<int>(real ? first + group : p.rows - 1);
+    if (kAgain) weights();
     float s[3] = {0.0f, 0.0f, 0.0f};
     for (int j = 0; j < P; ++j)
       for (int i = 0; i < V; ++i) {
@@ -328,8 +351,13 @@ __global__ void __launch_bounds__(1024) k_norm_weights(NormArgs p) {
   if (to == nullptr) return;
   const int c = blockIdx.x * 64 + lane;
   double sum = 0.0;
+  const float* part = p.partial + static_cast<int64_t>(k) * p.groups * p.width + c;
   if (c < p.width)
-    for (int g = w; g < p.groups; g += 16) sum += p.partial[(static_cast<int64_t>(k) * p.groups + g) * p.width + c];
+    for (int g = w; g < p.groups; g += 128) {
+      float x[8];                     // under way together
+      for (int j = 0; j < 8; ++j) x[j] = g + 16 * j < p.groups ? part[static_cast<int64_t>(g + 16 * j) * p.width] : 0.0f;
+      for (int j = 0; j < 8; ++j) sum += x[j];
+    }
   sums[w][lane] = sum;
   __syncthreads();
   if (w != 0 || c >= p.width) return;
@@ -349,7 +377,7 @@ bool in_pieces(const NormArgs& a, int esize) {
 
 template <typename T, bool IN16, bool BACK>
 void launch(const NormArgs& a, int dtype, hipStream_t s) {
-  const NormShape n = norm_shape(a.width, dtype);
+  const NormShape n = norm_shape(a.width, dtype, BACK);
   const int64_t all = (static_cast<int64_t>(a.rows) + norm_rows_at_once(n) - 1) / norm_rows_at_once(n);
   const dim3 grid(static_cast<uint32_t>(BACK ? a.groups : all < kGrid ? all : kGrid));
   const auto go = [&](auto lanes, auto pieces) {
@@ -365,8 +393,9 @@ void launch(const NormArgs& a, int dtype, hipStream_t s) {
   go(std::integral_constant<int, 128>{}, one);
   go(std::integral_constant<int, 256>{}, one);
   go(std::integral_constant<int, 512>{}, one);
-  go(std::integral_constant<int, 1024>{}, one);
-  go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  if constexpr (BACK) go(std::integral_constant<int, 512>{}, std::integral_constant<int, sizeof(T)>{});
+  if constexpr (!BACK || sizeof(T) == 4) go(std::integral_constant<int, 1024>{}, one);
+  if constexpr (!BACK || sizeof(T) == 2) go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
   if constexpr (sizeof(T) == 4) go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 

@@ -532,7 +532,11 @@ __global__ void __launch_bounds__(1024) k_scan_decay(ScanArgs p) {
   const int c = blockIdx.x * 64 + lane;
   double sum = 0.0;
   if (c < p.width)
-    for (int64_t j = w; j < p.pieces; j += 16) sum += p.partial[j * p.width + c];
+    for (int64_t j = w; j < p.pieces; j += 128) {
+      float x[8];                     // under way together
+      for (int i = 0; i < 8; ++i) x[i] = j + 16 * i < p.pieces ? p.partial[(j + 16 * i) * p.width + c] : 0.0f;
+      for (int i = 0; i < 8; ++i) sum += x[i];
+    }
   sums[w][lane] = sum;
   __syncthreads();
   if (w != 0 || c >= p.width) return;
