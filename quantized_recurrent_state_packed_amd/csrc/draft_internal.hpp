@@ -66,7 +66,7 @@ inline int32_t verify_tiles(int32_t vocab) { return (vocab + kVerifyTile - 1) / 
 // Waves a row is split over: enough that all rows together give the chip 16384 of them (64 a compute
 // unit, four times what it holds, since rows behind a request's drafts and greedy requests' leave waves without
 // work), none of them shorter than a tile.  64 requests of 5 drafts over 131072 tokens, us of the
-// scan: with 4096 waves 85, with 16384 TIME16.
+// scan: with 4096 waves 85, with 16384 62.
 inline int32_t verify_parts(int64_t rows, int32_t vocab) {
   int64_t parts = (16384 + rows - 1) / rows;
   if (parts > 64) parts = 64;
