@@ -378,8 +378,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan(ScanArgs p) {
       for (int v = 0; v < V; ++v) {
         const float less = one_less_exp2(speed[v] * logistic(gr[t][v]));
         const float keep = 1.0f - less;
-        const float in = __builtin_amdgcn_sqrtf(less * (1.0f + keep)) * logistic(ir[t][v]) *
-                         xr[t][v];
+        const float in = __builtin_amdgcn_sqrtf(less * (1.0f + keep)) * logistic(ir[t][v]) * xr[t][v];
         a[t][v] = WHOLE || t < n ? keep : 1.0f;
         u[t][v] = WHOLE || t < n ? in : 0.0f;
         A[v] *= a[t][v], B[v] = fmaf(a[t][v], B[v], u[t][v]);
@@ -442,10 +441,14 @@ __global__ void __launch_bounds__(64 * kBackWaves, 4) k_scan_backward(ScanArgs p
       for (int v = 0; v < V; ++v) speed[v] = __builtin_nanf("");
     const Rows<T, V> x(p.x, p.x_stride, t0, cc), ga(p.ga, p.ga_stride, t0, cc), gx(p.gx, p.gx_stride, t0, cc);
     const Rows<T, V> dy(p.dy, p.dy_stride, t0, cc);
-    for (int t = 0; t < R; ++t) {                   // rows behind the last one are read as it
+    // in the order of their use; rows behind the last one are read as it
+    for (int t = R - 1; t >= 0; --t) {
       const int row = WHOLE ? t : min(t, n - 1);
       ar[t] = ga.load(row);
       gr[t] = dy.load(row);
+    }
+    for (int t = 0; t < R; ++t) {
+      const int row = WHOLE ? t : min(t, n - 1);
       xr[t] = x.load(row);
       ir[t] = gx.load(row);
     }
@@ -473,12 +476,10 @@ __global__ void __launch_bounds__(64 * kBackWaves, 4) k_scan_backward(ScanArgs p
       slow[v] = speed[v] * kLog2;
     }
     for (int t = 0; t < R; ++t) {
-      again(ar[t]), again(ir[t]), again(xr[t]), again(gr[t]);
       for (int v = 0; v < V; ++v) {
         const float a = 1.0f - less[t][v];
         before[t][v] = h[v];
-        h[v] = fmaf(a, h[v], __builtin_amdgcn_sqrtf(less[t][v] * (1.0f + a)) * logistic(ir[t][v]) *
-                                 xr[t][v]);
+        h[v] = fmaf(a, h[v], __builtin_amdgcn_sqrtf(less[t][v] * (1.0f + a)) * logistic(ir[t][v]) * xr[t][v]);
       }
       again(ir[t]), again(xr[t]);
     }
@@ -487,7 +488,8 @@ __global__ void __launch_bounds__(64 * kBackWaves, 4) k_scan_backward(ScanArgs p
       float ox[V], oa[V], oi[V];
       for (int v = 0; v < V; ++v) {
         const float a = 1.0f - less[t][v], b2 = less[t][v] * (1.0f + a);
-        const float inv = b2 > 0.0f ? __builtin_amdgcn_rsqf(b2) : 0.0f;       // a state that is kept whole has no slope
+        // a state that is kept whole has no slope; the reciprocal root of a number below the normal ones is infinite
+        const float inv = b2 >= 1.17549435e-38f ? __builtin_amdgcn_rsqf(b2) : 0.0f;
         const float ra = logistic(ar[t][v]), ri = logistic(ir[t][v]);
         const float gain = ri * xr[t][v];
         const float now = g[v] + gr[t][v], in = now * (b2 * inv);

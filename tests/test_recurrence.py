@@ -391,6 +391,24 @@ def test_gates_and_decays_at_their_ends(dtype):
 
 
 @pytest.mark.gpu
+def test_gates_and_decays_that_leave_hardly_anything():
+    """1 - a of the size of the smallest binary32 numbers and below: what comes in is at most their root, 1e-18, and
+    every gradient is finite."""
+    import torch
+    c = Case([300], 8, "f32", lead=0, tail=0, resume=False)
+    c.ga[:, :4] = torch.linspace(-60.0, -104.0, 300, device="cuda")[:, None]
+    c.decay[:4] = torch.tensor([-5.0, 0.0, 5.0, -20.0], device="cuda")
+    c.decay[4:] = torch.tensor([-85.0, -87.5, -95.0, -110.0], device="cuda")
+    ws, saved = c.buffers()
+    c.forward(saved, workspace=ws)
+    c.backward(saved, workspace=ws)
+    torch.cuda.synchronize()
+    for t in (c.y, c.dx, c.dga, c.dgx, c.ddecay, c.state, c.dstate):
+        assert torch.isfinite(t).all()
+    assert float(c.y.abs().max()) < 1e-10 and float(c.dga.abs().max()) < 1e-10
+
+
+@pytest.mark.gpu
 def test_a_value_that_is_not_finite_spoils_its_own_request_and_channel_alone():
     import torch
     c, d = (Case([200, 70], 10, "f32", seed=4) for _ in range(2))
