@@ -13,7 +13,7 @@ stepq_status check_sizes(const stepq_norm_desc* d, int64_t tokens) {
   if (d->dtype != STEPQ_F32 && d->dtype != STEPQ_BF16 && d->dtype != STEPQ_F16) return STEPQ_ERR_INVALID_ARG;
   if (d->activation != STEPQ_GATE_SILU && d->activation != STEPQ_GATE_SIGMOID) return STEPQ_ERR_INVALID_ARG;
   if ((d->post != 0 && d->post != 1) || (d->pre != 0 && d->pre != 1)) return STEPQ_ERR_INVALID_ARG;
-  if (!std::isfinite(d->eps) || !(d->eps > 0.0f) || tokens < 0) return STEPQ_ERR_INVALID_ARG;
+  if (!std::isnormal(d->eps) || d->eps < 0.0f || tokens < 0) return STEPQ_ERR_INVALID_ARG;
   if (d->width > stepq::kMostWidth) return STEPQ_ERR_UNSUPPORTED;
   return tokens > 0x7fffffffLL / d->heads ? STEPQ_ERR_UNSUPPORTED : STEPQ_OK;
 }
@@ -23,6 +23,11 @@ int elem_bytes(int dtype) { return dtype == STEPQ_F32 ? 4 : 2; }
 bool rows_ok(const stepq::NormRows& r, const stepq_norm_desc& d) {
   return aligned(r.p, elem_bytes(d.dtype)) && r.stride >= static_cast<int64_t>(d.heads) * d.width &&
          r.stride <= (int64_t{1} << 40);
+}
+
+// An output in an input's buffer overwrites what its own lanes have read, if the rows lie alike.
+bool apart_or_alike(const stepq::NormRows& out, const stepq::NormRows& in, int64_t tokens) {
+  return !out.p || out.p != in.p || out.stride == in.stride || tokens == 1;
 }
 
 stepq_status from_hip(hipError_t e) { return e == hipSuccess ? STEPQ_OK : STEPQ_ERR_HIP; }
@@ -70,6 +75,9 @@ stepq_status stepq_norm_forward(const stepq_norm_desc* d, int64_t tokens, const 
   const stepq::NormRows* rows[] = {&a.block, &a.gate, &a.residual, &a.out, &a.normed};
   for (const stepq::NormRows* r : rows)
     if (r->p && !rows_ok(*r, *d)) return STEPQ_ERR_INVALID_ARG;
+  for (const stepq::NormRows* to : {&a.out, &a.normed})
+    for (const stepq::NormRows* from : {&a.block, &a.gate, &a.residual})
+      if (!apart_or_alike(*to, *from, tokens)) return STEPQ_ERR_INVALID_ARG;
   if (!aligned(post_weight, 4) || !aligned(scale, 4) || !aligned(pre_weight, 4)) return STEPQ_ERR_INVALID_ARG;
   a.post_weight = post_weight; a.scale = scale; a.pre_weight = pre_weight;
   flatten(a);
@@ -115,6 +123,9 @@ stepq_status stepq_norm_backward(const stepq_norm_desc* d, int64_t tokens, const
     const stepq::NormRows* rows[] = {&a.block, &a.gate, &a.out, &a.d_out, &a.d_normed, &a.d_block, &a.d_gate, &a.d_residual};
     for (const stepq::NormRows* r : rows)
       if (r->p && !rows_ok(*r, *d)) return STEPQ_ERR_INVALID_ARG;
+    for (const stepq::NormRows* to : {&a.d_block, &a.d_gate, &a.d_residual})
+      for (const stepq::NormRows* from : {&a.block, &a.gate, &a.out, &a.d_out, &a.d_normed})
+        if (!apart_or_alike(*to, *from, tokens)) return STEPQ_ERR_INVALID_ARG;
     if (d_post_weight || d_scale || d_pre_weight) {
       if (!workspace || !aligned(workspace, 16) || workspace_bytes < stepq_norm_workspace_bytes(d, tokens))
         return STEPQ_ERR_INVALID_ARG;

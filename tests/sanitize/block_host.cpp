@@ -93,7 +93,7 @@ void scans(std::mt19937& g) {
 
 void norms() {
   uint8_t* const base = reinterpret_cast<uint8_t*>(1 << 20);
-  void *a = reinterpret_cast<void*>(4096), *b = reinterpret_cast<void*>(8192), *c = reinterpret_cast<void*>(12288);
+  void *a = reinterpret_cast<void*>(4096), *b = reinterpret_cast<void*>(8192), *c = reinterpret_cast<void*>(12288), *e = reinterpret_cast<void*>(16384);
   float* f = static_cast<float*>(a);
   for (int width : {1, 31, 32, 33, 128, 129, 512, 1024, 4096, 4097, 8192, 16384})
     for (int heads : {1, 3})
@@ -106,7 +106,7 @@ void norms() {
                                     bytes, nullptr) == STEPQ_OK);
           CHECK(norm.groups >= 1 && static_cast<size_t>(norm.groups) * 3 * width * 4 <= bytes);
           CHECK(norm.heads == 1 && norm.block.stride == width && norm.rows == tokens * heads);
-          CHECK(stepq_norm_backward(&d, tokens, a, row + 8, a, row, a, row, f, f, f, a, row, a, row, a, row, b, row, c, row, f, f, f, base,
+          CHECK(stepq_norm_backward(&d, tokens, a, row + 8, a, row, a, row, f, f, f, a, row, a, row, e, row, b, row, c, row, f, f, f, base,
                                     bytes, nullptr) == STEPQ_OK);
           CHECK(norm.heads == heads && norm.rows == tokens * heads);
           const stepq::NormShape s = stepq::norm_shape(width, dtype, true), t = stepq::norm_shape(width, dtype, false);

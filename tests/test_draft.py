@@ -372,6 +372,36 @@ def test_rows_past_32_bits():
 
 
 @pytest.mark.gpu
+def test_the_largest_vocabulary():
+    """2^31 - 1 - 1024 logits, all banned but some at the ends, in the middle and beside a seam of tiles; and a draft."""
+    import torch
+    V = 2 ** 31 - 1 - 1024
+    x = torch.full((2, V), -float("inf"), dtype=torch.bfloat16, device="cuda")
+    at = [0, 1023, 1024, V // 2, V - 1025, V - 1]
+    for t in at:
+        x[:, t] = 1.0
+    op = DR.DraftVerify(1, 1, V, torch.bfloat16)
+    d = torch.tensor([[V - 1]], dtype=torch.int32, device="cuda")
+    for n, t in enumerate(at):
+        u = torch.tensor([[0.1, (n + 0.5) / len(at)]], device="cuda")
+        acc, tokens = op(x, d, u)
+        assert acc.tolist() == [1] and tokens.tolist() == [[V - 1, t]]
+    acc, tokens = op(x, d, torch.tensor([[0.9, 0.99]], device="cuda"))       # rejected: the last of the others
+    assert acc.tolist() == [0] and tokens.tolist() == [[V - 1025, -1]]
+    acc, tokens = op(x, d, u, temperature=torch.zeros(1, device="cuda"))
+    assert acc.tolist() == [0] and tokens.tolist() == [[0, -1]]
+
+
+@pytest.mark.gpu
+def test_drawing_takes_no_drafted_tokens():
+    import torch
+    op = DR.DraftVerify(3, 0, 5)
+    x = torch.zeros(3, 5, device="cuda")
+    _, tokens = op(x, None, torch.tensor([[0.1], [0.5], [0.99]], device="cuda"))
+    assert tokens[:, 0].tolist() == [0, 2, 4]
+
+
+@pytest.mark.gpu
 def test_refusals_that_need_a_device(monkeypatch):
     import torch
     from quantized_recurrent_state_packed_amd import linear as LN

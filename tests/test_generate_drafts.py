@@ -102,6 +102,14 @@ def test_a_draft_model_that_is_the_target_is_accepted():
 
 
 @pytest.mark.gpu
+def test_prompts_of_single_tokens():
+    """Nothing to run through before the first round."""
+    target, draft = models(2)
+    sequences, _ = G.DraftGenerator(target, draft, 3, 2).run([[5], [0], [52]], 6)
+    assert [len(s) for s in sequences] == [6] * 3 and all(0 <= t < 53 for s in sequences for t in s)
+
+
+@pytest.mark.gpu
 def test_greedy_sampling_is_the_targets_own_whatever_the_draft():
     target, draft = models(1)
     sequences, _ = G.DraftGenerator(target, draft, 4, 4, temperature=0.0).run(prompts(1), 8)

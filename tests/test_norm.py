@@ -51,7 +51,7 @@ def forward_status(lib, d=None, tokens=2, block=GOOD, bs=100, gate=GOOD, gs=100,
 BAD = [
     (dict(d=ctypes.c_void_p()), 1), (dict(width=0), 1), (dict(heads=0), 1), (dict(dtype=3), 1), (dict(act=2), 1), (dict(act=-1), 1),
     (dict(post=2), 1), (dict(pre=-1), 1), (dict(eps=0.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
-    (dict(eps=-1.0), 1), (dict(tokens=-1), 1), (dict(block=None), 1), (dict(block=GOOD + 1), 1), (dict(dtype=0, gate=GOOD + 2), 1),
+    (dict(eps=-1.0), 1), (dict(eps=1e-40), 1), (dict(tokens=-1), 1), (dict(block=None), 1), (dict(block=GOOD + 1), 1), (dict(dtype=0, gate=GOOD + 2), 1),
     (dict(bs=99), 1), (dict(heads=2), 1), (dict(w1=GOOD + 2), 1), (dict(sc=GOOD + 1), 1), (dict(w2=GOOD + 2), 1),
     (dict(bs=2 ** 41), 1), (dict(width=16385), 2), (dict(tokens=2 ** 31), 2), (dict(tokens=2 ** 30, heads=2), 2),
 ]
@@ -60,7 +60,7 @@ BAD = [
 @pytest.mark.parametrize("bad,status", BAD + [
     (dict(res=GOOD + 1), 1), (dict(rs=5), 1), (dict(out=None, normed=None, pre=0, w2=None), 1), (dict(normed=None), 1),
     (dict(pre=0, w2=None), 1), (dict(pre=0, normed=None), 1), (dict(post=0), 1), (dict(normed=GOOD), 1), (dict(ns=99), 1),
-    (dict(os=99), 1),
+    (dict(os=99), 1), (dict(res=GOOD, out=GOOD, rs=108), 1), (dict(normed=3 * GOOD, gate=3 * GOOD, ns=104), 1),
 ])
 def test_forward_arguments_that_are_refused(lib, bad, status):
     assert forward_status(lib, **bad) == status
@@ -78,7 +78,7 @@ def backward_status(lib, d=None, tokens=2, block=GOOD, bs=100, gate=GOOD, gs=100
     (dict(pre=0), 1), (dict(pre=0, w2=None, d_w2=None), 1), (dict(pre=0, w2=None, d_w2=None, d_normed=None, d_out=None), 1),
     (dict(w1=None), 1), (dict(sc=None), 1), (dict(w2=None), 1), (dict(d_w1=GOOD + 1), 1), (dict(d_block=2 * GOOD), 1),
     (dict(d_res=GOOD), 1), (dict(d_res=2 * GOOD), 1), (dict(ws=None), 1), (dict(ws=GOOD + 8), 1), (dict(nbytes=3 * 400 - 1), 1),
-    (dict(drs=99), 1), (dict(dns=99), 1),
+    (dict(drs=99), 1), (dict(dns=99), 1), (dict(dbs=108), 1), (dict(d_res=5 * GOOD, d_out=5 * GOOD, dos=120), 1),
 ])
 def test_backward_arguments_that_are_refused(lib, bad, status):
     assert backward_status(lib, **bad) == status
