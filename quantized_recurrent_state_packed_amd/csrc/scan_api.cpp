@@ -94,7 +94,8 @@ stepq_status stepq_scan_forward(const stepq_scan_desc* d, int32_t batch, int64_t
   a.decay = decay; a.cu_seqlens = cu_seqlens; a.slot_ids = slot_ids; a.resume = resume; a.state = state;
   a.saved = static_cast<float*>(saved);
   a.total_tokens = total_tokens; a.batch = batch; a.num_slots = num_slots; a.width = d->width; a.rate = d->rate;
-  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch, stepq::kScanPiece));
+  a.piece = stepq::scan_piece(*d, total_tokens, batch, false);
+  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch, a.piece));
   place(a, *d, workspace, w);
   return from_hip(stepq::launch_scan_forward(a, d->dtype, static_cast<hipStream_t>(stream)));
 }
@@ -130,7 +131,8 @@ stepq_status stepq_scan_backward(const stepq_scan_desc* d, int32_t batch, int64_
   a.saved = const_cast<float*>(static_cast<const float*>(saved));
   a.ddecay = ddecay;
   a.total_tokens = total_tokens; a.batch = batch; a.num_slots = num_slots; a.width = d->width; a.rate = d->rate;
-  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch, stepq::kBackPiece));
+  a.piece = stepq::scan_piece(*d, total_tokens, batch, true);
+  a.pieces = static_cast<uint32_t>(stepq::scan_pieces(total_tokens, batch, a.piece));
   if (batch == 0) a.pieces = 0;
   else place(a, *d, workspace, w);
   return from_hip(stepq::launch_scan_backward(a, d->dtype, static_cast<hipStream_t>(stream)));

@@ -18,9 +18,11 @@ namespace stepq {
 // 4 waves 345, of 6 422, of 8 300, of 16 446; 16 tokens of 4 waves 390.
 constexpr int kScanTokens = 32, kScanWaves = 4;
 constexpr int kBackTokens = 8, kBackWaves = 8;
+constexpr int kFewTokens = 8, kFewWaves = 8;
 constexpr int kScanPiece = kScanTokens * kScanWaves;      // tokens of a workgroup
 constexpr int kBackPiece = kBackTokens * kBackWaves;
-static_assert(kScanTokens % kBackTokens == 0);            // a forward pass saves a state every kBackTokens tokens
+constexpr int kFewPiece = kFewTokens * kFewWaves;
+static_assert(kScanTokens % kBackTokens == 0 && kFewTokens % kBackTokens == 0);      // a forward pass saves a state every kBackTokens tokens
 
 struct ScanArgs {
   const void* x;
@@ -57,12 +59,23 @@ struct ScanArgs {
   int32_t blocks;              // workgroups that a piece's channels take
   uint32_t pieces;
   float rate;
+  int32_t piece;               // tokens of a piece
 };
 
 // Pieces of `piece` tokens of all requests together: request b's start at index
 // cu_seqlens[b] / piece + b, so that no table of them is needed.  From b to b + 1 the index grows by
 // at least the ceil((cu[b + 1] - cu[b]) / piece) pieces of request b, and by 1 for an empty one.
 inline int64_t scan_pieces(int64_t total_tokens, int64_t batch, int piece) { return total_tokens / piece + batch; }
+
+// Tokens of a piece.  A forward pass of fewer workgroups than fill the chip takes smaller pieces, of more waves that have fewer
+// tokens each to go through.  us of bfloat16 calls, 128 tokens a piece (32 of 4 waves) against 64 (8 of 8), by workgroups
+// of the former: 37 tokens x 4096 (32) 8.2 : 5.2;  200 x 4096 (64) 12.5 : 10.4;  20000 x 128 (157) 26.2 : 23.8;  700 x 4096 (192)
+// 15.6 : 16.8;  1400 x 4096 (352) 23.7 : 24.8;  2800 x 4096 (704) 36.6 : 38.0;  5 prompts of 3001 x 1001 binary32 (224) 20 : 24.5.
+constexpr int64_t kFewGroups = 160;
+inline int scan_piece(const stepq_scan_desc& d, int64_t total_tokens, int64_t batch, bool backward) {
+  if (backward) return kBackPiece;
+  return scan_pieces(total_tokens, batch, kScanPiece) * ((d.width + 127) / 128) < kFewGroups ? kFewPiece : kScanPiece;
+}
 
 // What a call over requests longer than a piece keeps in its workspace: a ticket (at 0), every
 // piece's map of the state before it to the state behind it, the states behind pieces, each
@@ -73,7 +86,7 @@ struct ScanWorkspace {
 };
 inline ScanWorkspace scan_workspace(const stepq_scan_desc& d, int64_t total_tokens, int64_t batch, bool backward) {
   const auto whole = [](size_t bytes) { return (bytes + 15) / 16 * 16; };
-  const int piece = backward ? kBackPiece : kScanPiece;
+  const int piece = scan_piece(d, total_tokens, batch, backward);
   const size_t n = static_cast<size_t>(scan_pieces(total_tokens, batch, piece)) * d.width;
   const bool linked = total_tokens > piece;      // requests of a piece or less have nothing to hand on
   ScanWorkspace w{};

@@ -348,21 +348,21 @@ __device__ __forceinline__ void load_speeds(const ScanArgs& p, int c, float (&sp
 // waves a compute unit.  One prompt of 32768 x 4096 bfloat16 takes 234 us, 4.6 TB/s (a copy of its bytes 208): 35 vector
 // instructions an element, 5 of them of half rate, are 137 us of all vector units, which the loads hide in part.
 // Two channels a lane where rows allow it, single ones otherwise (3001 x 1001 binary32: 18.6 us).
-template <typename T, int V, bool LINKED>
-__global__ void __launch_bounds__(64 * kScanWaves) k_scan(ScanArgs p) {
-  constexpr int R = kScanTokens, W = kScanWaves;
+template <typename T, int V, bool LINKED, int R, int W>
+__global__ void __launch_bounds__(64 * W) k_scan(ScanArgs p) {
+  constexpr int kPiece = R * W;
   __shared__ Shared<V, W> s;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int block;
   const int64_t index = next_piece<V, W, LINKED>(p, s, 1, block);
-  const Piece q = find<kScanPiece>(p, index);
+  const Piece q = find<kPiece>(p, index);
   const int c = (block * 64 + lane) * V;
   if (q.request < 0) return publish_nothing<V, LINKED>(p, index, w, c);
   const bool mine = c < p.width;
   const uint32_t cc = mine ? c : 0;
   const int slot = slot_of(p, q.request);
-  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kScanPiece + w * R;
-  const int n = max(0, min(R, q.count - q.tile * kScanPiece - w * R));
+  const int64_t t0 = q.first + static_cast<int64_t>(q.tile) * kPiece + w * R;
+  const int n = max(0, min(R, q.count - q.tile * kPiece - w * R));
   float a[R][V], u[R][V], A[V], B[V], h[V], end[V];
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
   const auto read = [&](auto whole) {
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) k_scan(ScanArgs p) {
     for (int v = 0; v < V; ++v) h[v] = fmaf(a[t][v], h[v], u[t][v]);
     if (t < n) y.store(t, h);
   }
-  if (w == W - 1 && slot >= 0 && static_cast<int64_t>(q.tile + 1) * kScanPiece >= q.count)
+  if (w == W - 1 && slot >= 0 && static_cast<int64_t>(q.tile + 1) * kPiece >= q.count)
     for (int v = 0; v < V; ++v) p.state[static_cast<int64_t>(slot) * p.width + c + v] = h[v];
 }
 
@@ -605,11 +605,11 @@ hipError_t over_pieces(ScanArgs a, hipStream_t s) {
   }
   const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(a.pieces) * a.blocks));
   const auto go = [&](auto v, auto l) {
-    constexpr int kThreads = 64 * (BACK ? kBackWaves : kScanWaves);
     constexpr int V = decltype(v)::value;
     constexpr bool LINKED = decltype(l)::value;
-    if (BACK) k_scan_backward<T, V, LINKED><<<grid, kThreads, 0, s>>>(a);
-    else k_scan<T, V, LINKED><<<grid, kThreads, 0, s>>>(a);
+    if (BACK) k_scan_backward<T, V, LINKED><<<grid, 64 * kBackWaves, 0, s>>>(a);
+    else if (a.piece == kFewPiece) k_scan<T, V, LINKED, kFewTokens, kFewWaves><<<grid, 64 * kFewWaves, 0, s>>>(a);
+    else k_scan<T, V, LINKED, kScanTokens, kScanWaves><<<grid, 64 * kScanWaves, 0, s>>>(a);
   };
   const std::integral_constant<int, 1> one{};
   const std::integral_constant<int, 2> pair{};

@@ -60,14 +60,14 @@ void scans(std::mt19937& g) {
     const size_t bytes = stepq_scan_workspace_bytes(&d, batch, total), saved = stepq_scan_saved_bytes(&d, batch, total);
     float* f = static_cast<float*>(any);
     for (int back = 0; back < 2; ++back) {
-      const int piece = back ? stepq::kBackPiece : stepq::kScanPiece;
+      const int piece = stepq::scan_piece(d, total, batch, back == 1);
       const auto call = [&](size_t ws) {
         return back ? stepq_scan_backward(&d, batch, total, static_cast<int32_t*>(any), any, width, any, width, any, width, f, any, saved,
                                           any, width, nullptr, 0, nullptr, nullptr, any, width, any, width, any, width, f, base, ws, nullptr)
                     : stepq_scan_forward(&d, batch, total, static_cast<int32_t*>(any), any, width, any, width, any, width, f, nullptr, 0,
                                          nullptr, nullptr, any, width, any, saved, base, ws, nullptr);
       };
-      CHECK(call(bytes) == STEPQ_OK);
+      CHECK(call(bytes) == STEPQ_OK && scan.piece == piece);
       const size_t n = static_cast<size_t>(scan.pieces) * width;
       const bool linked = scan.ticket != nullptr;
       int64_t longest = 0;
