@@ -12,6 +12,7 @@ import ctypes
 
 from . import stepq as _s
 from .linear import check_current, check_dense, dense, dtype_code, stream_of
+from .recurrence import address
 from .stepq import STEPQ_ERR_INVALID_ARG, STEPQ_ERR_UNSUPPORTED, StepqError
 
 EXPORTED = ("stepq_verify_workspace_bytes", "stepq_verify_drafts")
@@ -43,6 +44,7 @@ class DraftVerify:
         self.batch, self.drafts, self.vocab = int(batch), int(drafts), int(vocab)
         self.dtype = torch.float32 if dtype is None else dtype
         self._code = dtype_code(self.dtype)
+        self._f32, self._i32, self._tensor = torch.float32, torch.int32, torch.Tensor
         null = ctypes.c_void_p()       # an empty call runs the library's own checks of the sizes
         _s._check(lib().stepq_verify_drafts(0, self.drafts, self.vocab, null, self._code, self.vocab, null, 0, null, null, null,
                                             null, null, null, null, 0, null), "DraftVerify")
@@ -59,9 +61,8 @@ class DraftVerify:
 
     def _logits(self, where: str, name: str, t, rows: int) -> int:
         """The stride of [rows, vocab] logits whose rows may be strided."""
-        import torch
         if _s._checks:
-            if not isinstance(t, torch.Tensor) or t.get_device() != self._index or t.dtype is not self.dtype:
+            if not isinstance(t, self._tensor) or t.get_device() != self._index or t.dtype is not self.dtype:
                 raise StepqError(STEPQ_ERR_INVALID_ARG, where, f"{name} must be a {self.dtype} tensor on {self.device}")
             if t.shape != (rows, self.vocab) or (self.vocab > 1 and t.stride(1) != 1):
                 raise StepqError(STEPQ_ERR_INVALID_ARG, where, f"{name} must be [{rows}, {self.vocab}] with rows in one piece "
@@ -74,21 +75,20 @@ class DraftVerify:
         draft was certain of its tokens), num_drafts [batch] (None: all) and temperature [batch]
         (None: 1).  Returns (accepted [batch], tokens [batch, drafts + 1]).  draft_tokens may be None
         where drafts is 0."""
-        import torch
         where, b, k, i = "stepq_verify_drafts", self.batch, self.drafts, self._index
         stride = self._logits(where, "logits", logits, b * (k + 1))
         draft_stride = 0 if draft_logits is None or k == 0 else self._logits(where, "draft_logits", draft_logits, b * k)
         if _s._checks:
-            if (k > 0 or draft_tokens is not None) and not dense(draft_tokens, torch.int32, (b, k), i) or i < 0:
-                check_dense(where, "draft_tokens", draft_tokens, (b, k), torch.int32, self.device)
-            if not dense(uniforms, torch.float32, (b, k + 1), i):
-                check_dense(where, "uniforms", uniforms, (b, k + 1), torch.float32, self.device)
-            if num_drafts is not None and not dense(num_drafts, torch.int32, (b,), i):
-                check_dense(where, "num_drafts", num_drafts, (b,), torch.int32, self.device)
-            if temperature is not None and not dense(temperature, torch.float32, (b,), i):
-                check_dense(where, "temperature", temperature, (b,), torch.float32, self.device)
+            if (k > 0 or draft_tokens is not None) and not dense(draft_tokens, self._i32, (b, k), i) or i < 0:
+                check_dense(where, "draft_tokens", draft_tokens, (b, k), self._i32, self.device)
+            if not dense(uniforms, self._f32, (b, k + 1), i):
+                check_dense(where, "uniforms", uniforms, (b, k + 1), self._f32, self.device)
+            if num_drafts is not None and not dense(num_drafts, self._i32, (b,), i):
+                check_dense(where, "num_drafts", num_drafts, (b,), self._i32, self.device)
+            if temperature is not None and not dense(temperature, self._f32, (b,), i):
+                check_dense(where, "temperature", temperature, (b,), self._f32, self.device)
             check_current(where, i)
-        p = _s._ptr
+        p = address
         _s._check(lib().stepq_verify_drafts(b, k, self.vocab, p(logits), self._code, stride,
                                             p(draft_logits) if k else None, draft_stride, p(draft_tokens) if k else None,
                                             p(num_drafts), p(temperature), p(uniforms), p(self.accepted), p(self.tokens),

@@ -12,6 +12,7 @@ import ctypes
 
 from . import stepq as _s
 from .linear import _refuse, check_current, check_dense, dense, dtype_code, leading, stream_of
+from .recurrence import address
 from .stepq import STEPQ_ERR_UNSUPPORTED, StepqError
 
 EXPORTED = ("stepq_norm_forward", "stepq_norm_workspace_bytes", "stepq_norm_backward")
@@ -56,6 +57,7 @@ class BlockNorm:
             _refuse("BlockNorm", f"unknown activation {activation!r}; known: {sorted(_ACTIVATIONS)}")
         self.width, self.heads, self.post, self.pre = int(width), int(heads), bool(post), bool(pre)
         self.dtype = torch.float32 if dtype is None else dtype
+        self._f32, self._tensor = torch.float32, torch.Tensor
         self.desc = stepq_norm_desc(self.width, self.heads, dtype_code(self.dtype), _ACTIVATIONS[activation], int(self.post),
                                     int(self.pre), float(eps))
         self._desc = ctypes.addressof(self.desc)
@@ -75,14 +77,11 @@ class BlockNorm:
 
     def _rows(self, where: str, name: str, t, tokens: int, index: int) -> int:
         """The stride of a [tokens, heads * width] tensor whose tokens may be strided; 0 for None."""
-        import torch
         if t is None:
             return 0
         if not _s._checks:
             return t.stride(0) if tokens > 1 else self._row
-        if dense(t, self.dtype, (tokens, self._row), index):
-            return self._row
-        if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype is not self.dtype:
+        if not isinstance(t, self._tensor) or t.get_device() != index or t.dtype is not self.dtype:
             _refuse(where, f"{name} must be a {self.dtype} tensor on cuda:{max(index, 0)}")
         if t.shape != (tokens, self._row):
             _refuse(where, f"{name} must have shape {[tokens, self._row]} (got {list(t.shape)})")
@@ -94,18 +93,15 @@ class BlockNorm:
         return n
 
     def _device(self, where: str, block) -> int:
-        import torch
-        if not isinstance(block, torch.Tensor) or not block.is_cuda:
+        if not isinstance(block, self._tensor) or not block.is_cuda:
             _refuse(where, "block must be a device tensor")
         return block.get_device()
 
     def _weights(self, where: str, index: int, weights) -> None:
-        import torch
-        if not _s._checks:
-            return
         for name, w in weights:
-            if w is not None and not dense(w, torch.float32, (self.width,), index):
-                check_dense(where, name, w, (self.width,), torch.float32, torch.device("cuda", index))
+            if w is not None and not dense(w, self._f32, (self.width,), index):
+                import torch
+                check_dense(where, name, w, (self.width,), self._f32, torch.device("cuda", index))
 
     def forward(self, block, out, normed=None, gate=None, residual=None, post_weight=None, scale=None, pre_weight=None,
                 stream=None) -> None:
@@ -114,16 +110,17 @@ class BlockNorm:
         where = "stepq_norm_forward"
         tokens = leading(where, "block", block)
         i = self._device(where, block)
-        bs, os_, ns, gs, rs = (self._rows(where, name, t, tokens, i) for name, t in (
-            ("block", block), ("out", out), ("normed", normed), ("gate", gate), ("residual", residual)))
-        self._weights(where, i, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)))
+        rows = self._rows
+        bs, os_, ns = rows(where, "block", block, tokens, i), rows(where, "out", out, tokens, i), rows(where, "normed", normed, tokens, i)
+        gs, rs = rows(where, "gate", gate, tokens, i), rows(where, "residual", residual, tokens, i)
         if _s._checks:
+            self._weights(where, i, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)))
             if (normed is not None) != self.pre or (out is None and not self.pre):
                 _refuse(where, "normed belongs to a norm before the next block, and out is needed where there is none")
             check_current(where, i)
         if tokens == 0:
             return
-        p = _s._ptr
+        p = address
         _s._check(lib().stepq_norm_forward(self._desc, tokens, p(block), bs, p(gate), gs, p(residual), rs, p(post_weight),
                                            p(scale), p(pre_weight), p(out), os_, p(normed), ns, stream_of(stream, i)), where)
 
@@ -140,9 +137,9 @@ class BlockNorm:
         named = (("block", block), ("gate", gate), ("out", out if self.pre else None), ("d_out", d_out), ("d_normed", d_normed),
                  ("d_block", d_block), ("d_gate", d_gate), ("d_residual", d_residual))
         bs, gs, os_, dos, dns, dbs, dgs, drs = (self._rows(where, name, t, tokens, i) for name, t in named)
-        self._weights(where, i, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight),
-                                 ("d_post_weight", d_post_weight), ("d_scale", d_scale), ("d_pre_weight", d_pre_weight)))
         if _s._checks:
+            self._weights(where, i, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight),
+                                     ("d_post_weight", d_post_weight), ("d_scale", d_scale), ("d_pre_weight", d_pre_weight)))
             if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and
                                               workspace.get_device() == i and workspace.dim() == 1 and
                                               workspace.is_contiguous()):
@@ -152,7 +149,7 @@ class BlockNorm:
             if stream is not None:
                 _refuse(where, "a call on another stream needs a workspace of its own")
             workspace = self.workspace(tokens, block.device)
-        p = _s._ptr
+        p = address
         ptrs = [p(t) for _, t in named]
         (bp, gp, op, dop, dnp, dbp, dgp, drp) = ptrs
         _s._check(lib().stepq_norm_backward(self._desc, tokens, bp, bs, gp, gs, op, os_, p(post_weight), p(scale), p(pre_weight),

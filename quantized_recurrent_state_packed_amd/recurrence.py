@@ -24,6 +24,11 @@ class stepq_scan_desc(ctypes.Structure):
 _lib = None
 
 
+def address(t):
+    """What the library takes for a tensor that has been checked, or for None."""
+    return None if t is None else t.data_ptr()
+
+
 def lib() -> ctypes.CDLL:
     global _lib
     if _lib is None:
@@ -52,6 +57,7 @@ class GatedRecurrence:
         import torch
         self.width, self.rate = int(width), float(rate)
         self.dtype = torch.float32 if dtype is None else dtype
+        self._f32, self._i32, self._u8, self._tensor = torch.float32, torch.int32, torch.uint8, torch.Tensor
         self.desc = stepq_scan_desc(self.width, dtype_code(self.dtype), self.rate)
         self._desc = ctypes.addressof(self.desc)
         # an empty call runs the library's own checks of the description
@@ -84,8 +90,7 @@ class GatedRecurrence:
 
     def _rows(self, where: str, name: str, t, tokens: int, index: int) -> int:
         """Checks a [tokens, width] tensor whose tokens may be strided; returns that stride."""
-        import torch
-        if not isinstance(t, torch.Tensor) or t.get_device() != index or index < 0 or t.dtype is not self.dtype:
+        if not isinstance(t, self._tensor) or t.get_device() != index or index < 0 or t.dtype is not self.dtype:
             _refuse(where, f"{name} must be a {self.dtype} tensor on cuda:{max(index, 0)}")
         if t.shape != (tokens, self.width):
             _refuse(where, f"{name} must have shape {[tokens, self.width]} (got {list(t.shape)})")
@@ -96,16 +101,18 @@ class GatedRecurrence:
             _refuse(where, f"{name}'s channels must lie side by side and its tokens must not overlap (strides {list(t.stride())})")
         return n
 
-    def _slots(self, where, slot_ids, state, resume, batch, index):
+    def _place(self, index: int):
         import torch
+        return torch.device("cuda", index) if index >= 0 else None
+
+    def _slots(self, where, slot_ids, state, resume, batch, index):
         if (slot_ids is None) != (state is None):
             _refuse(where, "slot_ids and states belong together")
         if state is not None:
-            dev = torch.device("cuda", index) if index >= 0 else None
-            if not dense(slot_ids, torch.int32, (batch,), index):
-                check_dense(where, "slot_ids", slot_ids, (batch,), torch.int32, dev)
-            if not dense(state, torch.float32, (leading(where, "state", state), self.width), index):
-                check_dense(where, "state", state, (None, self.width), torch.float32, dev)
+            if not dense(slot_ids, self._i32, (batch,), index):
+                check_dense(where, "slot_ids", slot_ids, (batch,), self._i32, self._place(index))
+            if not dense(state, self._f32, (leading(where, "state", state), self.width), index):
+                check_dense(where, "state", state, (None, self.width), self._f32, self._place(index))
             if state.shape[0] < 1:
                 _refuse(where, "there are no states")
         elif resume is not None:
@@ -113,25 +120,21 @@ class GatedRecurrence:
 
     def _common(self, where, cu_seqlens, rows, decay, slot_ids, state, resume, workspace):
         """Checks what the two passes over prompts have in common; (batch, tokens, device index, strides)."""
-        import torch
         batch, tokens = leading(where, "cu_seqlens", cu_seqlens) - 1, leading(where, "x", rows[0][1])
         if not _s._checks:
             return batch, tokens, decay.get_device(), [t.stride(0) if tokens > 1 else self.width for _, t in rows]
-        index = decay.get_device() if isinstance(decay, torch.Tensor) else -1
-        dev = decay.device if index >= 0 else None
-        if index < 0 or not dense(decay, torch.float32, (self.width,), index):
-            check_dense(where, "decay", decay, (self.width,), torch.float32, dev)
-        if batch < 0 or not dense(cu_seqlens, torch.int32, (batch + 1,), index):
-            check_dense(where, "cu_seqlens", cu_seqlens, (None,), torch.int32, dev)
+        index = decay.get_device() if isinstance(decay, self._tensor) else -1
+        if index < 0 or not dense(decay, self._f32, (self.width,), index):
+            check_dense(where, "decay", decay, (self.width,), self._f32, self._place(index))
+        if batch < 0 or not dense(cu_seqlens, self._i32, (batch + 1,), index):
+            check_dense(where, "cu_seqlens", cu_seqlens, (None,), self._i32, self._place(index))
             _refuse(where, "cu_seqlens must have an entry more than there are requests")
         strides = [self._rows(where, name, t, tokens, index) for name, t in rows]
         self._slots(where, slot_ids, state, resume, batch, index)
-        if resume is not None and not dense(resume, torch.uint8, (batch,), index):
-            check_dense(where, "resume", resume, (batch,), torch.uint8, dev)
-        if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and
-                                          workspace.get_device() == index and workspace.dim() == 1 and
-                                          workspace.is_contiguous()):
-            check_dense(where, "workspace", workspace, (None,), torch.uint8, dev)
+        if resume is not None and not dense(resume, self._u8, (batch,), index):
+            check_dense(where, "resume", resume, (batch,), self._u8, self._place(index))
+        if workspace is not None:
+            self._buffer(where, "workspace", workspace, index)
         check_current(where, index)
         return batch, tokens, index, strides
 
@@ -142,11 +145,10 @@ class GatedRecurrence:
             workspace = self.workspace(batch, tokens, device)
         return workspace
 
-    def _check_saved(self, where, saved, index):
-        import torch
-        if _s._checks and not (isinstance(saved, torch.Tensor) and saved.dtype is torch.uint8 and saved.dim() == 1 and
-                               saved.get_device() == index and saved.is_contiguous()):
-            check_dense(where, "saved", saved, (None,), torch.uint8, torch.device("cuda", index))
+    def _buffer(self, where, name, t, index):
+        if not (isinstance(t, self._tensor) and t.dtype is self._u8 and t.get_device() == index and t.dim() == 1 and
+                t.is_contiguous()):
+            check_dense(where, name, t, (None,), self._u8, self._place(index))
 
     def prefill(self, cu_seqlens, x, gate_a, gate_x, decay, slot_ids, state, y, resume=None, saved=None, workspace=None,
                 stream=None) -> None:
@@ -159,15 +161,15 @@ class GatedRecurrence:
         batch, tokens, i, (xs, as_, gs, ys) = self._common(
             where, cu_seqlens, (("x", x), ("gate_a", gate_a), ("gate_x", gate_x), ("y", y)), decay, slot_ids, state, resume,
             workspace)
-        if saved is not None:
-            self._check_saved(where, saved, i)
+        if saved is not None and _s._checks:
+            self._buffer(where, "saved", saved, i)
         if batch == 0:
             return
         workspace = self._workspace(where, workspace, batch, tokens, stream, decay.device)
         if tokens == 0:          # empty tensors have no address; every request is empty
             x = gate_a = gate_x = y = decay
             xs = as_ = gs = ys = self.width
-        p = _s._ptr
+        p = address
         _s._check(lib().stepq_scan_forward(self._desc, batch, tokens, p(cu_seqlens), p(x), xs, p(gate_a), as_, p(gate_x), gs,
                                            p(decay), p(slot_ids), 0 if state is None else state.shape[0], p(resume), p(state),
                                            p(y), ys, p(saved), 0 if saved is None else saved.numel(), p(workspace),
@@ -178,19 +180,19 @@ class GatedRecurrence:
         """stepq_scan_backward: from dy, and from the gradients of the states that requests end
         with in the slots of dstate, those of x, the gates and decay, and in the slots of dstate
         those of the states that requests start from."""
-        import torch
         where = "stepq_scan_backward"
         rows = (("x", x), ("gate_a", gate_a), ("gate_x", gate_x), ("dy", dy), ("dx", dx), ("dgate_a", dgate_a),
                 ("dgate_x", dgate_x))
         batch, tokens, i, strides = self._common(where, cu_seqlens, rows, decay, slot_ids, dstate, resume, workspace)
-        self._check_saved(where, saved, i)
-        if _s._checks and not dense(ddecay, torch.float32, (self.width,), i):
-            check_dense(where, "ddecay", ddecay, (self.width,), torch.float32, decay.device)
+        if _s._checks:
+            self._buffer(where, "saved", saved, i)
+            if not dense(ddecay, self._f32, (self.width,), i):
+                check_dense(where, "ddecay", ddecay, (self.width,), self._f32, decay.device)
         workspace = self._workspace(where, workspace, batch, tokens, stream, decay.device)
-        ptrs = [_s._ptr(t) for _, t in rows]
+        p = address
+        ptrs = [p(t) for _, t in rows]
         if tokens == 0:
-            ptrs, strides = [_s._ptr(decay)] * 7, [self.width] * 7
-        p = _s._ptr
+            ptrs, strides = [p(decay)] * 7, [self.width] * 7
         (xp, ap, gp, dyp, dxp, dap, dgp), (xs, as_, gs, dys, dxs, das, dgs) = ptrs, strides
         _s._check(lib().stepq_scan_backward(self._desc, batch, tokens, p(cu_seqlens), xp, xs, ap, as_, gp, gs, p(decay),
                                             p(saved), saved.numel(), dyp, dys, p(slot_ids),
@@ -200,23 +202,21 @@ class GatedRecurrence:
 
     def step(self, slot_ids, x, gate_a, gate_x, decay, state, y, stream=None) -> None:
         """stepq_scan_step: one token of every request, updating the slots of state."""
-        import torch
         where = "stepq_scan_step"
         batch = leading(where, "slot_ids", slot_ids)
-        rows = (x, gate_a, gate_x, y)
         if _s._checks:
-            i = decay.get_device() if isinstance(decay, torch.Tensor) else -1
-            if i < 0 or not dense(decay, torch.float32, (self.width,), i):
-                check_dense(where, "decay", decay, (self.width,), torch.float32, decay.device if i >= 0 else None)
-            strides = [self.width if dense(t, self.dtype, (batch, self.width), i) else self._rows(where, name, t, batch, i)
-                       for name, t in zip(("x", "gate_a", "gate_x", "y"), rows)]
+            i = decay.get_device() if isinstance(decay, self._tensor) else -1
+            if i < 0 or not dense(decay, self._f32, (self.width,), i):
+                check_dense(where, "decay", decay, (self.width,), self._f32, self._place(i))
+            strides = (self._rows(where, "x", x, batch, i), self._rows(where, "gate_a", gate_a, batch, i),
+                       self._rows(where, "gate_x", gate_x, batch, i), self._rows(where, "y", y, batch, i))
             if state is None or slot_ids is None:
                 _refuse(where, "a step needs states")
             self._slots(where, slot_ids, state, None, batch, i)
             check_current(where, i)
         else:
-            strides = [t.stride(0) if batch > 1 else self.width for t in rows]
-        p = _s._ptr
-        (xs, as_, gs, ys) = strides
+            strides = [t.stride(0) if batch > 1 else self.width for t in (x, gate_a, gate_x, y)]
+        p = address
+        xs, as_, gs, ys = strides
         _s._check(lib().stepq_scan_step(self._desc, batch, p(slot_ids), state.shape[0], p(x), xs, p(gate_a), as_, p(gate_x),
                                         gs, p(decay), p(state), p(y), ys, stream_of(stream, decay.get_device())), where)
