@@ -429,7 +429,7 @@ def test_a_value_that_is_not_finite_spoils_its_own_request_and_channel_alone():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("batch,width,pad", [(1, 1, 0), (5, 130, 0), (3, 1001, 1), (512, 64, 2)])
+@pytest.mark.parametrize("batch,width,pad", [(1, 1, 0), (5, 130, 0), (3, 1001, 1), (512, 64, 2), (4099, 64, 0)])
 def test_single_tokens(dtype, batch, width, pad):
     import torch
     c = Case([1] * batch, width, dtype, pad=pad, lead=0, tail=0, bad=((batch - 1, -3),) if batch > 2 else ())
