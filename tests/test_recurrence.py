@@ -292,7 +292,8 @@ class Case:
 
 
 LENGTHS = {"one": [1], "short": [37], "piece": [PIECE], "piece+1": [PIECE + 1], "half": [PIECE // 2],
-           "half+1": [PIECE // 2 + 1], "ragged": [3, 0, 1, 130, 64, 65, 7, 0], "long": [1500], "many": [1, 2, 0, 9, 8, 7] * 23, "two long": [700, 513]}
+           "half+1": [PIECE // 2 + 1], "ragged": [3, 0, 1, 130, 64, 65, 7, 0], "long": [1500],
+           "many": [1, 2, 0, 9, 8, 7] * 23, "two long": [700, 513], "sparse": [1, 0, 0, 2] * 30, "sparser": [0, 1, 0, 0] * 40}
 
 
 @pytest.mark.gpu
