@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kThreads) k_verify_scan(VerifyArgs p) {
     } else {
       float most = m;
       for (int s = 1; s < 64; s <<= 1) most = fmaxf(most, __shfl_xor(most, s));
-      sum = m == -kInf ? 0.0 : most == kInf ? (m == kInf ? sum : 0.0) : sum * power((static_cast<double>(m) - static_cast<double>(most)) * q.c);
+      if (m == -kInf || (most == kInf && m < kInf)) sum = 0.0;
+      else if (most < kInf) sum *= power((static_cast<double>(m) - static_cast<double>(most)) * q.c);
       for (int s = 1; s < 64; s <<= 1) sum += across(sum, s);
       m = most;
     }

@@ -6,10 +6,11 @@
 //
 // A run of tokens is an affine map of the state before it, h -> A h + B, and maps
 // of neighbouring runs compose.  A wave holds some tokens of 64 V channels in registers,
-// the waves of a workgroup follow each other in time and make up a piece.  Each wave works out its map, the maps meet in LDS, states are handed on from piece to
-// piece (hand_on), and every wave walks its tokens from the state that it starts from.  So
-// every tensor is read or written once, whatever a request's length, and one long request
-// spreads over the chip like many short ones.
+// the waves of a workgroup follow each other in time and make up a piece.  Each wave works
+// out its map, the maps meet in LDS, states are handed on from piece to piece (hand_on), and
+// every wave walks its tokens from the state that it starts from.  So every tensor is read or
+// written once, whatever a request's length, and one long request spreads over the chip
+// like many short ones.
 //
 // Backward, with c_t = a_{t+1} g_{t+1} what comes from the tokens behind (the final
 // state's gradient for the last one), g_t = dy_t + c_t:
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(64 * W) k_scan(ScanArgs p) {
   if (!mine) return;
   // as find() does for pieces: the states before every kBackTokens tokens
   const Rows<T, V> y(p.y, p.y_stride, t0, cc);
-  float* saved = p.saved == nullptr ? nullptr : p.saved + (q.first / kBackTokens + q.request + (q.tile * W + w) * (R / kBackTokens)) * p.width + cc;
+  const int64_t saved0 = q.first / kBackTokens + q.request + (q.tile * W + w) * (R / kBackTokens);
+  float* saved = p.saved == nullptr ? nullptr : p.saved + saved0 * p.width + cc;
   for (int t = 0; t < R; ++t) {
     if (t % kBackTokens == 0 && t < n && saved != nullptr)
       for (int v = 0; v < V; ++v) saved[t / kBackTokens * static_cast<int64_t>(p.width) + v] = h[v];
