@@ -388,7 +388,7 @@ void launch(const NormArgs& a, int dtype, hipStream_t s) {
   const auto go = [&](auto lanes, auto pieces) {
     constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value;
     if (n.lanes != L || n.pieces != P) return;
-    if (BACK) k_norm_backward<T, IN16, L, P><<<grid, threads_of(L), 0, s>>>(a);
+    if constexpr (BACK) k_norm_backward<T, IN16, L, P><<<grid, threads_of(L), 0, s>>>(a);
     else k_norm<T, IN16, L, P><<<grid, threads_of(L), 0, s>>>(a);
   };
   const std::integral_constant<int, 1> one{};

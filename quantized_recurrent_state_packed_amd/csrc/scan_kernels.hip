@@ -37,8 +37,6 @@ template <>
 struct Word<2> { typedef uint16_t type; };
 template <>
 struct Word<4> { typedef uint32_t type; };
-template <>
-struct Word<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
 
 template <typename T, int V>
 struct Vec {
@@ -46,8 +44,7 @@ struct Vec {
   Raw raw;
   __device__ __forceinline__ float operator[](int v) const {
     if constexpr (sizeof(T) == 4) {
-      if constexpr (V == 1) return __builtin_bit_cast(float, raw);
-      else return __builtin_bit_cast(float, static_cast<uint32_t>(raw[v]));
+      return __builtin_bit_cast(float, raw);
     } else if constexpr (std::is_same<T, __bf16>::value) {
       if constexpr (V == 1) return __builtin_bit_cast(float, static_cast<uint32_t>(raw) << 16);
       else return __builtin_bit_cast(float, v ? raw & 0xffff0000u : raw << 16);
@@ -366,18 +363,21 @@ __global__ void __launch_bounds__(64 * W) k_scan(ScanArgs p) {
   const int n = max(0, min(R, q.count - q.tile * kPiece - w * R));
   float a[R][V], u[R][V], A[V], B[V], h[V], end[V];
   for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+  // every loop over tokens has to be unrolled, or what it fills is not in registers
   const auto read = [&](auto whole) {
     constexpr bool WHOLE = decltype(whole)::value;
     float speed[V];
     load_speeds<V, LINKED>(p, cc, speed);
     Vec<T, V> xr[R], gr[R], ir[R];
     const Rows<T, V> x(p.x, p.x_stride, t0, cc), ga(p.ga, p.ga_stride, t0, cc), gx(p.gx, p.gx_stride, t0, cc);
+#pragma unroll
     for (int t = 0; t < R; ++t) {                 // rows behind the last one are read as it
       const int row = WHOLE ? t : min(t, n - 1);
       xr[t] = x.load(row);
       gr[t] = ga.load(row);
       ir[t] = gx.load(row);
     }
+#pragma unroll
     for (int t = 0; t < R; ++t)
       for (int v = 0; v < V; ++v) {
         const float less = one_less_exp2(speed[v] * logistic(gr[t][v]));
@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(64 * W) k_scan(ScanArgs p) {
   if (n == R) {
     read(std::true_type{});
   } else {
+#pragma unroll
     for (int t = 0; t < R; ++t)
       for (int v = 0; v < V; ++v) a[t][v] = 1.0f, u[t][v] = 0.0f;
     if (n > 0) read(std::false_type{});
@@ -404,6 +405,7 @@ __global__ void __launch_bounds__(64 * W) k_scan(ScanArgs p) {
   const Rows<T, V> y(p.y, p.y_stride, t0, cc);
   const int64_t saved0 = q.first / kBackTokens + q.request + (q.tile * W + w) * (R / kBackTokens);
   float* saved = p.saved == nullptr ? nullptr : p.saved + saved0 * p.width + cc;
+#pragma unroll
   for (int t = 0; t < R; ++t) {
     if (t % kBackTokens == 0 && t < n && saved != nullptr)
       for (int v = 0; v < V; ++v) saved[t / kBackTokens * static_cast<int64_t>(p.width) + v] = h[v];
@@ -450,16 +452,19 @@ __global__ void __launch_bounds__(64 * kBackWaves, 4) k_scan_backward(ScanArgs p
     const Rows<T, V> x(p.x, p.x_stride, t0, cc), ga(p.ga, p.ga_stride, t0, cc), gx(p.gx, p.gx_stride, t0, cc);
     const Rows<T, V> dy(p.dy, p.dy_stride, t0, cc);
     // in the order of their use; rows behind the last one are read as it
+#pragma unroll
     for (int t = R - 1; t >= 0; --t) {
       const int row = WHOLE ? t : min(t, n - 1);
       ar[t] = ga.load(row);
       gr[t] = dy.load(row);
     }
+#pragma unroll
     for (int t = 0; t < R; ++t) {
       const int row = WHOLE ? t : min(t, n - 1);
       xr[t] = x.load(row);
       ir[t] = gx.load(row);
     }
+#pragma unroll
     for (int t = R - 1; t >= 0; --t)
       for (int v = 0; v < V; ++v) {
         less[t][v] = one_less_exp2(speed[v] * logistic(ar[t][v]));
@@ -483,6 +488,7 @@ __global__ void __launch_bounds__(64 * kBackWaves, 4) k_scan_backward(ScanArgs p
       h[v] = p.saved[(q.first / R + q.request + q.tile * W + back) * p.width + cc + v];
       slow[v] = speed[v] * kLog2;
     }
+#pragma unroll
     for (int t = 0; t < R; ++t) {
       for (int v = 0; v < V; ++v) {
         const float a = 1.0f - less[t][v];
@@ -491,6 +497,7 @@ __global__ void __launch_bounds__(64 * kBackWaves, 4) k_scan_backward(ScanArgs p
       }
       again(ir[t]), again(xr[t]);
     }
+#pragma unroll
     for (int t = R - 1; t >= 0; --t) {
       if (!WHOLE && t >= n) continue;
       float ox[V], oa[V], oi[V];
@@ -590,12 +597,13 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanArgs p, int rows) {
   }
 }
 
-// Two channels a lane where every pair lies on a boundary of its size.
+// Two channels a lane where values have 16 bits and every pair lies on a boundary of its size.  Binary32 pairs take twice the
+// registers for what is read: 18391 tokens x 1408, us of forward and backward, 102 and 215 in pairs, 103 and 164 one by one.
 bool in_pairs(const ScanArgs& a, int esize) {
   const auto pair = [&](const void* p, int64_t stride) {
     return reinterpret_cast<uintptr_t>(p) % (2 * esize) == 0 && stride % 2 == 0;
   };
-  return a.width % 2 == 0 && pair(a.x, a.x_stride) && pair(a.ga, a.ga_stride) && pair(a.gx, a.gx_stride) &&
+  return esize == 2 && a.width % 2 == 0 && pair(a.x, a.x_stride) && pair(a.ga, a.ga_stride) && pair(a.gx, a.gx_stride) &&
          pair(a.y, a.y_stride) && pair(a.dy, a.dy_stride) && pair(a.dga, a.dga_stride) && pair(a.dgx, a.dgx_stride);
 }
 
@@ -614,14 +622,18 @@ hipError_t over_pieces(ScanArgs a, hipStream_t s) {
   const auto go = [&](auto v, auto l) {
     constexpr int V = decltype(v)::value;
     constexpr bool LINKED = decltype(l)::value;
-    if (BACK) k_scan_backward<T, V, LINKED><<<grid, 64 * kBackWaves, 0, s>>>(a);
-    else if (a.piece == kFewPiece) k_scan<T, V, LINKED, kFewTokens, kFewWaves><<<grid, 64 * kFewWaves, 0, s>>>(a);
-    else k_scan<T, V, LINKED, kScanTokens, kScanWaves><<<grid, 64 * kScanWaves, 0, s>>>(a);
+    if constexpr (BACK) {
+      k_scan_backward<T, V, LINKED><<<grid, 64 * kBackWaves, 0, s>>>(a);
+    } else if (a.piece == kFewPiece) {
+      k_scan<T, V, LINKED, kFewTokens, kFewWaves><<<grid, 64 * kFewWaves, 0, s>>>(a);
+    } else {
+      k_scan<T, V, LINKED, kScanTokens, kScanWaves><<<grid, 64 * kScanWaves, 0, s>>>(a);
+    }
   };
   const std::integral_constant<int, 1> one{};
   const std::integral_constant<int, 2> pair{};
-  if (two) linked ? go(pair, std::true_type{}) : go(pair, std::false_type{});
-  else linked ? go(one, std::true_type{}) : go(one, std::false_type{});
+  if (!two) linked ? go(one, std::true_type{}) : go(one, std::false_type{});
+  else if constexpr (sizeof(T) == 2) linked ? go(pair, std::true_type{}) : go(pair, std::false_type{});
   return hipGetLastError();
 }
 
@@ -646,8 +658,8 @@ hipError_t step(const ScanArgs& a, hipStream_t s) {
   // 6144 workgroups of a request each 12.5 us, of 2 requests 11.1, of 4 10.4, of 8 11.6
   const int rows = groups * a.batch >= 4096 ? 4 : 1;
   const dim3 grid(static_cast<uint32_t>((a.batch + rows - 1) / rows * groups));
-  if (two) k_scan_step<T, 2><<<grid, 256, 0, s>>>(a, rows);
-  else k_scan_step<T, 1><<<grid, 256, 0, s>>>(a, rows);
+  if (!two) k_scan_step<T, 1><<<grid, 256, 0, s>>>(a, rows);
+  else if constexpr (sizeof(T) == 2) k_scan_step<T, 2><<<grid, 256, 0, s>>>(a, rows);
   return hipGetLastError();
 }
 
