@@ -345,7 +345,7 @@ __device__ __forceinline__ void load_speeds(const ScanArgs& p, int c, float (&sp
 // One workgroup takes a piece of a request, 64 V channels of it: 96 loads of 4 bytes a lane are under way at once, 12
 // waves a compute unit.  One prompt of 32768 x 4096 bfloat16 takes 234 us, 4.6 TB/s (a copy of its bytes 208): 35 vector
 // instructions an element, 5 of them of half rate, are 137 us of all vector units, which the loads hide in part.
-// Two channels a lane where rows allow it, single ones otherwise (3001 x 1001 binary32: 18.6 us).
+// Two channels a lane where 16-bit rows allow it, single ones otherwise (3001 x 1001 binary32: 18.6 us).
 template <typename T, int V, bool LINKED, int R, int W>
 __global__ void __launch_bounds__(64 * W) k_scan(ScanArgs p) {
   constexpr int kPiece = R * W;
