@@ -167,12 +167,28 @@ __device__ __forceinline__ void load_weight(float (&w)[P][kVec<T>], const float*
 constexpr int threads_of(int L) { return L < kNormThreads ? kNormThreads : L; }
 constexpr int at_once(int L) { return threads_of(L) / L; }
 
-// The pieces of a row that a lane holds.
+// What of a row a group of L lanes reads: nothing behind the last row, since another group may be writing an output
+// where its inputs were.  A workgroup of one group has a row whenever it looks for one.
+template <int L>
+__device__ __forceinline__ int width_of(int64_t row, const NormArgs& p) {
+  if constexpr (at_once(L) == 1) return p.width;
+  const int width = row < p.rows ? p.width : 0;
+  return L >= 64 ? __builtin_amdgcn_readfirstlane(width) : width;
+}
+
+// to + a b where the group has a row.  Behind the last one a product may be NaN, by a weight that is infinite.
+template <int L>
+__device__ __forceinline__ float added(bool real, float a, float b, float to) {
+  if constexpr (at_once(L) == 1) return fmaf(real ? a : 0.0f, b, to);
+  else return real ? fmaf(a, b, to) : to;
+}
+
+// The pieces of a row of `width` values that a lane holds.
 template <typename T, bool IN16, int L, int P>
-__device__ __forceinline__ void load_row(const NormRows& r, int row, const NormArgs& p, int lane, Piece<T> (&x)[P]) {
+__device__ __forceinline__ void load_row(const NormRows& r, int row, const NormArgs& p, int lane, int width, Piece<T> (&x)[P]) {
   if (r.p == nullptr) return;
   const T* at = row_of<T>(r, row, p.heads, p.width);
-  for (int j = 0; j < P; ++j) x[j] = load<T, IN16>(at, (j * L + lane) * kVec<T>, p.width);
+  for (int j = 0; j < P; ++j) x[j] = load<T, IN16>(at, (j * L + lane) * kVec<T>, width);
 }
 
 // Bound by memory: 8192 tokens of 4096 bfloat16 values, all parts, take 65 us, 5.2 TB/s, 8192 x 48 gated rows of 128 57.6,
@@ -190,11 +206,12 @@ __global__ void __launch_bounds__(threads_of(L)) k_norm(NormArgs p) {
   load_weight<T, P>(w2, p.pre_weight, lane, L, p.width);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kAtOnce, first0 = static_cast<int64_t>(blockIdx.x) * kAtOnce;
   Piece<T> o[P], z[P], x[P];
-  const auto read = [&](int64_t first) {        // groups behind the last row read it
+  const auto read = [&](int64_t first) {
     const int row = static_cast<int>(first + group < p.rows ? first + group : p.rows - 1);
-    load_row<T, IN16, L, P>(p.block, row, p, lane, o);
-    load_row<T, IN16, L, P>(p.gate, row, p, lane, z);
-    load_row<T, IN16, L, P>(p.residual, row, p, lane, x);
+    const int width = width_of<L>(first + group, p);
+    load_row<T, IN16, L, P>(p.block, row, p, lane, width, o);
+    load_row<T, IN16, L, P>(p.gate, row, p, lane, width, z);
+    load_row<T, IN16, L, P>(p.residual, row, p, lane, width, x);
   };
   if (first0 < p.rows) read(first0);
   for (int64_t first = first0; first < p.rows; first += step) {
@@ -257,13 +274,14 @@ __global__ void __launch_bounds__(threads_of(L)) k_norm_backward(NormArgs p) {
     for (int i = 0; i < V; ++i) d1[j][i] = ds[j][i] = d2[j][i] = 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kAtOnce, first0 = static_cast<int64_t>(blockIdx.x) * kAtOnce;
   Piece<T> o[P], z[P], t[P], gt[P], gy[P];
-  const auto read = [&](int64_t first) {        // groups behind the last row read it
+  const auto read = [&](int64_t first) {
     const int row = static_cast<int>(first + group < p.rows ? first + group : p.rows - 1);
-    load_row<T, IN16, L, P>(p.block, row, p, lane, o);
-    load_row<T, IN16, L, P>(p.gate, row, p, lane, z);
-    load_row<T, IN16, L, P>(p.d_out, row, p, lane, gt);
-    load_row<T, IN16, L, P>(p.out, row, p, lane, t);
-    load_row<T, IN16, L, P>(p.d_normed, row, p, lane, gy);
+    const int width = width_of<L>(first + group, p);
+    load_row<T, IN16, L, P>(p.block, row, p, lane, width, o);
+    load_row<T, IN16, L, P>(p.gate, row, p, lane, width, z);
+    load_row<T, IN16, L, P>(p.d_out, row, p, lane, width, gt);
+    load_row<T, IN16, L, P>(p.out, row, p, lane, width, t);
+    load_row<T, IN16, L, P>(p.d_normed, row, p, lane, width, gy);
   };
   if (first0 < p.rows) read(first0);
   for (int64_t first = first0; first < p.rows; first += step) {
@@ -293,17 +311,17 @@ __global__ void __launch_bounds__(threads_of(L)) k_norm_backward(NormArgs p) {
         if (p.pre) {
           const float b = t[j][i], dy = gy[j][i];
           g += r2 * (w2[j][i] * dy - b * back);
-          d2[j][i] = fmaf(real ? dy : 0.0f, b * r2, d2[j][i]);
+          d2[j][i] = added<L>(real, dy, b * r2, d2[j][i]);
         }
         all[i] = g;
         const float u = o[j][i] * r1, n = u * w1[j][i];
         float slope = 0.0f, act = 1.0f;
         if (p.gate.p != nullptr) act = activated(z[j][i], p.silu, slope);
-        ds[j][i] = fmaf(real ? g : 0.0f, n * act, ds[j][i]);
+        ds[j][i] = added<L>(real, g, n * act, ds[j][i]);
         const float q = g * sc[j][i];
         dz[i] = q * n * slope;
         const float k = q * act;
-        d1[j][i] = fmaf(real ? k : 0.0f, u, d1[j][i]);
+        d1[j][i] = added<L>(real, k, u, d1[j][i]);
         m[j][i] = k * w1[j][i];
         sum[0] = fmaf(o[j][i], m[j][i], sum[0]);
       }

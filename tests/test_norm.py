@@ -471,3 +471,47 @@ def test_refusals_that_need_a_device(monkeypatch):
     monkeypatch.setattr(LN, "_current_device", lambda: 1)
     refused(forward, "current")
     refused(backward, "current")
+
+
+@pytest.mark.gpu
+def test_what_a_group_without_a_row_works_out_is_not_added():
+    """5 tokens of 64 leave 11 of a workgroup's 16 groups without a row.  An infinite gate in the last token makes its
+    column's sums infinite, as the formula does, and leaves the other columns as they are with a finite gate."""
+    import torch
+    c = Case(5, 64, "f32", pre=False)
+    d = c.rows(c.g.standard_normal((5, 64)))
+    sums = []
+    for last in (1.0, float("inf")):
+        c.gate[4, 7] = last
+        out, db, dg = c.rows(), c.rows(), c.rows()
+        w = [torch.empty(64, device="cuda") for _ in range(2)]
+        c.op.backward(c.block, out, d, db, None, c.gate, dg, None, c.w1, w[0], c.sc, w[1])
+        sums.append(w)
+    torch.cuda.synchronize()
+    rest = torch.arange(64, device="cuda") != 7
+    for a, b in zip(*sums):
+        assert torch.isfinite(a).all() and torch.isinf(b[7]) and torch.equal(a[rest], b[rest])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width,tokens", [(16, 65), (32, 257), (128, 17), (512, 5), (1000, 3)])
+def test_gradients_beyond_binary16_in_the_buffers_of_inputs(width, tokens):
+    """The last token's gradient of block is infinite in binary16 and overwrites block, whose values other groups of
+    the workgroup must not see: the weights' gradients are finite and those of outputs in buffers of their own."""
+    import torch
+    c = Case(tokens, width, "f16")
+    c.block[-1] = (c.block[-1].sign() + 0.5) * 2.0 ** -14          # its reciprocal root is 1000 and more
+    dt, dy = (c.rows(c.g.standard_normal((tokens, width))) for _ in range(2))
+    dt[-1] = 6e4
+    out = c.rows(2.0 * c.g.standard_normal((tokens, width)))
+    w = [torch.empty(width, device="cuda") for _ in range(6)]
+    db, dg, dr = c.rows(), c.rows(), c.rows()
+    c.op.backward(c.block, out, dt, db, dy, c.gate, dg, dr, c.w1, w[0], c.sc, w[1], c.w2, w[2])
+    torch.cuda.synchronize()
+    assert torch.isinf(db[-1]).any() and all(torch.isfinite(t).all() for t in w[:3])
+    for _ in range(5):
+        b, g, d, t = c.block.clone(), c.gate.clone(), dt.clone(), out.clone()
+        c.op.backward(b, t, d, b, dy, g, g, d, c.w1, w[3], c.sc, w[4], c.w2, w[5])
+        torch.cuda.synchronize()
+        for p, q in ((b, db), (g, dg), (d, dr), *zip(w[:3], w[3:])):
+            assert torch.equal(p, q)
