@@ -91,15 +91,16 @@ __device__ __forceinline__ float moved(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false));
 }
 
-// Sums over the L lanes of a row, the same bits in each of them.
+// Sums over the L lanes of a row, the same bits in each of them: at every step both of two lanes add what the other
+// one has, and lanes whose sums are of the same values have the same bits of them.
 template <int L, int N>
 __device__ __forceinline__ void row_sums(float (&x)[N], float (*lds)[N]) {
   for (int n = 0; n < N; ++n) {
     x[n] += moved<0xB1>(x[n]);          // quad_perm: neighbours, then pairs
     x[n] += moved<0x4E>(x[n]);
     if (L >= 16) {
-      x[n] += moved<0x124>(x[n]);       // row_ror: 4, then 8
-      x[n] += moved<0x128>(x[n]);
+      x[n] += moved<0x141>(x[n]);       // row_half_mirror: the other four of eight, row_mirror: the other eight of sixteen
+      x[n] += moved<0x140>(x[n]);
     }
     if (L >= 64) {
       x[n] += __shfl_xor(x[n], 16);

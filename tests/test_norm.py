@@ -515,3 +515,18 @@ def test_gradients_beyond_binary16_in_the_buffers_of_inputs(width, tokens):
         torch.cuda.synchronize()
         for p, q in ((b, db), (g, dg), (d, dr), *zip(w[:3], w[3:])):
             assert torch.equal(p, q)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [16, 64, 256, 512, 4096])
+def test_equal_values_of_a_row_have_equal_results(width):
+    """Whatever lane holds them: every lane scales by the same reciprocal root."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(width)
+    x = torch.randn(500, width, generator=g, device="cuda")
+    x[:, ::4] = 1.5                     # a lane's first value of its four
+    out, normed = torch.empty_like(x), torch.empty_like(x)
+    NM.BlockNorm(width, eps=EPS).forward(x, out, normed)
+    torch.cuda.synchronize()
+    for t in (out, normed):
+        assert torch.equal(t[:, ::4], t[:, :1].expand(500, width // 4))
