@@ -583,3 +583,27 @@ def test_refusals_that_need_a_device(monkeypatch):
     monkeypatch.setattr(LN, "_current_device", lambda: 1)
     for call in calls:
         refused(call, "current")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rate", [0.0027, 0.0054, 0.0108, 0.0216])
+def test_retentions_are_good_to_their_last_place(rate):
+    """One step from a state of 1 with nothing coming in leaves the retention itself.  An open gate and decays of 16 and more,
+    whose softplus is the decay in binary32, make its logarithm z = -rate log2(e) decay, in binary32 products.
+    1 - a is then good to a step, 2^-24, of 2^z, or, up to |z| = 1/2, where it is -z times a polynomial s, to 1.5e-7 of itself: 1.4e-8
+    of the polynomial, half a step of its last sum (2^-25 of 0.58 and more, 5.1e-8), of the product (2^-24), of its first coefficient (1.5e-8)
+    and, halved and more, of the sums before (1e-8).  a is good to half a step, 2^-25, more."""
+    import torch
+    width = 4096
+    decay = np.linspace(16.0, 32.0, width, endpoint=False).astype(np.float32)
+    z = (np.float32(-rate) * np.float32(1.4426950408889634)) * decay
+    assert z.dtype == np.float32 and z.min() >= -1.0
+    rec = RC.GatedRecurrence(width, torch.float32, rate)
+    x, ga = torch.zeros(1, width, device="cuda"), torch.full((1, width), float("inf"), device="cuda")
+    state, y = torch.ones(1, width, device="cuda"), torch.empty(1, width, device="cuda")
+    rec.step(torch.zeros(1, dtype=torch.int32, device="cuda"), x, ga, x, torch.from_numpy(decay).cuda(), state, y)
+    torch.cuda.synchronize()
+    z = z.astype(np.float64)
+    error = np.abs(state[0].double().cpu().numpy() - np.exp2(z))
+    room = np.where(z > -0.5, 1.5e-7 * -np.expm1(z * np.log(2.0)), 2.0 ** -24) + 2.0 ** -25
+    assert np.all(error <= room), float((error / room).max())
