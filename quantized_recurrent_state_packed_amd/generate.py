@@ -277,7 +277,7 @@ class DraftGenerator:
         kept = tokens.view(-1)[source]
         for m, states, ws in zip((self.target, self.draft), self.states, self.workspaces):
             m.prefill(kept, cu, self.slots, states, resume=self.resume, workspace=ws)
-        return accepted, out
+        return accepted.clone(), out.clone()          # the next round overwrites these
 
     def run(self, prompts, steps: int, seed: int = 0):
         """At least `steps` tokens a request, cut to `steps`: [batch][steps]; and the share of drafts accepted."""

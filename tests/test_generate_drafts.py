@@ -227,3 +227,20 @@ def test_a_training_step_of_two_blocks():
     for a, b in pairs:
         a = a.double().cpu()
         assert float((a - b).norm()) <= 2e-4 * float(b.norm())
+
+
+@pytest.mark.gpu
+def test_a_rounds_results_stay_behind_the_next_one():
+    import torch
+    target, draft = models(2)
+    gen = G.DraftGenerator(target, draft, 4, 3)
+    u = torch.from_numpy(np.random.default_rng(6).random((3, 4, 7)).astype(np.float32)).cuda()
+    last, results, copies = gen.prefill(prompts(2)), [], []
+    for r in range(3):
+        accepted, out = gen.round(last, u[r])
+        results.append((accepted, out))
+        copies.append((accepted.clone(), out.clone()))
+        last = out.gather(1, accepted.long()[:, None])[:, 0].long()
+    torch.cuda.synchronize()
+    for kept, copy in zip(results, copies):
+        assert all(torch.equal(a, b) for a, b in zip(kept, copy))
