@@ -19,8 +19,10 @@
  * HIP device that is current, on which every buffer has to lie (not checked here; the
  * Python bindings do).  Buffers are aligned as their elements, workspaces and what a
  * forward pass saves to 16 bytes.  A *_stride is the distance of two tokens in elements,
- * at least a token's width, so slices of one fused projection need no copy; outputs must
- * not overlap inputs or each other unless said otherwise.  Two calls that use one workspace
+ * at least a token's width, so slices of one fused projection need no copy, and at most 2^24
+ * (stepq_scan_*, whose kernels reach a piece's rows by offsets of 32 bits), 2^40 (stepq_norm_*) or 2^38
+ * (stepq_verify_drafts); others are STEPQ_ERR_INVALID_ARG.  Outputs must not overlap inputs or
+ * each other unless said otherwise.  Two calls that use one workspace
  * must be ordered; its contents need no initialisation and mean nothing afterwards.
  */
 #ifndef STEPQ_BLOCK_H

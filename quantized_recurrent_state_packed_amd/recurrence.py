@@ -15,6 +15,7 @@ from .stepq import STEPQ_ERR_UNSUPPORTED, StepqError
 
 EXPORTED = ("stepq_scan_workspace_bytes", "stepq_scan_saved_bytes", "stepq_scan_forward", "stepq_scan_backward",
             "stepq_scan_step")
+MAX_STRIDE = 1 << 24      # elements from token to token
 
 
 class stepq_scan_desc(ctypes.Structure):
@@ -99,6 +100,8 @@ class GatedRecurrence:
             n = self.width
         if (e != 1 and self.width > 1) or n < self.width:
             _refuse(where, f"{name}'s channels must lie side by side and its tokens must not overlap (strides {list(t.stride())})")
+        if n > MAX_STRIDE:
+            _refuse(where, f"{name}'s tokens may lie at most {MAX_STRIDE} elements apart (got {n})")
         return n
 
     def _place(self, index: int):

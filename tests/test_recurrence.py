@@ -607,3 +607,30 @@ def test_retentions_are_good_to_their_last_place(rate):
     error = np.abs(state[0].double().cpu().numpy() - np.exp2(z))
     room = np.where(z > -0.5, 1.5e-7 * -np.expm1(z * np.log(2.0)), 2.0 ** -24) + 2.0 ** -25
     assert np.all(error <= room), float((error / room).max())
+
+
+def test_the_header_says_how_far_apart_tokens_may_lie(lib):
+    text = HEADER.read_text()
+    convention = text[text.index("A *_stride"):text.index("Outputs must not overlap")]
+    assert "at most 2^24" in convention and RC.MAX_STRIDE == 2 ** 24 and "2^40" in convention and "2^38" in convention
+    for status in (forward_status, backward_status):
+        for name in ("xs", "gas", "gxs"):
+            assert status(lib, **{name: RC.MAX_STRIDE + 1}) == S.STEPQ_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_tokens_too_far_apart_are_refused_with_the_reason():
+    import torch
+    c = Case([2], 8, "bf16", lead=0, tail=0)
+    for stride, good in ((RC.MAX_STRIDE, True), (RC.MAX_STRIDE + 1, False)):
+        far = torch.zeros(stride + 8, dtype=torch.bfloat16, device="cuda").as_strided((2, 8), (stride, 1))
+        calls = (lambda: c.rec.prefill(c.cu, far, c.ga, c.gx, c.decay, c.ids, c.state, c.y),
+                 lambda: c.rec.step(torch.arange(2, dtype=torch.int32, device="cuda"), far, c.ga, c.gx, c.decay, c.state, c.y))
+        for call in calls:
+            if good:
+                call()
+                continue
+            with pytest.raises(S.StepqError, match="x's tokens may lie at most 16777216 elements apart") as e:
+                call()
+            assert e.value.status == S.STEPQ_ERR_INVALID_ARG
+    torch.cuda.synchronize()
