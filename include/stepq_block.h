@@ -133,8 +133,8 @@ typedef struct {
  * scale are float [width], shared by the heads.  gate, residual, post_weight, scale and
  * pre_weight may be NULL; out may be NULL where pre is 1.  out and normed may each be the
  * buffer of block, gate or residual, at the same stride (not of each other).
- * tokens * heads is below 2^31.  A value that is not finite spoils its row alone; a row whose mean
- * square is beyond binary32's range is normalised to 0. */
+ * tokens * heads is below 2^31.  A value that is not finite spoils its row alone; a row whose sum of
+ * squares is beyond binary32's range is normalised to 0. */
 stepq_status stepq_norm_forward(const stepq_norm_desc *desc, int64_t tokens, const void *block, int64_t block_stride,
                                 const void *gate, int64_t gate_stride, const void *residual,
                                 int64_t residual_stride, const float *post_weight, const float *scale,

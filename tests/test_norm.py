@@ -530,3 +530,21 @@ def test_equal_values_of_a_row_have_equal_results(width):
     torch.cuda.synchronize()
     for t in (out, normed):
         assert torch.equal(t[:, ::4], t[:, :1].expand(500, width // 4))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [4, 64, 256, 1000, 4096, 16384])
+def test_rows_whose_sum_of_squares_binary32_does_not_hold(width):
+    """Rows of values whose squares add up to 2^126 and to 2^130: the former are normalised, the latter are 0, also
+    where their mean is in range."""
+    import torch
+    x = torch.ones(8, width, device="cuda")
+    x[::2] *= (2.0 ** 126 / width) ** 0.5
+    x[1::2] *= (2.0 ** 130 / width) ** 0.5
+    out, normed = torch.empty_like(x), torch.empty_like(x)
+    NM.BlockNorm(width, pre=False, eps=EPS).forward(x, out)
+    NM.BlockNorm(width, post=False, eps=EPS).forward(x, None, normed)
+    torch.cuda.synchronize()
+    for t in (out, normed):
+        # sums of equal squares, a reciprocal root (one step) and a product
+        assert float((t[::2] - 1.0).abs().max()) <= 40 * 2.0 ** -24 and float(t[1::2].abs().max()) == 0.0
