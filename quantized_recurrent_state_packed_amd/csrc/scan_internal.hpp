@@ -69,7 +69,7 @@ inline int64_t scan_pieces(int64_t total_tokens, int64_t batch, int piece) { ret
 
 // Tokens of a piece.  A forward pass of fewer workgroups than fill the chip takes smaller pieces, of more waves that have fewer
 // tokens each to go through.  us of bfloat16 calls, 128 tokens a piece (32 of 4 waves) against 64 (8 of 8), by workgroups
-// of the former: 37 tokens x 4096 (32) 8.2 : 5.2;  200 x 4096 (64) 12.5 : 10.4;  20000 x 128 (157) 26.2 : 23.8;  700 x 4096 (192)
+// of the former, counted with 128 channels each (binary32 and odd rows have 64 in one, and twice as many): 37 tokens x 4096 (32) 8.2 : 5.2;  200 x 4096 (64) 12.5 : 10.4;  20000 x 128 (157) 26.2 : 23.8;  700 x 4096 (192)
 // 15.6 : 16.8;  1400 x 4096 (352) 23.7 : 24.8;  2800 x 4096 (704) 36.6 : 38.0;  5 prompts of 3001 x 1001 binary32 (224) 20 : 24.5.
 constexpr int64_t kFewGroups = 160;
 inline int scan_piece(const stepq_scan_desc& d, int64_t total_tokens, int64_t batch, bool backward) {

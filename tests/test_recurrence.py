@@ -19,7 +19,7 @@ from quantized_recurrent_state_packed_amd import stepq as S
 HEADER = Path(__file__).resolve().parents[1] / "include" / "stepq_block.h"
 GOOD = 4096          # an address that is never dereferenced
 RATE = 8.0
-PIECE = 128          # tokens of a workgroup of the forward pass, twice those of the backward pass
+PIECE = 128          # tokens of a workgroup of a large forward pass, twice those of a small one and of the backward pass
 
 
 @pytest.fixture(scope="module")
