@@ -657,7 +657,7 @@ hipError_t step(const ScanArgs& a, hipStream_t s) {
   const int channels = two ? 512 : 256;
   const int64_t groups = (a.width + channels - 1) / channels;
   // us of 1, 2, 4 and 8 requests a workgroup, by workgroups of the former (bfloat16, 6144 channels): 768 3.6, 3.6, 4.2, 5.9;  1536 4.4,
-  // 4.3, 4.9, 6.2;  3072 6.8, 6.0, 6.1, 7.2;  6144 11.9, 10.3, 9.7, 11.4;  12288 21.1, 18.6, 18.0, 18.0.  Of 1001 channels one by one:
+  // 4.3, 4.9, 6.2;  4080 7.8, 7.0, 6.7, 7.9;  6144 11.9, 10.3, 9.7, 11.4;  12288 21.1, 18.6, 18.0, 18.0.  Of 1001 channels one by one:
   // 2048 4.4, 4.2, 4.4, 5.5;  8192 10.3, 8.3, 7.4, 8.0
   const int rows = groups * a.batch >= 4096 ? 4 : 1;
   const dim3 grid(static_cast<uint32_t>((a.batch + rows - 1) / rows * groups));
